@@ -219,6 +219,68 @@ loopvq_status loopvq_merge2(const float *out_a, const float *lse_a, const float 
                             const float *lse_b, int rows, int D, float *out, float *lse,
                             void *stream);
 
+/* Workspace bytes loopvq_bf16_decode_attn_scored needs for up to max_len tokens per sequence. */
+size_t loopvq_bf16_scored_workspace_bytes(const loopvq_bf16_cache *cache, int max_len);
+
+/*
+ * loopvq_bf16_decode_attn that also accumulates every token's attention
+ * weight, the measure by which loopvq_bf16_evict chooses.  (No page of the
+ * paper: an operator of this library for caches held in bf16.)  For
+ * start_b <= n < len_b:
+ *   score_out[b][h][n] = score_in[b][h][n] + sum over the query heads g of
+ *                        KV head h of exp(s_gn - lse_g).
+ * With another part of the same softmax (attention over tokens that are not in
+ * this cache, such as a shared prefix: loopvq_bf16_shared_attn, loopvq_shared_attn)
+ * out and lse are the merged ones, as by loopvq_merge2, and the weights are
+ * those of the joint softmax.
+ *
+ * other_out  fp32 [B][Hq][D] and other_lse fp32 [B][Hq]: the other part, or
+ *            both NULL; a row with other_lse = -inf has no other tokens.  out may
+ *            be other_out; lse may not overlap other_lse.
+ * score_in   fp32 [B][Hkv][Nmax], or NULL for zeros.
+ * score_out  fp32 [B][Hkv][Nmax]: score_in itself, or memory apart from it;
+ *            elements of other tokens stay as they are.
+ * The other arguments are those of loopvq_bf16_decode_attn; workspace of at
+ * least loopvq_bf16_scored_workspace_bytes(cache, max_len) bytes, ordered like
+ * any workspace.  Sums run in a fixed order: equal inputs give equal bits.
+ */
+loopvq_status loopvq_bf16_decode_attn_scored(const loopvq_bf16_cache *cache, const uint16_t *q,
+                                             const int32_t *starts, const int32_t *lens, int max_len, float scale,
+                                             const float *other_out, const float *other_lse, const float *score_in,
+                                             float *score_out, float *out, float *lse, void *workspace,
+                                             size_t ws_bytes, void *stream);
+
+/* Workspace bytes loopvq_bf16_evict needs. */
+size_t loopvq_bf16_evict_workspace_bytes(const loopvq_bf16_cache *cache, int max_len, int budget);
+
+/*
+ * Evict tokens of a bf16 cache by their scores.  (An operator of this library;
+ * no page of the paper.)  Every (sequence b, KV head h) with len_b > budget
+ * keeps `budget` of its slots n < len_b: first the protected ones, whose
+ * position is a sink (pos < n_sink) or recent (pos >= next_pos_b - n_recent),
+ * then the highest scores; equal ones (protected ones among themselves too) by
+ * the lowest slot, NaN last.  The i-th emptied slot below the budget (in
+ * ascending order) then takes the key, value, score and position of the i-th
+ * kept slot at or behind the budget; the other kept slots stay where they are.
+ * Attention over the first `budget` slots is attention over the kept tokens
+ * (keys are stored rotated, so slots need no order).
+ *
+ * cache     k and v are rewritten in the emptied slots (through the const
+ *           pointers); slots at or behind the budget stay as they are.
+ * score_in  fp32 [B][Hkv][Nmax]; pos_in int32 [B][Hkv][Nmax], the position of
+ *           each slot's token; lens_in int32 [B], clamped to [0, max_len];
+ *           next_pos int32 [B], the position of the sequence's next token.
+ * budget    >= 1, n_sink + n_recent <= budget (both >= 0).
+ * score_out, pos_out, lens_out: the arrays after the eviction: the inputs
+ *           themselves, or memory apart from them.  Written for slots
+ *           n < min(len_b, budget) = lens_out_b only.
+ * workspace of at least loopvq_bf16_evict_workspace_bytes bytes, 16-byte aligned.
+ */
+loopvq_status loopvq_bf16_evict(const loopvq_bf16_cache *cache, const float *score_in, const int32_t *pos_in,
+                                const int32_t *lens_in, const int32_t *next_pos, int max_len, int budget,
+                                int n_sink, int n_recent, float *score_out, int32_t *pos_out, int32_t *lens_out,
+                                void *workspace, size_t ws_bytes, void *stream);
+
 /*
  * TaSQ applied before loop-axis coupling (App. B): keys are mapped to
  *   u = P(w (.) k / sigma)

@@ -8,4 +8,5 @@ from .loopvq import (Cache, CacheDesc, LoopVQError, prepare, encode, decode_attn
                      decode_attn_range, Bf16Cache, Bf16CacheDesc, bf16_decode_attn, bf16_decode_workspace_bytes,
                      merge2, Window, WindowDesc, window_advance, window_append, window_workspace_bytes,
                      window_decode_attn, window_append_decode_attn, Tasq, TasqDesc, tasq_encode,
-                     tasq_decode_attn, fault_check, set_wait_limit_ns, wait_limit_ns)
+                     tasq_decode_attn, fault_check, set_wait_limit_ns, wait_limit_ns,
+                     bf16_decode_attn_scored, bf16_scored_workspace_bytes, bf16_evict, bf16_evict_workspace_bytes)

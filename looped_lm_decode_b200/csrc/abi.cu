@@ -248,6 +248,137 @@ loopvq_status loopvq_bf16_decode_attn(const loopvq_bf16_cache *c, const uint16_t
     return LOOPVQ_OK;
 }
 
+// Whether [a, a + na) and [b, b + nb) bytes share memory.
+static bool overlaps(const void *a, size_t na, const void *b, size_t nb) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return x < y + nb && y < x + na;
+}
+
+// An output that is the input itself or memory apart from it.
+static loopvq_status check_same_or_apart(const void *in, const void *out, size_t bytes, const char *name) {
+    if (in != out && overlaps(in, bytes, out, bytes))
+        return fail(LOOPVQ_ERR_INVALID_ARG, "%s overlaps its input without being it", name);
+    return LOOPVQ_OK;
+}
+
+static loopvq_status check_word_ptr(const void *p, const char *name) {
+    if (!p) return fail(LOOPVQ_ERR_INVALID_ARG, "%s is NULL", name);
+    if (reinterpret_cast<uintptr_t>(p) & 3u) return fail(LOOPVQ_ERR_INVALID_ARG, "%s not 4-byte aligned", name);
+    return LOOPVQ_OK;
+}
+
+// The other part of a joint softmax: both arrays or neither.
+static loopvq_status check_other(const float *other_out, const float *other_lse) {
+    if (!other_out != !other_lse) return fail(LOOPVQ_ERR_INVALID_ARG, "other_out and other_lse go together");
+    if (!other_out) return LOOPVQ_OK;
+    LQ_TRY(check_ptr(other_out, "other_out"));
+    return check_word_ptr(other_lse, "other_lse");
+}
+
+size_t loopvq_bf16_scored_workspace_bytes(const loopvq_bf16_cache *c, int max_len) {
+    if (check_bf16(c) != LOOPVQ_OK || max_len < 0 || max_len > c->Nmax) return 0;
+    return loopvq::bf16_scored_ws_bytes(*c, max_len);
+}
+
+loopvq_status loopvq_bf16_decode_attn_scored(const loopvq_bf16_cache *c, const uint16_t *q, const int32_t *starts,
+                                             const int32_t *lens, int max_len, float scale, const float *other_out,
+                                             const float *other_lse, const float *score_in, float *score_out,
+                                             float *out, float *lse, void *workspace, size_t ws_bytes, void *stream) {
+    g_err[0] = 0;
+    LQ_TRY(check_bf16(c));
+    LQ_TRY(check_ptr(q, "q"));
+    LQ_TRY(check_word_ptr(lens, "lens"));
+    LQ_TRY(check_ptr(out, "out"));
+    LQ_TRY(check_other(other_out, other_lse));
+    LQ_TRY(check_word_ptr(score_out, "score_out"));
+    if (score_in) LQ_TRY(check_word_ptr(score_in, "score_in"));
+    if (starts) LQ_TRY(check_word_ptr(starts, "starts"));
+    if (lse) LQ_TRY(check_word_ptr(lse, "lse"));
+    if (max_len < 0 || max_len > c->Nmax)
+        return fail(LOOPVQ_ERR_INVALID_ARG, "max_len=%d out of [0, Nmax=%d]", max_len, c->Nmax);
+    if (!std::isfinite(scale)) return fail(LOOPVQ_ERR_INVALID_ARG, "scale is not finite");
+    if (scale <= 0.f) scale = 1.0f / std::sqrt((float)c->D);
+    if (c->B > 65535 || c->Hkv > 65535) return fail(LOOPVQ_ERR_UNSUPPORTED, "B or Hkv exceeds 65535");
+    const size_t rows = (size_t)c->B * c->Hq;
+    if (other_out)
+        LQ_TRY(check_same_or_apart(other_out, out, rows * c->D * sizeof(float), "out"));
+    if (lse && other_lse && overlaps(lse, rows * sizeof(float), other_lse, rows * sizeof(float)))
+        return fail(LOOPVQ_ERR_INVALID_ARG, "lse overlaps other_lse");
+    if (score_in)
+        LQ_TRY(check_same_or_apart(score_in, score_out, (size_t)c->B * c->Hkv * c->Nmax * sizeof(float), "score_out"));
+    const loopvq::DecodePlan plan = loopvq::plan_bf16(*c, max_len);
+    if (plan.nsplit > 65535) return fail(LOOPVQ_ERR_UNSUPPORTED, "too many splits");
+    const size_t need = loopvq::bf16_scored_ws_bytes(*c, max_len);
+    if (!workspace || ws_bytes < need)
+        return fail(LOOPVQ_ERR_WORKSPACE, "workspace of %zu bytes needed, %zu given", need,
+                    workspace ? ws_bytes : (size_t)0);
+    if (!aligned16(workspace)) return fail(LOOPVQ_ERR_INVALID_ARG, "workspace is not 16-byte aligned");
+    const loopvq::Bf16Scored sc{other_out, other_lse, score_in, score_out};
+    cudaError_t e = loopvq::launch_bf16_decode(*c, plan, q, starts, lens, max_len, scale, out, lse, workspace,
+                                               (cudaStream_t)stream, &sc);
+    if (e != cudaSuccess) return cuda_fail(e, "loopvq_bf16_decode_attn_scored");
+    return LOOPVQ_OK;
+}
+
+size_t loopvq_bf16_evict_workspace_bytes(const loopvq_bf16_cache *c, int max_len, int budget) {
+    if (check_bf16(c) != LOOPVQ_OK || max_len < 0 || max_len > c->Nmax || budget < 1) return 0;
+    return loopvq::evict_ws_bytes(c->B, c->Hkv, max_len, budget);
+}
+
+loopvq_status loopvq_bf16_evict(const loopvq_bf16_cache *c, const float *score_in, const int32_t *pos_in,
+                                const int32_t *lens_in, const int32_t *next_pos, int max_len, int budget, int n_sink,
+                                int n_recent, float *score_out, int32_t *pos_out, int32_t *lens_out, void *workspace,
+                                size_t ws_bytes, void *stream) {
+    g_err[0] = 0;
+    LQ_TRY(check_bf16(c));
+    LQ_TRY(check_word_ptr(score_in, "score_in"));
+    LQ_TRY(check_word_ptr(pos_in, "pos_in"));
+    LQ_TRY(check_word_ptr(lens_in, "lens_in"));
+    LQ_TRY(check_word_ptr(next_pos, "next_pos"));
+    LQ_TRY(check_word_ptr(score_out, "score_out"));
+    LQ_TRY(check_word_ptr(pos_out, "pos_out"));
+    LQ_TRY(check_word_ptr(lens_out, "lens_out"));
+    if (max_len < 0 || max_len > c->Nmax)
+        return fail(LOOPVQ_ERR_INVALID_ARG, "max_len=%d out of [0, Nmax=%d]", max_len, c->Nmax);
+    if (budget < 1) return fail(LOOPVQ_ERR_INVALID_ARG, "budget=%d must be positive", budget);
+    if (n_sink < 0 || n_recent < 0 || (int64_t)n_sink + n_recent > budget)
+        return fail(LOOPVQ_ERR_INVALID_ARG, "n_sink=%d and n_recent=%d must fit into the budget of %d", n_sink, n_recent,
+                    budget);
+    if ((int64_t)c->B * c->Hkv > 65535)
+        return fail(LOOPVQ_ERR_UNSUPPORTED, "B * Hkv = %lld exceeds 65535", (long long)c->B * c->Hkv);
+    const size_t words = (size_t)c->B * c->Hkv * c->Nmax * 4;
+    LQ_TRY(check_same_or_apart(score_in, score_out, words, "score_out"));
+    LQ_TRY(check_same_or_apart(pos_in, pos_out, words, "pos_out"));
+    LQ_TRY(check_same_or_apart(lens_in, lens_out, (size_t)c->B * 4, "lens_out"));
+    const size_t need = loopvq::evict_ws_bytes(c->B, c->Hkv, max_len, budget);
+    if (!workspace || ws_bytes < need)
+        return fail(LOOPVQ_ERR_WORKSPACE, "workspace of %zu bytes needed, %zu given", need,
+                    workspace ? ws_bytes : (size_t)0);
+    if (!aligned16(workspace)) return fail(LOOPVQ_ERR_INVALID_ARG, "workspace is not 16-byte aligned");
+    loopvq::EvictArgs a{};
+    a.k = const_cast<uint16_t *>(c->k);
+    a.v = const_cast<uint16_t *>(c->v);
+    a.score_in = score_in;
+    a.pos_in = pos_in;
+    a.lens_in = lens_in;
+    a.next_pos = next_pos;
+    a.score_out = score_out;
+    a.pos_out = pos_out;
+    a.lens_out = lens_out;
+    a.ws = reinterpret_cast<int32_t *>(workspace);
+    a.B = c->B;
+    a.Hkv = c->Hkv;
+    a.Nmax = c->Nmax;
+    a.D = c->D;
+    a.max_len = max_len;
+    a.budget = budget;
+    a.n_sink = n_sink;
+    a.n_recent = n_recent;
+    cudaError_t e = loopvq::launch_evict(a, (cudaStream_t)stream);
+    if (e != cudaSuccess) return cuda_fail(e, "loopvq_bf16_evict");
+    return LOOPVQ_OK;
+}
+
 loopvq_status loopvq_merge2(const float *out_a, const float *lse_a, const float *out_b, const float *lse_b,
                             int rows, int D, float *out, float *lse, void *stream) {
     g_err[0] = 0;

@@ -30,6 +30,13 @@ struct Bf16Args {
     float2 *ws_ml;           // [B][Hq][nsplit]
     int B, Hkv, Hq, Nmax, max_len, split_len, nsplit;
     float qscale;            // scale * log2(e)
+    // the scored form only
+    float *ws_s;             // [B][Hq][sstride] scores in log2 units
+    int sstride;             // max_len rounded up to 4
+    const float *other_out;  // [B][Hq][D] attention over other tokens, or null
+    const float *other_lse;  // [B][Hq]
+    const float *score_in;   // [B][Hkv][Nmax], or null for zeros
+    float *score_out;        // [B][Hkv][Nmax]
 };
 
 // 16-byte copy that reads src_bytes (16 or 0) and zero-fills the rest
@@ -45,7 +52,9 @@ __device__ __forceinline__ void unpack8(const uint4 &w, float2 (&x)[4]) {
     x[3] = unpack2(w.w);
 }
 
-template <int D, int QPK, int WARPS, int MINB, int DEPTH>
+// SCORED: also writes every attended token's score (log2 units), 4 bytes per token and query head beside the
+// 4 D bytes of cache that a token and KV head is read from.
+template <int D, int QPK, int WARPS, int MINB, int DEPTH, bool SCORED = false>
 __global__ void __launch_bounds__(WARPS * 32, MINB) bf16_split_kernel(const Bf16Args a) {
     constexpr int NL = D / 8;                              // lanes per token slot
     constexpr int SPW = 32 / NL;
@@ -83,7 +92,7 @@ __global__ void __launch_bounds__(WARPS * 32, MINB) bf16_split_kernel(const Bf16
 #pragma unroll
         for (int j = 0; j < TT; ++j) {
             const int n = p + j;
-            const bool ok = n < tok_end;
+            const bool ok = n < tok_end && n >= st;        // a masked token's values may be anything: not read
             const size_t off = (size_t)(ok ? n : tok_begin) * D;
             const uint32_t dst = ring + (uint32_t)stg * QB + (uint32_t)(j * NT) * 16u;
             cp_async16_zfill(dst, kb + off, ok ? 16u : 0u);
@@ -156,6 +165,10 @@ __global__ void __launch_bounds__(WARPS * 32, MINB) bf16_split_kernel(const Bf16
             const float keep = reduce_scatter<TT, NL>(ps[hq], ls, slot_mask);
             const int n = p0 + tk;
             const float s = (n < tok_end && n >= st) ? keep : -CUDART_INF_F;
+            if constexpr (SCORED) {
+                if (tile_owner<TT, NL>(tk) == ls && n < tok_end && n >= st)
+                    a.ws_s[((size_t)b * a.Hq + h * QPK + hq) * a.sstride + n] = s;
+            }
             if (__any_sync(slot_mask, s > m_[hq] + 8.f)) {
                 float tmax = s;
 #pragma unroll
@@ -278,6 +291,86 @@ __global__ void __launch_bounds__(D) bf16_merge_kernel(const Bf16Args a, float *
     if (lse != nullptr && d == 0) lse[bh] = any ? (mx + log2f(lsum)) * 0.69314718055994530942f : -CUDART_INF_F;
 }
 
+// Merge of the scored form: the splits' partials and, if given, another part (out, lse) over other tokens; then
+// every token's weight exp(s - lse), summed over the query heads of its KV head, is added to its score.  One CTA
+// per (chunk of tokens, KV head, sequence); the CTA behind the last chunk writes out and lse.  The weights need
+// the joint log-sum-exp, which exists only once every split is done: hence scores are kept (4 bytes each, read
+// back from L2) rather than keys read twice (2 D bytes).  Every score element has one writer, and sums run in a
+// fixed order, so results do not depend on the order of execution.
+constexpr int kScoreThreads = 256;
+constexpr int kScoreChunk = 2048;                          // tokens per CTA
+
+template <int D, int QPK>
+__global__ void __launch_bounds__(kScoreThreads) bf16_scored_merge_kernel(const Bf16Args a, float *out, float *lse) {
+    const int h = blockIdx.y, b = blockIdx.z, tid = threadIdx.x;
+    const int len = min(max(__ldg(a.lens + b), 0), a.max_len);
+    const int st = a.starts ? min(max(__ldg(a.starts + b), 0), len) : 0;
+    const bool last = blockIdx.x == gridDim.x - 1;         // writes out and lse
+    const int n0 = (int)blockIdx.x * kScoreChunk;
+    if (!last && (n0 >= len || n0 + kScoreChunk <= st)) return;
+    const int ns = len > st ? (len - (st & ~3) + a.split_len - 1) / a.split_len : 0;
+
+    // log-sum-exps of the query heads: one warp per head, in log2 units
+    __shared__ float s_mx[QPK], s_l2[QPK];                 // own maximum; joint log2-sum-exp2
+    __shared__ float s_scale[QPK], s_other[QPK];           // factors of the own sum and of the other part
+    for (int g = tid >> 5; g < QPK; g += kScoreThreads / 32) {
+        const size_t bh = (size_t)b * a.Hq + h * QPK + g;
+        const float2 *ml = a.ws_ml + bh * a.nsplit;
+        float mx = -CUDART_INF_F, sum = 0.f;
+        for (int sp = tid & 31; sp < ns; sp += 32) mx = fmaxf(mx, ml[sp].x);
+#pragma unroll
+        for (int o = 16; o >= 1; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+        if (mx != -CUDART_INF_F)
+            for (int sp = tid & 31; sp < ns; sp += 32) sum += ml[sp].y * ex2(ml[sp].x - mx);
+#pragma unroll
+        for (int o = 16; o >= 1; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        if ((tid & 31) == 0) {
+            const float own = sum > 0.f ? mx + log2f(sum) : -CUDART_INF_F;
+            const float oth = a.other_lse ? a.other_lse[bh] * 1.44269504088896340736f : -CUDART_INF_F;
+            const float top = fmaxf(own, oth);
+            float l2 = -CUDART_INF_F, ws = 0.f, wo = 0.f;
+            if (top != -CUDART_INF_F) {
+                const float ea = ex2(own - top), eb = ex2(oth - top);
+                l2 = top + log2f(ea + eb);
+                ws = sum > 0.f ? ea / (sum * (ea + eb)) : 0.f;
+                wo = eb / (ea + eb);
+            }
+            s_mx[g] = mx;
+            s_l2[g] = l2;
+            s_scale[g] = ws;
+            s_other[g] = wo;
+        }
+    }
+    __syncthreads();
+
+    if (last) {
+        for (int it = tid; it < QPK * D; it += kScoreThreads) {
+            const int g = it / D, d = it % D;
+            const size_t bh = (size_t)b * a.Hq + h * QPK + g;
+            const float2 *ml = a.ws_ml + bh * a.nsplit;
+            const float *o = a.ws_o + bh * a.nsplit * D + d;
+            float acc = 0.f;
+            for (int sp = 0; sp < ns; ++sp)
+                if (s_mx[g] != -CUDART_INF_F) acc += o[(size_t)sp * D] * ex2(ml[sp].x - s_mx[g]);
+            float r = acc * s_scale[g];
+            if (s_other[g] > 0.f) r += s_other[g] * a.other_out[bh * D + d];
+            out[bh * D + d] = r;
+            if (lse != nullptr && d == 0)
+                lse[bh] = s_l2[g] == -CUDART_INF_F ? -CUDART_INF_F : s_l2[g] * 0.69314718055994530942f;
+        }
+        return;
+    }
+    const size_t row = ((size_t)b * a.Hkv + h) * a.Nmax;
+    const float *s0 = a.ws_s + ((size_t)b * a.Hq + h * QPK) * a.sstride;
+    const int n1 = min(n0 + kScoreChunk, len);
+    for (int n = max(n0, st) + tid; n < n1; n += kScoreThreads) {
+        float w = 0.f;
+#pragma unroll
+        for (int g = 0; g < QPK; ++g) w += ex2(s0[(size_t)g * a.sstride + n] - s_l2[g]);
+        a.score_out[row + n] = (a.score_in ? a.score_in[row + n] : 0.f) + w;
+    }
+}
+
 static constexpr int kBfWarps = 8;
 static constexpr int kBfMinBlocks = 2;
 static constexpr int kBfDepth = 3;
@@ -320,20 +413,44 @@ static cudaError_t launch_bf16_t(const Bf16Args &a, float *out, float *lse, cuda
     return cudaGetLastError();
 }
 
+template <int D, int QPK>
+static cudaError_t launch_bf16_scored_t(const Bf16Args &a, float *out, float *lse, cudaStream_t s) {
+    constexpr int NSLOT = kBfWarps * (32 / (D / 8));
+    const size_t smem = bf16_smem_bytes();
+    if ((size_t)NSLOT * QPK * (D + 4) * sizeof(float) > smem) return cudaErrorInvalidConfiguration;
+    auto kern = bf16_split_kernel<D, QPK, kBfWarps, kBfMinBlocks, kBfDepth, true>;
+    cudaError_t e = ensure_dynamic_smem((const void *)kern, smem);
+    if (e != cudaSuccess) return e;
+    if (a.nsplit > 0) {
+        kern<<<dim3(a.nsplit, a.Hkv, a.B), kBfWarps * 32, smem, s>>>(a);
+        e = cudaGetLastError();
+        if (e != cudaSuccess) return e;
+    }
+    const unsigned chunks = (unsigned)((a.max_len + kScoreChunk - 1) / kScoreChunk) + 1;
+    bf16_scored_merge_kernel<D, QPK><<<dim3(chunks, a.Hkv, a.B), kScoreThreads, 0, s>>>(a, out, lse);
+    return cudaGetLastError();
+}
+
 template <int D>
 static cudaError_t dispatch_bf16(int qpk, const Bf16Args &a, float *out, float *lse, cudaStream_t s) {
+    const bool scored = a.score_out != nullptr;
     switch (qpk) {
-        case 1: return launch_bf16_t<D, 1>(a, out, lse, s);
-        case 2: return launch_bf16_t<D, 2>(a, out, lse, s);
-        case 4: return launch_bf16_t<D, 4>(a, out, lse, s);
-        case 8: return launch_bf16_t<D, 8>(a, out, lse, s);
+        case 1: return scored ? launch_bf16_scored_t<D, 1>(a, out, lse, s) : launch_bf16_t<D, 1>(a, out, lse, s);
+        case 2: return scored ? launch_bf16_scored_t<D, 2>(a, out, lse, s) : launch_bf16_t<D, 2>(a, out, lse, s);
+        case 4: return scored ? launch_bf16_scored_t<D, 4>(a, out, lse, s) : launch_bf16_t<D, 4>(a, out, lse, s);
+        case 8: return scored ? launch_bf16_scored_t<D, 8>(a, out, lse, s) : launch_bf16_t<D, 8>(a, out, lse, s);
         default: return cudaErrorInvalidValue;
     }
 }
 
+size_t bf16_scored_ws_bytes(const loopvq_bf16_cache &c, int max_len) {
+    const size_t base = (plan_bf16(c, max_len).ws_bytes + 255) & ~(size_t)255;
+    return base + (size_t)c.B * c.Hq * (((size_t)max_len + 3) & ~(size_t)3) * sizeof(float);
+}
+
 cudaError_t launch_bf16_decode(const loopvq_bf16_cache &c, const DecodePlan &plan, const uint16_t *q,
                                const int32_t *starts, const int32_t *lens, int max_len, float scale, float *out,
-                               float *lse, void *workspace, cudaStream_t s) {
+                               float *lse, void *workspace, cudaStream_t s, const Bf16Scored *sc) {
     Bf16Args a{};
     a.k = c.k;
     a.v = c.v;
@@ -351,6 +468,15 @@ cudaError_t launch_bf16_decode(const loopvq_bf16_cache &c, const DecodePlan &pla
     a.split_len = plan.split_len;
     a.nsplit = plan.nsplit;
     a.qscale = scale * 1.44269504088896340736f;
+    if (sc != nullptr) {
+        a.ws_s = reinterpret_cast<float *>(reinterpret_cast<char *>(workspace) +
+                                           ((plan.ws_bytes + 255) & ~(size_t)255));
+        a.sstride = (max_len + 3) & ~3;
+        a.other_out = sc->other_out;
+        a.other_lse = sc->other_lse;
+        a.score_in = sc->score_in;
+        a.score_out = sc->score_out;
+    }
     const int qpk = c.Hq / c.Hkv;
     if (c.D == 128) return dispatch_bf16<128>(qpk, a, out, lse, s);
     if (c.D == 64) return dispatch_bf16<64>(qpk, a, out, lse, s);

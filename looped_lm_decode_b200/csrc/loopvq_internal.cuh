@@ -95,9 +95,31 @@ cudaError_t launch_tasq_encode_tc(const loopvq_cache &cc, const loopvq_tasq &tq,
                                   const void *xv, const int64_t *strides, int b0, int nb, int tok0, int ntok,
                                   cudaStream_t s);
 DecodePlan plan_bf16(const loopvq_bf16_cache &c, int max_len);
+// The scored form of the bf16 decode: the other part of a joint softmax (or null) and the token scores.
+struct Bf16Scored {
+    const float *other_out, *other_lse;
+    const float *score_in;   // null: zeros
+    float *score_out;
+};
 cudaError_t launch_bf16_decode(const loopvq_bf16_cache &c, const DecodePlan &plan, const uint16_t *q,
                                const int32_t *starts, const int32_t *lens, int max_len, float scale, float *out,
-                               float *lse, void *workspace, cudaStream_t s);
+                               float *lse, void *workspace, cudaStream_t s, const Bf16Scored *sc = nullptr);
+size_t bf16_scored_ws_bytes(const loopvq_bf16_cache &c, int max_len);
+// Eviction (evict.cu).  Workspace: per (sequence, KV head) a count, the emptied slots and the moved tokens' slots.
+struct EvictArgs {
+    uint16_t *k, *v;         // [B][Hkv][Nmax][D]
+    const float *score_in;   // [B][Hkv][Nmax]
+    const int32_t *pos_in;   // [B][Hkv][Nmax]
+    const int32_t *lens_in;  // [B]
+    const int32_t *next_pos; // [B]
+    float *score_out;
+    int32_t *pos_out, *lens_out;
+    int32_t *ws;             // [B * Hkv] counts, then per (b, h) holes [cap], sources [cap]
+    int B, Hkv, Nmax, D, max_len, budget, n_sink, n_recent;
+    int cap;                 // most rows that can move in a (sequence, KV head)
+};
+size_t evict_ws_bytes(int B, int Hkv, int max_len, int budget);
+cudaError_t launch_evict(const EvictArgs &a, cudaStream_t s);
 cudaError_t launch_merge2(const float *out_a, const float *lse_a, const float *out_b, const float *lse_b, int rows,
                           int D, float *out, float *lse, cudaStream_t s);
 int window_slots(const loopvq_window &w);

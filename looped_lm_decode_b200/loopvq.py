@@ -24,6 +24,8 @@ EXPORTS = ("loopvq_idx_words", "loopvq_codebook_elems", "loopvq_slice_elems", "l
            "loopvq_dequant_debug", "loopvq_last_error", "loopvq_abi_version",
            "loopvq_decode_attn_noalloc", "loopvq_noalloc_scratch_bytes", "loopvq_decode_attn_range",
            "loopvq_bf16_decode_workspace_bytes", "loopvq_bf16_decode_attn", "loopvq_merge2",
+           "loopvq_bf16_scored_workspace_bytes", "loopvq_bf16_decode_attn_scored",
+           "loopvq_bf16_evict_workspace_bytes", "loopvq_bf16_evict",
            "loopvq_window_slots", "loopvq_window_advance", "loopvq_window_append",
            "loopvq_window_workspace_bytes", "loopvq_window_decode_attn", "loopvq_window_append_decode_attn",
            "loopvq_tasq_w_elems",
@@ -96,6 +98,14 @@ def lib():
         L.loopvq_bf16_decode_attn.restype = i
         L.loopvq_merge2.argtypes = [vp, vp, vp, vp, i, i, vp, vp, vp]
         L.loopvq_merge2.restype = i
+        L.loopvq_bf16_scored_workspace_bytes.argtypes = [PB, i]
+        L.loopvq_bf16_scored_workspace_bytes.restype = sz
+        L.loopvq_bf16_decode_attn_scored.argtypes = [PB, vp, vp, vp, i, f, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+        L.loopvq_bf16_decode_attn_scored.restype = i
+        L.loopvq_bf16_evict_workspace_bytes.argtypes = [PB, i, i]
+        L.loopvq_bf16_evict_workspace_bytes.restype = sz
+        L.loopvq_bf16_evict.argtypes = [PB, vp, vp, vp, vp, i, i, i, i, vp, vp, vp, vp, sz, vp]
+        L.loopvq_bf16_evict.restype = i
         PW = C.POINTER(WindowDesc)
         L.loopvq_window_slots.argtypes = [PW]
         L.loopvq_window_slots.restype = i
@@ -321,6 +331,100 @@ def merge2(out_a, lse_a, out_b, lse_b, out=None, lse=None, stream=None):
     _check(lib().loopvq_merge2(_ptr(out_a), _ptr(lse_a), _ptr(out_b), _ptr(lse_b), rows, D, _ptr(out), _ptr(lse),
                                _stream(stream)))
     return out, lse
+
+
+def _need(t: torch.Tensor, name: str, shape, dtypes, device):
+    """Refuses an array that the kernels would read past or misread."""
+    if t.shape != tuple(shape) or t.dtype not in dtypes or not t.is_contiguous() or t.device != device:
+        raise LoopVQError(LOOPVQ_ERR_INVALID_ARG, f"{name} must be contiguous {list(shape)} of "
+                          f"{' or '.join(str(d).replace('torch.', '') for d in dtypes)} on {device}: got "
+                          f"{list(t.shape)} {t.dtype} on {t.device}")
+
+
+def _need_current(device):
+    """The launch goes to the current GPU: memory of another one, or of the host, is refused."""
+    if device.type != "cuda" or device.index != torch.cuda.current_device():
+        raise LoopVQError(LOOPVQ_ERR_INVALID_ARG, f"the cache is on {device}, which is not the current GPU")
+    return device
+
+
+_Q, _F32, _I32 = (torch.bfloat16, torch.int16), (torch.float32,), (torch.int32,)
+
+
+def _need_other(other, rows, Hq, D, device):
+    if other is None:
+        return None, None
+    _need(other[0], "other out", (rows, Hq, D), _F32, device)
+    _need(other[1], "other lse", (rows, Hq), _F32, device)
+    return other
+
+
+def bf16_scored_workspace_bytes(cache: Bf16Cache, max_len: int) -> int:
+    return lib().loopvq_bf16_scored_workspace_bytes(cache.ref(), max_len)
+
+
+def bf16_decode_attn_scored(cache: Bf16Cache, q: torch.Tensor, lens: torch.Tensor, max_len: int, score,
+                            score_out=None, starts=None, scale: float = 0.0, other=None, out=None, lse=None,
+                            workspace=None, stream=None):
+    """bf16_decode_attn that adds every token's attention weight to its score, fp32 [B][Hkv][Nmax]: score_out =
+    score + weights (score_out None: score itself, in place; score None: zeros).  other: (out, lse) of the same
+    queries over tokens that are not in this cache, or None; the result and the weights are then those of the
+    joint softmax.  Returns (out, lse, score_out)."""
+    B, Hq, D, dev = cache.B, cache.Hq, cache.D, _need_current(cache.k.device)
+    if score_out is None:
+        score_out = score
+    if score_out is None:
+        raise LoopVQError(LOOPVQ_ERR_INVALID_ARG, "score and score_out are both None")
+    _need(q, "q", (B, Hq, D), _Q, dev)
+    _need(lens, "lens", (B,), _I32, dev)
+    if starts is not None:
+        _need(starts, "starts", (B,), _I32, dev)
+    for t, name in ((score, "score"), (score_out, "score_out")):
+        if t is not None:
+            _need(t, name, (B, cache.Hkv, cache.Nmax), _F32, dev)
+    oo, ol = _need_other(other, B, Hq, D, dev)
+    if out is None:
+        out = torch.empty((B, Hq, D), dtype=torch.float32, device=dev)
+    if lse is None:
+        lse = torch.empty((B, Hq), dtype=torch.float32, device=dev)
+    _need(out, "out", (B, Hq, D), _F32, dev)
+    _need(lse, "lse", (B, Hq), _F32, dev)
+    if workspace is None:
+        workspace = torch.empty(max(bf16_scored_workspace_bytes(cache, max_len), 16), dtype=torch.uint8, device=dev)
+    _check(lib().loopvq_bf16_decode_attn_scored(cache.ref(), _ptr(q), _ptr(starts), _ptr(lens), max_len, scale,
+                                                _ptr(oo), _ptr(ol), _ptr(score), _ptr(score_out), _ptr(out),
+                                                _ptr(lse), _ptr(workspace),
+                                                workspace.numel() * workspace.element_size(), _stream(stream)))
+    return out, lse, score_out
+
+
+def bf16_evict_workspace_bytes(cache: Bf16Cache, max_len: int, budget: int) -> int:
+    return lib().loopvq_bf16_evict_workspace_bytes(cache.ref(), max_len, budget)
+
+
+def bf16_evict(cache: Bf16Cache, score: torch.Tensor, pos: torch.Tensor, lens: torch.Tensor, next_pos: torch.Tensor,
+               max_len: int, budget: int, n_sink: int = 8, n_recent: int = 64, score_out=None, pos_out=None,
+               lens_out=None, workspace=None, stream=None):
+    """Keep at most `budget` tokens of every (sequence, KV head): positions below n_sink, the n_recent positions
+    before next_pos, and the highest scores; kept rows behind the budget move into emptied slots of cache.k and
+    cache.v.  score fp32 and pos int32 [B][Hkv][Nmax], lens and next_pos int32 [B]; the outputs default to the
+    inputs (in place).  Returns (score_out, pos_out, lens_out)."""
+    B, H, N, dev = cache.B, cache.Hkv, cache.Nmax, _need_current(cache.k.device)
+    score_out = score if score_out is None else score_out
+    pos_out = pos if pos_out is None else pos_out
+    lens_out = lens if lens_out is None else lens_out
+    for t, name, shape, dt in ((score, "score", (B, H, N), _F32), (pos, "pos", (B, H, N), _I32),
+                               (lens, "lens", (B,), _I32), (next_pos, "next_pos", (B,), _I32),
+                               (score_out, "score_out", (B, H, N), _F32), (pos_out, "pos_out", (B, H, N), _I32),
+                               (lens_out, "lens_out", (B,), _I32)):
+        _need(t, name, shape, dt, dev)
+    if workspace is None:
+        workspace = torch.empty(max(bf16_evict_workspace_bytes(cache, max_len, budget), 16), dtype=torch.uint8,
+                                device=dev)
+    _check(lib().loopvq_bf16_evict(cache.ref(), _ptr(score), _ptr(pos), _ptr(lens), _ptr(next_pos), max_len, budget,
+                                   n_sink, n_recent, _ptr(score_out), _ptr(pos_out), _ptr(lens_out), _ptr(workspace),
+                                   workspace.numel() * workspace.element_size(), _stream(stream)))
+    return score_out, pos_out, lens_out
 
 
 class Tasq:
