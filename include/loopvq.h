@@ -44,7 +44,7 @@ typedef enum {
     LOOPVQ_ERR_UNSUPPORTED = 2,   /* valid but not built: D, c, Tc, Hq/Hkv outside the supported set */
     LOOPVQ_ERR_WORKSPACE = 3,     /* workspace missing or smaller than loopvq_decode_workspace_bytes */
     LOOPVQ_ERR_CUDA = 4,          /* a launch failed; loopvq_last_error() holds the CUDA message */
-    LOOPVQ_ERR_TIMEOUT = 5,       /* reported by loopvq_fault_check: an encode's bounded wait ran out */
+    LOOPVQ_ERR_TIMEOUT = 5,       /* reported by loopvq_fault_check: a kernel's bounded wait ran out */
     LOOPVQ_ERR_OVERFLOW = 6       /* reported by loopvq_fault_check: a window roll found the coded cache full */
 } loopvq_status;
 
@@ -218,6 +218,60 @@ loopvq_status loopvq_bf16_decode_attn(const loopvq_bf16_cache *cache, const uint
 loopvq_status loopvq_merge2(const float *out_a, const float *lse_a, const float *out_b,
                             const float *lse_b, int rows, int D, float *out, float *lse,
                             void *stream);
+
+/* Workspace bytes loopvq_bf16_shared_attn / loopvq_shared_attn need for `rows` queries and up to max_len tokens. */
+size_t loopvq_bf16_shared_workspace_bytes(const loopvq_bf16_cache *cache, int rows, int max_len);
+size_t loopvq_shared_workspace_bytes(const loopvq_cache *cache, int rows, int max_len);
+
+/*
+ * Attention of many query tokens over one sequence of a bf16 cache: the
+ * prefix that a batch shares, read once for all of them on the tensor cores.
+ * (An operator of this library: the paper decodes every sequence over its own
+ * cache.)  For every query token r < rows and query head hq (KV head
+ * hq / (Hq/Hkv)), over the tokens start <= n < len of sequence seq:
+ *   s_n = scale * <q_r,hq, k_n>,  out = sum_n softmax(s)_n v_n,
+ *   lse = ln sum_n exp(s_n).
+ * Every query attends to every one of these tokens.  With another part of the
+ * same softmax (each query's attention over tokens of its own, from
+ * loopvq_bf16_decode_attn or any other decode call) out and lse are the merged
+ * ones, as by loopvq_merge2, at no further launch.
+ *
+ * seq        0 <= seq < B: the sequence that holds the prefix.
+ * q          bf16 [rows][Hq][D], rotated at the queries' positions, 16-byte aligned.
+ * rows       >= 0 query tokens (of any number of sequences); 0 launches nothing.
+ * starts, lens  int32 [B] device (starts may be NULL); the entries of seq are
+ *            read and clamped as in loopvq_decode_attn_range.
+ * max_len    host upper bound of len, 0 <= max_len <= Nmax.
+ * scale      <= 0 selects 1/sqrt(D).
+ * other_out  fp32 [rows][Hq][D] and other_lse fp32 [rows][Hq]: the other part,
+ *            or both NULL; a row with other_lse = -inf has no other tokens.  out
+ *            may be other_out and lse may be other_lse.
+ * out        fp32 [rows][Hq][D]; lse fp32 [rows][Hq], may be NULL.  No tokens at
+ *            all: zeros and -inf.
+ * workspace  of at least loopvq_bf16_shared_workspace_bytes(cache, rows, max_len)
+ *            bytes, 16-byte aligned, ordered like any workspace.
+ * B * Hkv * Nmax counts rows of the cache; Hkv * Nmax < 2^31.  Waits inside the
+ * kernel are bounded (loopvq_set_wait_limit_ns); one that runs out gives NaN rows
+ * and a fault (loopvq_fault_check).  The first call on a device looks up the fault
+ * word and a driver entry point: make it before any stream capture.
+ */
+loopvq_status loopvq_bf16_shared_attn(const loopvq_bf16_cache *cache, int seq, const uint16_t *q, int rows,
+                                      const int32_t *starts, const int32_t *lens, int max_len, float scale,
+                                      const float *other_out, const float *other_lse, float *out, float *lse,
+                                      void *workspace, size_t ws_bytes, void *stream);
+
+/*
+ * loopvq_bf16_shared_attn over a coded cache: loop step t of layer `layer` of
+ * sequence seq, whose keys and values are rebuilt (and the keys rotated at
+ * their positions, the token indices) once for all queries, as in
+ * loopvq_decode_attn.  Codes of K and above rebuild to unspecified values.
+ * Workspace of at least loopvq_shared_workspace_bytes(cache, rows, max_len)
+ * bytes.  Not for TaSQ-coded keys.
+ */
+loopvq_status loopvq_shared_attn(const loopvq_cache *cache, int layer, int t, int seq, const uint16_t *q, int rows,
+                                 const int32_t *starts, const int32_t *lens, int max_len, float scale,
+                                 const float *other_out, const float *other_lse, float *out, float *lse,
+                                 void *workspace, size_t ws_bytes, void *stream);
 
 /* Workspace bytes loopvq_bf16_decode_attn_scored needs for up to max_len tokens per sequence. */
 size_t loopvq_bf16_scored_workspace_bytes(const loopvq_bf16_cache *cache, int max_len);
@@ -484,6 +538,9 @@ const char *loopvq_last_error(void);
  *     out it stops, waits (bounded by 2 s) for the work it already issued,
  *     releases its tensor memory, writes 0xFF code bytes for the tokens it
  *     had not finished and sets the fault;
+ *   - the shared-prefix attention (loopvq_bf16_shared_attn, loopvq_shared_attn)
+ *     bounds each wait for its own copies and products in the same way; a
+ *     thread block whose wait runs out makes the rows it worked on NaN;
  *   - loopvq_window_advance does not roll a sequence whose coded cache has no
  *     room for the page (coded_end + 8 > Nmax) and sets the fault; that
  *     sequence's window stays full, so its next append overwrites the newest
@@ -496,7 +553,7 @@ const char *loopvq_last_error(void);
  * any stream capture).
  *
  * loopvq_set_wait_limit_ns sets, for the whole process, the bound in
- * nanoseconds on each such wait of the encoder (default 2e9); 0 tests the
+ * nanoseconds on each such wait (default 2e9); 0 tests the
  * wait once without blocking and gives up if the work is not finished,
  * which tests use to exercise this path.
  * No page of the paper corresponds; it is the library's error channel.

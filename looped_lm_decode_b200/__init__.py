@@ -9,4 +9,5 @@ from .loopvq import (Cache, CacheDesc, LoopVQError, prepare, encode, decode_attn
                      merge2, Window, WindowDesc, window_advance, window_append, window_workspace_bytes,
                      window_decode_attn, window_append_decode_attn, Tasq, TasqDesc, tasq_encode,
                      tasq_decode_attn, fault_check, set_wait_limit_ns, wait_limit_ns,
+                     bf16_shared_attn, bf16_shared_workspace_bytes, shared_attn, shared_workspace_bytes,
                      bf16_decode_attn_scored, bf16_scored_workspace_bytes, bf16_evict, bf16_evict_workspace_bytes)

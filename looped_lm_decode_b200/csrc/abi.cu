@@ -275,6 +275,90 @@ static loopvq_status check_other(const float *other_out, const float *other_lse)
     return check_word_ptr(other_lse, "other_lse");
 }
 
+// Arguments that the two shared-prefix calls have in common; sets the default scale.
+static loopvq_status check_shared(int B, int Hkv, int Hq, int D, int Nmax, int seq, const uint16_t *q, int rows,
+                                  const int32_t *starts, const int32_t *lens, int max_len, float *scale,
+                                  const float *other_out, const float *other_lse, float *out, float *lse) {
+    if (seq < 0 || seq >= B) return fail(LOOPVQ_ERR_INVALID_ARG, "seq=%d out of [0, %d)", seq, B);
+    if (rows < 0) return fail(LOOPVQ_ERR_INVALID_ARG, "rows=%d is negative", rows);
+    if (rows == 0) return LOOPVQ_OK;
+    LQ_TRY(check_ptr(q, "q"));
+    LQ_TRY(check_word_ptr(lens, "lens"));
+    LQ_TRY(check_ptr(out, "out"));
+    LQ_TRY(check_other(other_out, other_lse));
+    if (starts) LQ_TRY(check_word_ptr(starts, "starts"));
+    if (lse) LQ_TRY(check_word_ptr(lse, "lse"));
+    if (max_len < 0 || max_len > Nmax)
+        return fail(LOOPVQ_ERR_INVALID_ARG, "max_len=%d out of [0, Nmax=%d]", max_len, Nmax);
+    if (!std::isfinite(*scale)) return fail(LOOPVQ_ERR_INVALID_ARG, "scale is not finite");
+    if (*scale <= 0.f) *scale = 1.0f / std::sqrt((float)D);
+    if (Hkv > 65535 || (int64_t)rows * (Hq / Hkv) > 65535LL * 128)
+        return fail(LOOPVQ_ERR_UNSUPPORTED, "Hkv=%d or rows * Hq / Hkv = %lld too large", Hkv,
+                    (long long)rows * (Hq / Hkv));
+    const size_t n = (size_t)rows * Hq;
+    if (other_out) {
+        LQ_TRY(check_same_or_apart(other_out, out, n * D * sizeof(float), "out"));
+        if (lse) LQ_TRY(check_same_or_apart(other_lse, lse, n * sizeof(float), "lse"));
+    }
+    return LOOPVQ_OK;
+}
+
+static loopvq_status check_ws(const void *workspace, size_t given, size_t need) {
+    if (!workspace || given < need)
+        return fail(LOOPVQ_ERR_WORKSPACE, "workspace of %zu bytes needed, %zu given", need, workspace ? given : (size_t)0);
+    if (!aligned16(workspace)) return fail(LOOPVQ_ERR_INVALID_ARG, "workspace is not 16-byte aligned");
+    return LOOPVQ_OK;
+}
+
+size_t loopvq_bf16_shared_workspace_bytes(const loopvq_bf16_cache *c, int rows, int max_len) {
+    if (check_bf16(c) != LOOPVQ_OK || rows < 0 || max_len < 0 || max_len > c->Nmax) return 0;
+    return loopvq::shared_ws_bytes(c->Hkv, c->Hq, c->D, rows, max_len, false);
+}
+
+size_t loopvq_shared_workspace_bytes(const loopvq_cache *cc, int rows, int max_len) {
+    if (check_shape(cc) != LOOPVQ_OK || rows < 0 || max_len < 0 || max_len > cc->Nmax) return 0;
+    return loopvq::shared_ws_bytes(cc->Hkv, cc->Hq, cc->D, rows, max_len, true);
+}
+
+loopvq_status loopvq_bf16_shared_attn(const loopvq_bf16_cache *c, int seq, const uint16_t *q, int rows,
+                                      const int32_t *starts, const int32_t *lens, int max_len, float scale,
+                                      const float *other_out, const float *other_lse, float *out, float *lse,
+                                      void *workspace, size_t ws_bytes, void *stream) {
+    g_err[0] = 0;
+    LQ_TRY(check_bf16(c));
+    LQ_TRY(check_shared(c->B, c->Hkv, c->Hq, c->D, c->Nmax, seq, q, rows, starts, lens, max_len, &scale, other_out,
+                        other_lse, out, lse));
+    if ((int64_t)c->Hkv * c->Nmax + 128 > INT32_MAX)
+        return fail(LOOPVQ_ERR_UNSUPPORTED, "Hkv * Nmax = %lld exceeds 2^31", (long long)c->Hkv * c->Nmax);
+    if (rows == 0) return LOOPVQ_OK;
+    LQ_TRY(check_ws(workspace, ws_bytes, loopvq::shared_ws_bytes(c->Hkv, c->Hq, c->D, rows, max_len, false)));
+    cudaError_t e = loopvq::launch_bf16_shared(*c, seq, q, rows, starts, lens, max_len, scale, {other_out, other_lse},
+                                               out, lse, workspace, (cudaStream_t)stream);
+    if (e != cudaSuccess) return cuda_fail(e, "loopvq_bf16_shared_attn");
+    return LOOPVQ_OK;
+}
+
+loopvq_status loopvq_shared_attn(const loopvq_cache *cc, int layer, int t, int seq, const uint16_t *q, int rows,
+                                 const int32_t *starts, const int32_t *lens, int max_len, float scale,
+                                 const float *other_out, const float *other_lse, float *out, float *lse,
+                                 void *workspace, size_t ws_bytes, void *stream) {
+    g_err[0] = 0;
+    LQ_TRY(check_shape(cc));
+    LQ_TRY(check_ptr(cc->idx, "idx"));
+    LQ_TRY(check_ptr(cc->slices, "slices"));
+    LQ_TRY(check_ptr(cc->rope, "rope"));
+    if (layer < 0 || layer >= cc->L) return fail(LOOPVQ_ERR_INVALID_ARG, "layer=%d out of [0, %d)", layer, cc->L);
+    if (t < 0 || t >= cc->T) return fail(LOOPVQ_ERR_INVALID_ARG, "t=%d out of [0, %d)", t, cc->T);
+    LQ_TRY(check_shared(cc->B, cc->Hkv, cc->Hq, cc->D, cc->Nmax, seq, q, rows, starts, lens, max_len, &scale,
+                        other_out, other_lse, out, lse));
+    if (rows == 0) return LOOPVQ_OK;
+    LQ_TRY(check_ws(workspace, ws_bytes, loopvq::shared_ws_bytes(cc->Hkv, cc->Hq, cc->D, rows, max_len, true)));
+    cudaError_t e = loopvq::launch_shared(*cc, layer, t, seq, q, rows, starts, lens, max_len, scale,
+                                          {other_out, other_lse}, out, lse, workspace, (cudaStream_t)stream);
+    if (e != cudaSuccess) return cuda_fail(e, "loopvq_shared_attn");
+    return LOOPVQ_OK;
+}
+
 size_t loopvq_bf16_scored_workspace_bytes(const loopvq_bf16_cache *c, int max_len) {
     if (check_bf16(c) != LOOPVQ_OK || max_len < 0 || max_len > c->Nmax) return 0;
     return loopvq::bf16_scored_ws_bytes(*c, max_len);

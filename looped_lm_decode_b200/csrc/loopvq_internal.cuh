@@ -45,6 +45,7 @@ void set_last_error(const char *msg);
 // Bits of the per-GPU fault word (faults.cu), reported by loopvq_fault_check.
 constexpr unsigned int kFaultEncodeWait = 1u;   // a tensor-core encode's bounded wait ran out
 constexpr unsigned int kFaultWindowFull = 2u;   // a window roll found the coded cache full
+constexpr unsigned int kFaultAttnWait = 4u;     // a shared-prefix attention's bounded wait ran out
 // Device address of the fault word on the current device (looked up once per device).
 cudaError_t fault_word_for_current_device(unsigned int **out);
 // Bound on each wait of the tensor-core encoder for its own contraction (loopvq_set_wait_limit_ns).
@@ -105,6 +106,17 @@ cudaError_t launch_bf16_decode(const loopvq_bf16_cache &c, const DecodePlan &pla
                                const int32_t *starts, const int32_t *lens, int max_len, float scale, float *out,
                                float *lse, void *workspace, cudaStream_t s, const Bf16Scored *sc = nullptr);
 size_t bf16_scored_ws_bytes(const loopvq_bf16_cache &c, int max_len);
+// Attention of many query tokens over one sequence (shared_attn.cu), with another part to merge in (or nulls).
+struct SharedOther {
+    const float *out, *lse;
+};
+size_t shared_ws_bytes(int Hkv, int Hq, int D, int rows, int max_len, bool coded);
+cudaError_t launch_bf16_shared(const loopvq_bf16_cache &c, int seq, const uint16_t *q, int rows, const int32_t *starts,
+                               const int32_t *lens, int max_len, float scale, const SharedOther &other, float *out,
+                               float *lse, void *workspace, cudaStream_t s);
+cudaError_t launch_shared(const loopvq_cache &cc, int layer, int t, int seq, const uint16_t *q, int rows,
+                          const int32_t *starts, const int32_t *lens, int max_len, float scale,
+                          const SharedOther &other, float *out, float *lse, void *workspace, cudaStream_t s);
 // Eviction (evict.cu).  Workspace: per (sequence, KV head) a count, the emptied slots and the moved tokens' slots.
 struct EvictArgs {
     uint16_t *k, *v;         // [B][Hkv][Nmax][D]

@@ -1,0 +1,788 @@
+// Attention of many query tokens over one sequence of a cache: the prefix that a batch shares, read (and, in a
+// coded cache, rebuilt) once for all of them.
+//
+// The library's own operator (the LoopVQ paper decodes every sequence over its own cache).  For the R = rows *
+// Hq / Hkv query rows of a KV head, O = softmax(scale Q K^T) V over the prefix's tokens: two matrix products, so
+// both run on the tensor cores with accumulators in tensor memory.
+//
+// One CTA per (token split, KV head, up to 2 x 128 query rows).  Its warps:
+//   0-3, 4-7  softmax of stream 0 and stream 1: thread = query row = tensor-memory lane
+//   8         issues every product (one thread)
+//   9 ..      bf16 cache: one thread copies K and V tiles by TMA; coded cache: eight warps rebuild them
+// A step is one product pair S = Q K^T, O += P V of 128 rows by one tile of tokens.  Steps alternate between two
+// streams, each with its own S, O, maximum and sum, so that the products of one stream run under the softmax of
+// the other: with up to 128 rows the streams take the tiles in turn (and give two partial results), with more
+// they take the two halves of the rows (and share every tile).
+//
+// Precision: the library returns fp32, so P is not rounded to bf16 once but split into two bf16 parts (the
+// remainder of the first rounding in the second, 2^-18 of P at most), two products into the same accumulator; a
+// rebuilt, rotated key is split the same way.  bf16 queries, keys and values are exact.
+//
+// P overwrites S in place, 32 score columns becoming 16 + 16 columns of packed pairs.  The running maximum moves
+// only when a tile passes it by 2^8 (any reference is exact; it bounds P), so O is rarely rescaled.
+#include <cuda.h>
+
+#include <atomic>
+
+#include "decode_kernel.cuh"
+#include "tcgen05.cuh"
+
+namespace loopvq {
+
+namespace {
+
+struct SharedArgs {
+    const uint16_t *q;       // [rows][Hq][D]
+    const int32_t *start;    // of the sequence, or null
+    const int32_t *len;
+    float *ws_o;             // [nrec][rows * Hq][D], row = h * R + r
+    float2 *ws_ml;           // [nrec][rows * Hq]
+    int rows, Hkv, Hq, R, qpk, max_len, nsplit;
+    float qscale;            // scale * log2(e)
+    unsigned int *fault;
+    unsigned long long wait_ns;
+    // bf16 cache: rows of the sequence's tensor map per KV head
+    int head_rows;
+    // coded cache
+    const uint32_t *idx;     // of (layer, block, sequence, h = 0)
+    size_t idx_head;         // words per KV head
+    const uint16_t *slk, *slv;
+    const float *rope;
+    int K;
+};
+
+// Shared-memory plan (bytes from a 1024-byte boundary).  NT tokens per tile, KP bf16 parts per key.
+template <int D, int MB, int C>
+struct Plan {
+    static constexpr bool coded = C != 0;
+    static constexpr int NT = coded ? 64 : 128;
+    static constexpr int KP = coded ? 2 : 1;
+    static constexpr int kPanel = NT * 128;                          // 64 channels of a tile
+    static constexpr int kTile = (D / 64) * kPanel;
+    static constexpr int kStage = (KP + 1) * kTile;                  // K parts, then V
+    static constexpr int kQ = (D / 64) * 128 * 128;                  // one row block
+    static constexpr int ST = D == 64 ? (coded ? 4 : 4) : (MB == 1 ? 3 : 2);
+    static constexpr int kTable = coded ? 256 * C * 2 : 0;           // one slice; K then V
+    static constexpr int offQ = 0;
+    static constexpr int offStage = MB * kQ;
+    static constexpr int offTable = offStage + ST * kStage;
+    static constexpr int offBar = offTable + 2 * kTable;
+    static constexpr int kBars = 4 * ST + 7;
+    static constexpr int offTmem = offBar + kBars * 8;
+    static constexpr int kUsed = offTmem + 16;
+    static constexpr int kAlloc = kUsed + 1024;
+    static constexpr int kThreads = coded ? 9 * 32 + 256 : 320;
+    static_assert(kAlloc <= 232448, "shared memory");
+    static_assert(kAlloc > 116 * 1024 || D == 64, "one CTA per SM: tensor memory is allocated whole");
+};
+
+constexpr int kTmemCols = 512;                                       // S0 S1 at 0, 128; O0 O1 at 256, 384
+
+// Rows n (128 bytes of 64 channels) of a panel: 16-byte chunk j lies at chunk j ^ (n & 7).
+__device__ __forceinline__ uint32_t sw128(int n, int chunk) { return (uint32_t)n * 128u + ((uint32_t)(chunk ^ (n & 7)) << 4); }
+
+__device__ __forceinline__ void sts128(uint32_t addr, uint4 v) {
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
+                 : "memory");
+}
+
+// The running softmax of one query row of one stream, and what its thread does with a tile's scores.
+template <int D, int NT>
+struct RowSoftmax {
+    float m, l;                                                      // maximum reference (log2 units), sum
+
+    // S columns at ts; tokens [lo, hi) of the tile count; O columns at to.  first: O holds nothing yet.
+    // odone: barrier (parity) of the stream's previous O += P V.
+    __device__ __forceinline__ bool tile(uint32_t ts, uint32_t to, int lo, int hi, float qs, bool first, uint32_t odone,
+                                         uint32_t odone_parity, uint64_t limit, volatile int *dead) {
+        // NT = 64 shares the register file with the rebuilding warps (96 a thread): 32 scores at a time, read from
+        // tensor memory once for the maximum and once for the exponentials; NT = 128 keeps them
+        constexpr bool keep = NT == 128;
+        uint32_t v[keep ? NT / 32 : 1][32];
+        const bool edge = lo > 0 || hi < NT;
+        auto mask = [&](uint32_t (&x)[32], int c) {
+            if (edge) {
+#pragma unroll
+                for (int k = 0; k < 32; ++k)
+                    if (c * 32 + k < lo || c * 32 + k >= hi) x[k] = 0xff800000u;
+            }
+        };
+        if constexpr (keep) {
+#pragma unroll
+            for (int c = 0; c < NT / 32; ++c) tc::tmem_ld32(ts + c * 32, v[c]);
+#pragma unroll
+            for (int c = 0; c < NT / 32; ++c) tc::tmem_wait_ld(v[c]);
+        }
+        float a0 = -CUDART_INF_F, a1 = a0, a2 = a0, a3 = a0;
+#pragma unroll
+        for (int c = 0; c < NT / 32; ++c) {
+            uint32_t (&x)[32] = v[keep ? c : 0];
+            if constexpr (!keep) {
+                tc::tmem_ld32(ts + c * 32, x);
+                tc::tmem_wait_ld(x);
+            }
+            mask(x, c);
+#pragma unroll
+            for (int k = 0; k < 32; k += 4) {
+                a0 = fmaxf(a0, __uint_as_float(x[k]));
+                a1 = fmaxf(a1, __uint_as_float(x[k + 1]));
+                a2 = fmaxf(a2, __uint_as_float(x[k + 2]));
+                a3 = fmaxf(a3, __uint_as_float(x[k + 3]));
+            }
+        }
+        const float mt = fmaxf(fmaxf(a0, a1), fmaxf(a2, a3)) * qs;
+        const bool up = mt > m + 8.f;
+        if (__any_sync(0xffffffffu, up)) {
+            const float corr = up ? ex2(m - mt) : 1.f;
+            if (up) m = mt;
+            l *= corr;
+            if (!first) {
+                const bool ok = tc::mbar_wait_or_dead(odone, odone_parity, limit, dead);
+                if (!__all_sync(0xffffffffu, ok)) return false;
+                tc::tc_fence_after();
+#pragma unroll 1
+                for (int c = 0; c < D; c += 32) {
+                    uint32_t o[32];
+                    tc::tmem_ld32(to + c, o);
+                    tc::tmem_wait_ld(o);
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * corr);
+                    tc::tmem_st32(to + c, o);
+                }
+            }
+        }
+        const float nm = m == -CUDART_INF_F ? 0.f : -m;
+        float s0 = 0.f, s1 = 0.f;
+#pragma unroll
+        for (int c = 0; c < NT / 32; ++c) {
+            uint32_t (&x)[32] = v[keep ? c : 0];
+            if constexpr (!keep) {
+                tc::tmem_ld32(ts + c * 32, x);
+                tc::tmem_wait_ld(x);
+                mask(x, c);
+            }
+            uint32_t w[32];
+#pragma unroll
+            for (int k = 0; k < 16; ++k) {
+                const float p0 = ex2(fmaf(__uint_as_float(x[2 * k]), qs, nm));
+                const float p1 = ex2(fmaf(__uint_as_float(x[2 * k + 1]), qs, nm));
+                s0 += p0;
+                s1 += p1;
+                const uint32_t hi2 = cvt_bf16x2(p1, p0);
+                w[k] = hi2;
+                w[16 + k] = cvt_bf16x2(p1 - bf16hi(hi2), p0 - bf16lo(hi2));
+            }
+            tc::tmem_st32(ts + c * 32, w);
+        }
+        l += s0 + s1;
+        tc::tmem_wait_st();
+        return true;
+    }
+};
+
+// D channels (64 or 128), MB blocks of 128 query rows per CTA, C = 0 for a bf16 cache or the channels per code of
+// a coded one; PG: one codebook per channel group, whose slices (128 bytes per entry and more) do not fit beside
+// the tiles and are gathered from L2.
+template <int D, int MB, int C, bool PG>
+__global__ void __launch_bounds__(Plan<D, MB, C>::kThreads, 1)
+    shared_attn_kernel(const SharedArgs a, const __grid_constant__ CUtensorMap kmap,
+                       const __grid_constant__ CUtensorMap vmap) {
+    using P = Plan<D, MB, PG ? 4 : C>;
+    constexpr bool coded = C != 0;
+    constexpr int NT = P::NT, KP = P::KP, ST = P::ST, NPAN = D / 64;
+
+    extern __shared__ unsigned char smem_raw[];
+    const uint32_t base = (tc::smem_u32(smem_raw) + 1023u) & ~1023u;
+    unsigned char *smem = smem_raw + (base - tc::smem_u32(smem_raw));
+    const uint32_t sQ = base + P::offQ, sStage = base + P::offStage, bars = base + P::offBar;
+    auto kfull = [&](int s) { return bars + 8u * s; };
+    auto vfull = [&](int s) { return bars + 8u * (ST + s); };
+    auto kempty = [&](int s) { return bars + 8u * (2 * ST + s); };
+    auto vempty = [&](int s) { return bars + 8u * (3 * ST + s); };
+    auto sfull = [&](int w) { return bars + 8u * (4 * ST + w); };
+    auto pfull = [&](int w) { return bars + 8u * (4 * ST + 2 + w); };
+    auto odone = [&](int w) { return bars + 8u * (4 * ST + 4 + w); };
+    const uint32_t drain = bars + 8u * (4 * ST + 6);
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + P::offTmem);
+    volatile int *dead = reinterpret_cast<volatile int *>(smem + P::offTmem + 4);
+
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int split = blockIdx.x, h = blockIdx.y;
+    const int r0 = blockIdx.z * (MB * 128);                          // first query row of this CTA
+
+    const int len = min(max(__ldg(a.len), 0), a.max_len);
+    const int st = a.start ? min(max(__ldg(a.start), 0), len) : 0;
+    const int tok0 = coded ? (st & ~3) : st;                         // index words come in tiles of 4 tokens
+    const int tiles_all = len > st ? (len - tok0 + NT - 1) / NT : 0;
+    const int t_first = (int)((long long)split * tiles_all / a.nsplit);
+    const int ntiles = (int)((long long)(split + 1) * tiles_all / a.nsplit) - t_first;
+    const int tok_first = tok0 + t_first * NT;
+    const int nsteps = ntiles * MB;                                  // step i: stream i & 1
+    const size_t RT = (size_t)a.rows * a.Hq;
+    // record of stream w: two row blocks share one record index, alternating tiles make two
+    auto record = [&](int w) { return MB == 2 ? (size_t)split : (size_t)split * 2 + w; };
+
+    if (ntiles == 0) {                                               // nothing in this split
+        for (int r = r0 + tid; r < min(r0 + MB * 128, a.R); r += P::kThreads) {
+            a.ws_ml[record(0) * RT + (size_t)h * a.R + r] = f2(-CUDART_INF_F, 0.f);
+            if (MB == 1) a.ws_ml[record(1) * RT + (size_t)h * a.R + r] = f2(-CUDART_INF_F, 0.f);
+        }
+        return;
+    }
+
+    // ---- set-up: barriers and the first copies, tensor memory, queries (and the slices of a coded cache)
+    auto issue_k = [&](int t) {
+        const int s = t % ST;
+        tc::mbar_expect_tx(kfull(s), P::kTile);
+#pragma unroll
+        for (int p = 0; p < NPAN; ++p)
+            tc::tma_load_2d(sStage + s * P::kStage + p * P::kPanel, &kmap, p * 64, h * a.head_rows + tok_first + t * NT,
+                            kfull(s));
+    };
+    auto issue_v = [&](int t) {
+        const int s = t % ST;
+        tc::mbar_expect_tx(vfull(s), P::kTile);
+#pragma unroll
+        for (int p = 0; p < NPAN; ++p)
+            tc::tma_load_2d(sStage + s * P::kStage + KP * P::kTile + p * P::kPanel, &vmap, p * 64,
+                            h * a.head_rows + tok_first + t * NT, vfull(s));
+    };
+    int issued = 0;                                                  // tiles copied by the producer thread
+    if (warp == 9 && lane == 0) {
+        for (int s = 0; s < ST; ++s) {
+            tc::mbar_init(kfull(s), coded ? 8 : 1);
+            tc::mbar_init(vfull(s), 1);
+            tc::mbar_init(kempty(s), 1);
+            tc::mbar_init(vempty(s), 1);
+        }
+        for (int w = 0; w < 2; ++w) {
+            tc::mbar_init(sfull(w), 1);
+            tc::mbar_init(pfull(w), 128);
+            tc::mbar_init(odone(w), 1);
+        }
+        tc::mbar_init(drain, 1);
+        *dead = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        if constexpr (!coded) {
+            for (; issued < ntiles && issued < ST; ++issued) {
+                issue_k(issued);
+                issue_v(issued);
+            }
+        }
+    }
+    if (warp == 8) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(tc::smem_u32(tmem_slot)),
+                     "r"(kTmemCols));
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    }
+    for (int it = tid; it < MB * 128 * (D / 8); it += P::kThreads) { // 16-byte chunks of the query rows
+        const int r = it / (D / 8), ch = it % (D / 8);
+        uint4 v = make_uint4(0, 0, 0, 0);
+        if (r0 + r < a.R) {
+            const int row = (r0 + r) / a.qpk, g = (r0 + r) % a.qpk;
+            v = *reinterpret_cast<const uint4 *>(a.q + ((size_t)row * a.Hq + h * a.qpk + g) * D + ch * 8);
+        }
+        sts128(sQ + (r / 128) * P::kQ + (ch / 8) * (128 * 128) + sw128(r % 128, ch % 8), v);
+    }
+    if constexpr (coded && !PG) {
+        const uint16_t *src[2] = {a.slk + (size_t)h * a.K * C, a.slv + (size_t)h * a.K * C};
+        for (int it = tid; it < 2 * 256 * C / 4; it += P::kThreads) {
+            const int kv = it / (256 * C / 4), e = it % (256 * C / 4) * 4;
+            uint2 v = make_uint2(0, 0);                              // entries past K: zeros
+            if (e / C < a.K) v = *reinterpret_cast<const uint2 *>(src[kv] + e);
+            *reinterpret_cast<uint2 *>(smem + P::offTable + kv * P::kTable + e * 2) = v;
+        }
+    }
+    tc::fence_async_smem();
+    tc::tc_fence_before();
+    __syncthreads();
+    tc::tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+
+    if (warp < 8) {
+        // ---- softmax of stream w: 128 threads, one query row each
+        const int w = warp >> 2, row = tid & 127;
+        const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
+        const uint32_t ts = tmem + lane_base + w * 128, to = tmem + lane_base + 256 + w * 128;
+        const int rq = r0 + (MB == 2 ? w * 128 : 0) + row;           // query row of this thread
+        const bool any = __any_sync(0xffffffffu, rq < a.R);          // warps of padding only keep step
+        RowSoftmax<D, NT> sm{-CUDART_INF_F, 0.f};
+        bool ok = true;
+        int j = 0;
+        for (int i = w; i < nsteps; i += 2, ++j) {
+            const int t = MB == 2 ? j : i;
+            ok = __all_sync(0xffffffffu, tc::mbar_wait_or_dead(sfull(w), j & 1, a.wait_ns, dead));
+            if (!ok) break;
+            tc::tc_fence_after();
+            if (any) {
+                const int n0 = tok_first + t * NT;
+                ok = sm.tile(ts, to, st - n0, len - n0, a.qscale, j == 0, odone(w), (j - 1) & 1, a.wait_ns, dead);
+                if (!ok) break;
+            }
+            tc::tc_fence_before();
+            tc::mbar_arrive(pfull(w));
+        }
+        if (ok && j > 0) {
+            ok = __all_sync(0xffffffffu, tc::mbar_wait_or_dead(odone(w), (j - 1) & 1, a.wait_ns, dead));
+            tc::tc_fence_after();
+        }
+        if (any) {
+            const size_t rec = record(w) * RT + (size_t)h * a.R + rq;
+            if (rq < a.R)
+                a.ws_ml[rec] = !ok ? f2(0.f, CUDART_NAN_F) : j > 0 ? f2(sm.m, sm.l) : f2(-CUDART_INF_F, 0.f);
+            if (ok && j > 0) {
+#pragma unroll 1
+                for (int c = 0; c < D; c += 32) {
+                    uint32_t o[32];
+                    tc::tmem_ld32(to + c, o);
+                    tc::tmem_wait_ld(o);
+                    if (rq < a.R) {
+                        uint4 *dst = reinterpret_cast<uint4 *>(a.ws_o + rec * D + c);
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) dst[k] = make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+                    }
+                }
+            }
+        }
+        tc::tc_fence_before();
+    } else if (warp == 8) {
+        // ---- products
+        constexpr uint32_t id_qk = tc::idesc_bf16(128, NT);
+        constexpr uint32_t id_pv = tc::idesc_bf16(128, D) | (1u << 16);        // B: channels contiguous
+        bool ok = true;
+        auto wait = [&](uint32_t bar, uint32_t parity) {
+            ok = __all_sync(0xffffffffu, tc::mbar_wait_or_dead(bar, parity, a.wait_ns, dead));
+            return ok;
+        };
+        auto qk = [&](int i) {                                       // S of step i
+            const int t = MB == 2 ? i >> 1 : i, s = t % ST;
+            if (!wait(kfull(s), (t / ST) & 1)) return;
+            tc::tc_fence_after();
+            if (lane == 0) {
+                const uint32_t qb = sQ + (MB == 2 ? (i & 1) * P::kQ : 0), kb = sStage + s * P::kStage;
+#pragma unroll
+                for (int part = 0; part < KP; ++part)
+#pragma unroll
+                    for (int k = 0; k < D / 16; ++k)                 // 16 channels per product: 32 bytes of a row
+                        tc::mma_bf16(tmem + (i & 1) * 128,
+                                     tc::smem_desc_sw128(qb + (k / 4) * (128 * 128) + (k % 4) * 32, 16, 1024),
+                                     tc::smem_desc_sw128(kb + part * P::kTile + (k / 4) * P::kPanel + (k % 4) * 32, 16, 1024),
+                                     id_qk, part + k > 0);
+                if (!coded && (MB == 1 || (i & 1)) && t + ST < ntiles) tc::mma_commit(kempty(s));
+                tc::mma_commit(sfull(i & 1));
+            }
+            __syncwarp();
+        };
+        qk(0);
+        if (ok && nsteps > 1) qk(1);
+        for (int i = 0; ok && i < nsteps; ++i) {
+            const int t = MB == 2 ? i >> 1 : i, s = t % ST, w = i & 1;
+            const uint32_t vb = sStage + s * P::kStage + KP * P::kTile;
+            if constexpr (!coded) {
+                if (!wait(vfull(s), (t / ST) & 1)) break;
+                // rows behind the last token may hold anything: 0 x that has to be 0
+                const int end = len - (tok_first + t * NT);
+                if (end < NT && (MB == 1 || w == 0)) {
+                    for (int it = lane; it < (NT - end) * (D / 8); it += 32) {
+                        const int n = end + it / (D / 8), ch = it % (D / 8);
+                        sts128(vb + (ch / 8) * P::kPanel + n * 128 + (ch % 8) * 16, make_uint4(0, 0, 0, 0));
+                    }
+                    tc::fence_async_smem();
+                    __syncwarp();
+                }
+            }
+            if (!wait(pfull(w), (i >> 1) & 1)) break;
+            tc::tc_fence_after();
+            if (lane == 0) {
+                const uint32_t od = tmem + 256 + w * 128, pa = tmem + w * 128;
+#pragma unroll
+                for (int part = 0; part < 2; ++part)
+#pragma unroll
+                    for (int k = 0; k < NT / 16; ++k)                // 16 tokens per product: 8 packed columns
+                        tc::mma_bf16_ta(od, pa + (k / 2) * 32 + part * 16 + (k % 2) * 8,
+                                        tc::smem_desc_sw128(vb + k * 2048, P::kPanel, 1024), id_pv,
+                                        i > 1 || part + k > 0);
+                if ((MB == 1 || w == 1) && t + ST < ntiles) tc::mma_commit(vempty(s));
+                tc::mma_commit(odone(w));
+            }
+            __syncwarp();
+            if (i + 2 < nsteps) qk(i + 2);
+        }
+    } else if constexpr (!coded) {
+        // ---- copies
+        if (lane == 0) {
+            bool ok = true;
+            for (int t = issued; t < ntiles; ++t) {
+                const int s = t % ST;
+                const uint32_t par = (t / ST - 1) & 1;
+                if (!(ok = tc::mbar_wait_or_dead(kempty(s), par, a.wait_ns, dead))) break;
+                issue_k(t);
+                if (!(ok = tc::mbar_wait_or_dead(vempty(s), par, a.wait_ns, dead))) {
+                    // the drain below waits for both halves of every issued tile
+                    issue_v(t);
+                    ++issued;
+                    break;
+                }
+                issue_v(t);
+                ++issued;
+            }
+        }
+    } else {
+        // ---- rebuilding: a warp takes 8 tokens of the tile, a lane one token and one piece of 8 + 8 channels
+        // (a RoPE pair each) at a time
+        constexpr int NP = D / (2 * C);
+        constexpr int IT = D / 64;                                   // rounds of 4 pieces
+        constexpr int NW = C == 4 ? 2 : 1;                           // index words per piece
+        const int rw = warp - 9, tl = lane & 7, pl = lane >> 3;
+        const uint32_t *idx = a.idx + (size_t)h * a.idx_head;
+        const unsigned char *tab[2] = {smem + P::offTable, smem + P::offTable + P::kTable};
+        const uint16_t *gsl[2] = {a.slk + (size_t)h * a.K * D, a.slv + (size_t)h * a.K * D};
+        const int kmax = a.K - 1;
+        auto load_words = [&](int t, uint32_t (&wd)[IT][NW]) {
+            const int n = tok_first + t * NT + rw * 8 + tl;
+#pragma unroll
+            for (int it = 0; it < IT; ++it)
+#pragma unroll
+                for (int k = 0; k < NW; ++k) {
+                    const int piece = it * 4 + pl;
+                    const int p = C == 4 ? piece * 2 + k : piece / (C / 8);
+                    wd[it][k] = (t < ntiles && n >= st && n < len) ? __ldg(idx + idx_word(n, p, NP)) : 0u;
+                }
+        };
+        // 8 channels of piece `piece` (half 0: the low channels, 1: their partners) from the codes of its words
+        auto gather = [&](int kv, int half, int piece, const uint32_t (&wd)[NW]) -> uint4 {
+            const int sh = kv * 16 + half * 8;
+            uint4 v;
+            if constexpr (C == 4) {
+                const int c0 = (wd[0] >> sh) & 255, c1 = (wd[NW - 1] >> sh) & 255;
+                uint2 x, y;
+                if constexpr (PG) {
+                    const int g = half * NP + piece * 2;
+                    x = __ldg(reinterpret_cast<const uint2 *>(gsl[kv] + (size_t)min(c0, kmax) * D + g * C));
+                    y = __ldg(reinterpret_cast<const uint2 *>(gsl[kv] + (size_t)min(c1, kmax) * D + (g + 1) * C));
+                } else {
+                    x = *reinterpret_cast<const uint2 *>(tab[kv] + c0 * 8);
+                    y = *reinterpret_cast<const uint2 *>(tab[kv] + c1 * 8);
+                }
+                v = make_uint4(x.x, x.y, y.x, y.y);
+            } else {
+                const int c0 = (wd[0] >> sh) & 255, sub = piece % (C / 8);
+                if constexpr (PG) {
+                    const int g = half * NP + piece / (C / 8);
+                    v = __ldg(reinterpret_cast<const uint4 *>(gsl[kv] + (size_t)min(c0, kmax) * D + g * C + sub * 8));
+                } else {
+                    v = *reinterpret_cast<const uint4 *>(tab[kv] + c0 * (C * 2) + sub * 16);
+                }
+            }
+            return v;
+        };
+        uint32_t wd[IT][NW];
+        load_words(0, wd);
+        for (int t = 0; t < ntiles; ++t) {
+            const int s = t % ST;
+            const int nl = rw * 8 + tl, n = tok_first + t * NT + nl;
+            const bool in = n >= st && n < len;
+            float4 cs[IT][2], sn[IT][2];
+#pragma unroll
+            for (int it = 0; it < IT; ++it) {
+                const float4 *rp = reinterpret_cast<const float4 *>(a.rope + (size_t)(in ? n : tok0) * D + (it * 4 + pl) * 8);
+                cs[it][0] = __ldg(rp);
+                cs[it][1] = __ldg(rp + 1);
+                sn[it][0] = __ldg(rp + D / 8);
+                sn[it][1] = __ldg(rp + D / 8 + 1);
+            }
+            uint32_t nx[IT][NW];
+            load_words(t + 1, nx);
+            if (t >= ST) {
+                const bool ok = tc::mbar_wait_or_dead(vempty(s), (t / ST - 1) & 1, a.wait_ns, dead);
+                if (!__all_sync(0xffffffffu, ok)) break;
+            }
+            const uint32_t kb = sStage + s * P::kStage, vb = kb + KP * P::kTile;
+#pragma unroll
+            for (int it = 0; it < IT; ++it) {
+                const int piece = it * 4 + pl;
+                const uint4 z = make_uint4(0, 0, 0, 0);
+                const uint4 v0 = in ? gather(1, 0, piece, wd[it]) : z, v1 = in ? gather(1, 1, piece, wd[it]) : z;
+                const uint4 k0 = in ? gather(0, 0, piece, wd[it]) : z, k1 = in ? gather(0, 1, piece, wd[it]) : z;
+                const uint32_t kl[4] = {k0.x, k0.y, k0.z, k0.w}, kh[4] = {k1.x, k1.y, k1.z, k1.w};
+                const float c8[8] = {cs[it][0].x, cs[it][0].y, cs[it][0].z, cs[it][0].w,
+                                     cs[it][1].x, cs[it][1].y, cs[it][1].z, cs[it][1].w};
+                const float s8[8] = {sn[it][0].x, sn[it][0].y, sn[it][0].z, sn[it][0].w,
+                                     sn[it][1].x, sn[it][1].y, sn[it][1].z, sn[it][1].w};
+                uint32_t ah[4], al[4], bh[4], bl[4];                 // rotated: bf16 parts of the low and high channels
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const float2 x = unpack2(kl[k]), y = unpack2(kh[k]);
+                    const float ra0 = x.x * c8[2 * k] - y.x * s8[2 * k], ra1 = x.y * c8[2 * k + 1] - y.y * s8[2 * k + 1];
+                    const float rb0 = y.x * c8[2 * k] + x.x * s8[2 * k], rb1 = y.y * c8[2 * k + 1] + x.y * s8[2 * k + 1];
+                    ah[k] = cvt_bf16x2(ra1, ra0);
+                    al[k] = cvt_bf16x2(ra1 - bf16hi(ah[k]), ra0 - bf16lo(ah[k]));
+                    bh[k] = cvt_bf16x2(rb1, rb0);
+                    bl[k] = cvt_bf16x2(rb1 - bf16hi(bh[k]), rb0 - bf16lo(bh[k]));
+                }
+                // low channels 8 piece .., high channels D/2 + 8 piece ..
+                const uint32_t lo_at = sw128(nl, piece);
+                const uint32_t hi_at = D == 128 ? P::kPanel + sw128(nl, piece) : sw128(nl, piece + 4);
+                sts128(kb + lo_at, make_uint4(ah[0], ah[1], ah[2], ah[3]));
+                sts128(kb + hi_at, make_uint4(bh[0], bh[1], bh[2], bh[3]));
+                sts128(kb + P::kTile + lo_at, make_uint4(al[0], al[1], al[2], al[3]));
+                sts128(kb + P::kTile + hi_at, make_uint4(bl[0], bl[1], bl[2], bl[3]));
+                sts128(vb + lo_at, v0);
+                sts128(vb + hi_at, v1);
+            }
+            tc::fence_async_smem();
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(kfull(s));
+#pragma unroll
+            for (int it = 0; it < IT; ++it)
+#pragma unroll
+                for (int k = 0; k < NW; ++k) wd[it][k] = nx[it][k];
+        }
+    }
+
+    // ---- all done (or given up): free the tensor memory
+    __syncthreads();
+    if (*dead) {
+        if (tid == 0) atomicOr(a.fault, kFaultAttnWait);
+        if (!coded && warp == 9 && lane == 0)                        // copies still in flight
+            for (int t = issued > ST ? issued - ST : 0; t < issued; ++t) {
+                tc::mbar_wait_bounded(kfull(t % ST), (t / ST) & 1, tc::kDrainNs);
+                tc::mbar_wait_bounded(vfull(t % ST), (t / ST) & 1, tc::kDrainNs);
+            }
+        if (warp == 8 && lane == 0) {                                // products still in flight
+            tc::mma_commit(drain);
+            tc::mbar_wait_bounded(drain, 0, tc::kDrainNs);
+        }
+        __syncthreads();
+    }
+    tc::tc_fence_after();
+    if (warp == 8)
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols));
+}
+
+// Log-sum-exp merge of the records of every query row, and of another part over other tokens: one warp per row.
+// Row h * R + r of the records is query token r / qpk, head h * qpk + r % qpk.
+template <int D>
+__global__ void __launch_bounds__(256) shared_merge_kernel(const SharedArgs a, int nrec, const float *other_out,
+                                                           const float *other_lse, float *out, float *lse) {
+    constexpr int V = D / 32;                                        // channels per lane
+    const size_t RT = (size_t)a.rows * a.Hq;
+    const size_t row = (size_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+    const int lane = threadIdx.x & 31;
+    if (row >= RT) return;
+    const size_t r = row % a.R, h = row / a.R;
+    const size_t dst = (r / a.qpk) * a.Hq + h * a.qpk + r % a.qpk;
+    float mx = -CUDART_INF_F;
+    for (int i = lane; i < nrec; i += 32) mx = fmaxf(mx, a.ws_ml[(size_t)i * RT + row].x);
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+    const float ol = other_lse ? other_lse[dst] * 1.44269504088896340736f : -CUDART_INF_F;
+    const float top = fmaxf(mx, ol);
+    float acc[V], sum = 0.f;
+#pragma unroll
+    for (int k = 0; k < V; ++k) acc[k] = 0.f;
+    if (mx != -CUDART_INF_F) {
+#pragma unroll 4
+        for (int i = 0; i < nrec; ++i) {
+            const float2 ml = a.ws_ml[(size_t)i * RT + row];
+            if (ml.x == -CUDART_INF_F) continue;                     // a record without tokens was not written
+            const float w = ex2(ml.x - top);
+            sum += w * ml.y;
+            const float *o = a.ws_o + ((size_t)i * RT + row) * D + lane * V;
+            if constexpr (V == 4) {
+                const float4 x = *reinterpret_cast<const float4 *>(o);
+                acc[0] += w * x.x;
+                acc[1] += w * x.y;
+                acc[2] += w * x.z;
+                acc[3] += w * x.w;
+            } else {
+                const float2 x = *reinterpret_cast<const float2 *>(o);
+                acc[0] += w * x.x;
+                acc[1] += w * x.y;
+            }
+        }
+    }
+    float res[V];
+    const float wo = top == -CUDART_INF_F ? 0.f : ex2(ol - top);
+    const float total = sum + wo;
+    const float inv = total != 0.f ? 1.f / total : 0.f;              // no tokens at all: zeros
+#pragma unroll
+    for (int k = 0; k < V; ++k) {
+        float x = acc[k];
+        if (wo > 0.f) x += wo * other_out[dst * D + lane * V + k];
+        res[k] = x * inv;
+    }
+#pragma unroll
+    for (int k = 0; k < V; ++k) out[dst * D + lane * V + k] = res[k];
+    __syncwarp();                                                    // lse may be other_lse
+    if (lse != nullptr && lane == 0)
+        lse[dst] = total == 0.f ? -CUDART_INF_F : (top + log2f(total)) * 0.69314718055994530942f;
+}
+
+struct SharedPlan {
+    int mb, nsplit, nrec, nz;
+};
+
+// Splits: a CTA owns an SM (its tiles fill shared memory), so the splits that fill whole waves of 148 CTAs are
+// compared by waves x (tiles per split + set-up), the set-up and drain of a CTA counted as two tiles.
+SharedPlan plan_shared(int Hkv, int R, int max_len, int nt) {
+    SharedPlan p{};
+    p.mb = R > 128 ? 2 : 1;
+    p.nz = (R + p.mb * 128 - 1) / (p.mb * 128);
+    const long units = (long)Hkv * p.nz, tiles = (max_len + nt - 1) / nt;
+    long best = -1;
+    p.nsplit = 1;
+    for (int w = 1; w <= 4; ++w) {
+        long ns = 148L * w / units;
+        ns = ns < 1 ? 1 : ns > tiles ? (tiles > 0 ? tiles : 1) : ns;
+        const long waves = (units * ns + 147) / 148;
+        const long cost = waves * ((tiles + ns - 1) / ns + 2);
+        if (best < 0 || cost < best) {
+            best = cost;
+            p.nsplit = (int)ns;
+        }
+    }
+    p.nrec = p.nsplit * (p.mb == 1 ? 2 : 1);
+    return p;
+}
+
+size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
+
+size_t ws_bytes(const SharedPlan &p, size_t RT, int D) {
+    return align256(p.nrec * RT * D * sizeof(float)) + p.nrec * RT * sizeof(float2);
+}
+
+// cuTensorMapEncodeTiled through the runtime: the library does not link the driver.
+using EncodeTiled = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
+                                 const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
+                                 CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+cudaError_t encode_tiled_fn(EncodeTiled *out) {
+    static std::atomic<void *> fn{nullptr};
+    void *p = fn.load(std::memory_order_acquire);
+    if (p == nullptr) {
+        cudaDriverEntryPointQueryResult found;
+        cudaError_t e = cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &found);
+        if (e != cudaSuccess) return e;
+        if (found != cudaDriverEntryPointSuccess || p == nullptr) return cudaErrorNotSupported;
+        fn.store(p, std::memory_order_release);
+    }
+    *out = reinterpret_cast<EncodeTiled>(p);
+    return cudaSuccess;
+}
+
+// Map of one sequence's rows [rows][D]: boxes of 128 tokens x 64 channels, rows of 128 bytes swizzled.
+cudaError_t make_map(CUtensorMap *m, const uint16_t *p, size_t rows, int D, int nt) {
+    EncodeTiled enc;
+    cudaError_t e = encode_tiled_fn(&enc);
+    if (e != cudaSuccess) return e;
+    const cuuint64_t dims[2] = {(cuuint64_t)D, (cuuint64_t)rows};
+    const cuuint64_t strides[1] = {(cuuint64_t)D * 2};
+    const cuuint32_t box[2] = {64, (cuuint32_t)nt}, es[2] = {1, 1};
+    const CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<uint16_t *>(p), dims, strides, box, es,
+                           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+template <int D, int MB, int C, bool PG>
+cudaError_t launch_t(const SharedArgs &a, const SharedPlan &p, const CUtensorMap &km, const CUtensorMap &vm,
+                     cudaStream_t s) {
+    using PL = Plan<D, MB, PG ? 4 : C>;
+    auto kern = shared_attn_kernel<D, MB, C, PG>;
+    cudaError_t e = ensure_dynamic_smem((const void *)kern, PL::kAlloc);
+    if (e != cudaSuccess) return e;
+    kern<<<dim3(p.nsplit, a.Hkv, p.nz), PL::kThreads, PL::kAlloc, s>>>(a, km, vm);
+    return cudaGetLastError();
+}
+
+template <int C, bool PG>
+cudaError_t launch_d(int D, const SharedArgs &a, const SharedPlan &p, const CUtensorMap &km, const CUtensorMap &vm,
+                     cudaStream_t s) {
+    if (D == 128)
+        return p.mb == 2 ? launch_t<128, 2, C, PG>(a, p, km, vm, s) : launch_t<128, 1, C, PG>(a, p, km, vm, s);
+    if (D == 64) return p.mb == 2 ? launch_t<64, 2, C, PG>(a, p, km, vm, s) : launch_t<64, 1, C, PG>(a, p, km, vm, s);
+    return cudaErrorInvalidValue;
+}
+
+cudaError_t finish(const SharedArgs &a, const SharedPlan &p, int D, const SharedOther &o, float *out, float *lse,
+                   cudaStream_t s) {
+    const unsigned blocks = (unsigned)(((size_t)a.rows * a.Hq + 7) / 8);
+    if (D == 128) shared_merge_kernel<128><<<blocks, 256, 0, s>>>(a, p.nrec, o.out, o.lse, out, lse);
+    else shared_merge_kernel<64><<<blocks, 256, 0, s>>>(a, p.nrec, o.out, o.lse, out, lse);
+    return cudaGetLastError();
+}
+
+SharedArgs common_args(int rows, int Hkv, int Hq, int D, const SharedPlan &p, const uint16_t *q, const int32_t *start,
+                       const int32_t *len, int max_len, float scale, void *workspace) {
+    SharedArgs a{};
+    a.q = q;
+    a.start = start;
+    a.len = len;
+    a.rows = rows;
+    a.Hkv = Hkv;
+    a.Hq = Hq;
+    a.qpk = Hq / Hkv;
+    a.R = rows * a.qpk;
+    a.max_len = max_len;
+    a.nsplit = p.nsplit;
+    a.qscale = scale * 1.44269504088896340736f;
+    a.ws_o = reinterpret_cast<float *>(workspace);
+    a.ws_ml = reinterpret_cast<float2 *>(reinterpret_cast<char *>(workspace) +
+                                         align256(p.nrec * (size_t)rows * Hq * D * sizeof(float)));
+    a.wait_ns = wait_limit_ns();
+    return a;
+}
+
+}  // namespace
+
+size_t shared_ws_bytes(int Hkv, int Hq, int D, int rows, int max_len, bool coded) {
+    return ws_bytes(plan_shared(Hkv, rows * (Hq / Hkv), max_len, coded ? 64 : 128), (size_t)rows * Hq, D);
+}
+
+cudaError_t launch_bf16_shared(const loopvq_bf16_cache &c, int seq, const uint16_t *q, int rows, const int32_t *starts,
+                               const int32_t *lens, int max_len, float scale, const SharedOther &other, float *out,
+                               float *lse, void *workspace, cudaStream_t s) {
+    const SharedPlan p = plan_shared(c.Hkv, rows * (c.Hq / c.Hkv), max_len, 128);
+    SharedArgs a = common_args(rows, c.Hkv, c.Hq, c.D, p, q, starts ? starts + seq : nullptr, lens + seq, max_len, scale,
+                               workspace);
+    cudaError_t e = fault_word_for_current_device(&a.fault);
+    if (e != cudaSuccess) return e;
+    a.head_rows = c.Nmax;
+    const size_t at = (size_t)seq * c.Hkv * c.Nmax * c.D, map_rows = (size_t)c.Hkv * c.Nmax;
+    CUtensorMap km, vm;
+    e = make_map(&km, c.k + at, map_rows, c.D, 128);
+    if (e == cudaSuccess) e = make_map(&vm, c.v + at, map_rows, c.D, 128);
+    if (e == cudaSuccess) e = launch_d<0, false>(c.D, a, p, km, vm, s);
+    if (e != cudaSuccess) return e;
+    return finish(a, p, c.D, other, out, lse, s);
+}
+
+cudaError_t launch_shared(const loopvq_cache &cc, int layer, int t, int seq, const uint16_t *q, int rows,
+                          const int32_t *starts, const int32_t *lens, int max_len, float scale,
+                          const SharedOther &other, float *out, float *lse, void *workspace, cudaStream_t s) {
+    const SharedPlan p = plan_shared(cc.Hkv, rows * (cc.Hq / cc.Hkv), max_len, 64);
+    SharedArgs a = common_args(rows, cc.Hkv, cc.Hq, cc.D, p, q, starts ? starts + seq : nullptr, lens + seq, max_len,
+                               scale, workspace);
+    cudaError_t e = fault_word_for_current_device(&a.fault);
+    if (e != cudaSuccess) return e;
+    a.idx = cc.idx + idx_base(cc, layer, t / cc.Tc, seq, 0);
+    a.idx_head = idx_words_per_bh(cc.Nmax, cc.D, cc.c);
+    a.slk = cc.slices + slice_base(cc, layer, t, 0, 0);
+    a.slv = cc.slices + slice_base(cc, layer, t, 1, 0);
+    a.rope = cc.rope;
+    a.K = cc.K;
+    CUtensorMap none{};
+    const bool pg = ncb_of(cc) > 1;
+    switch (cc.c) {
+        case 4: e = pg ? launch_d<4, true>(cc.D, a, p, none, none, s) : launch_d<4, false>(cc.D, a, p, none, none, s); break;
+        case 8: e = pg ? launch_d<8, true>(cc.D, a, p, none, none, s) : launch_d<8, false>(cc.D, a, p, none, none, s); break;
+        case 16: e = pg ? launch_d<16, true>(cc.D, a, p, none, none, s) : launch_d<16, false>(cc.D, a, p, none, none, s); break;
+        case 32: e = pg ? launch_d<32, true>(cc.D, a, p, none, none, s) : launch_d<32, false>(cc.D, a, p, none, none, s); break;
+        default: return cudaErrorInvalidValue;
+    }
+    if (e != cudaSuccess) return e;
+    return finish(a, p, cc.D, other, out, lse, s);
+}
+
+}  // namespace loopvq

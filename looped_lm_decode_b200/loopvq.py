@@ -24,7 +24,8 @@ EXPORTS = ("loopvq_idx_words", "loopvq_codebook_elems", "loopvq_slice_elems", "l
            "loopvq_dequant_debug", "loopvq_last_error", "loopvq_abi_version",
            "loopvq_decode_attn_noalloc", "loopvq_noalloc_scratch_bytes", "loopvq_decode_attn_range",
            "loopvq_bf16_decode_workspace_bytes", "loopvq_bf16_decode_attn", "loopvq_merge2",
-           "loopvq_bf16_scored_workspace_bytes", "loopvq_bf16_decode_attn_scored",
+           "loopvq_bf16_shared_workspace_bytes", "loopvq_shared_workspace_bytes", "loopvq_bf16_shared_attn",
+           "loopvq_shared_attn", "loopvq_bf16_scored_workspace_bytes", "loopvq_bf16_decode_attn_scored",
            "loopvq_bf16_evict_workspace_bytes", "loopvq_bf16_evict",
            "loopvq_window_slots", "loopvq_window_advance", "loopvq_window_append",
            "loopvq_window_workspace_bytes", "loopvq_window_decode_attn", "loopvq_window_append_decode_attn",
@@ -98,6 +99,14 @@ def lib():
         L.loopvq_bf16_decode_attn.restype = i
         L.loopvq_merge2.argtypes = [vp, vp, vp, vp, i, i, vp, vp, vp]
         L.loopvq_merge2.restype = i
+        L.loopvq_bf16_shared_workspace_bytes.argtypes = [PB, i, i]
+        L.loopvq_bf16_shared_workspace_bytes.restype = sz
+        L.loopvq_shared_workspace_bytes.argtypes = [P, i, i]
+        L.loopvq_shared_workspace_bytes.restype = sz
+        L.loopvq_bf16_shared_attn.argtypes = [PB, i, vp, i, vp, vp, i, f, vp, vp, vp, vp, vp, sz, vp]
+        L.loopvq_bf16_shared_attn.restype = i
+        L.loopvq_shared_attn.argtypes = [P, i, i, i, vp, i, vp, vp, i, f, vp, vp, vp, vp, vp, sz, vp]
+        L.loopvq_shared_attn.restype = i
         L.loopvq_bf16_scored_workspace_bytes.argtypes = [PB, i]
         L.loopvq_bf16_scored_workspace_bytes.restype = sz
         L.loopvq_bf16_decode_attn_scored.argtypes = [PB, vp, vp, vp, i, f, vp, vp, vp, vp, vp, vp, vp, sz, vp]
@@ -357,6 +366,63 @@ def _need_other(other, rows, Hq, D, device):
     _need(other[0], "other out", (rows, Hq, D), _F32, device)
     _need(other[1], "other lse", (rows, Hq), _F32, device)
     return other
+
+
+def bf16_shared_workspace_bytes(cache: Bf16Cache, rows: int, max_len: int) -> int:
+    return lib().loopvq_bf16_shared_workspace_bytes(cache.ref(), rows, max_len)
+
+
+def shared_workspace_bytes(cache: Cache, rows: int, max_len: int) -> int:
+    return lib().loopvq_shared_workspace_bytes(cache.ref(), rows, max_len)
+
+
+def _shared_args(cache, q, starts, lens, other, out, lse, dev):
+    rows = q.shape[0]
+    _need(q, "q", (rows, cache.Hq, cache.D), _Q, dev)
+    _need(lens, "lens", (cache.B,), _I32, dev)
+    if starts is not None:
+        _need(starts, "starts", (cache.B,), _I32, dev)
+    oo, ol = _need_other(other, rows, cache.Hq, cache.D, dev)
+    if out is None:
+        out = torch.empty((rows, cache.Hq, cache.D), dtype=torch.float32, device=dev)
+    if lse is None:
+        lse = torch.empty((rows, cache.Hq), dtype=torch.float32, device=dev)
+    _need(out, "out", (rows, cache.Hq, cache.D), _F32, dev)
+    _need(lse, "lse", (rows, cache.Hq), _F32, dev)
+    return rows, oo, ol, out, lse
+
+
+def bf16_shared_attn(cache: Bf16Cache, seq: int, q: torch.Tensor, lens: torch.Tensor, max_len: int, starts=None,
+                     scale: float = 0.0, other=None, out=None, lse=None, workspace=None, stream=None):
+    """Attention of every query token q[r], bf16 [rows][Hq][D], over the tokens starts[seq] <= n < lens[seq] of one
+    sequence of the cache (the prefix that a batch shares); other: (out, lse) of the same queries over tokens of their
+    own, merged in, or None.  lens, starts int32 [B].  Returns (out fp32 [rows][Hq][D], lse fp32 [rows][Hq])."""
+    dev = _need_current(cache.k.device)
+    rows, oo, ol, out, lse = _shared_args(cache, q, starts, lens, other, out, lse, dev)
+    if rows == 0:
+        return out, lse
+    if workspace is None:
+        workspace = torch.empty(max(bf16_shared_workspace_bytes(cache, rows, max_len), 16), dtype=torch.uint8,
+                                device=dev)
+    _check(lib().loopvq_bf16_shared_attn(cache.ref(), seq, _ptr(q), rows, _ptr(starts), _ptr(lens), max_len, scale,
+                                         _ptr(oo), _ptr(ol), _ptr(out), _ptr(lse), _ptr(workspace),
+                                         workspace.numel() * workspace.element_size(), _stream(stream)))
+    return out, lse
+
+
+def shared_attn(cache: Cache, layer: int, t: int, seq: int, q: torch.Tensor, lens: torch.Tensor, max_len: int,
+                starts=None, scale: float = 0.0, other=None, out=None, lse=None, workspace=None, stream=None):
+    """bf16_shared_attn over loop step t of one sequence of a coded cache."""
+    dev = _need_current(cache.idx.device)
+    rows, oo, ol, out, lse = _shared_args(cache, q, starts, lens, other, out, lse, dev)
+    if rows == 0:
+        return out, lse
+    if workspace is None:
+        workspace = torch.empty(max(shared_workspace_bytes(cache, rows, max_len), 16), dtype=torch.uint8, device=dev)
+    _check(lib().loopvq_shared_attn(cache.ref(), layer, t, seq, _ptr(q), rows, _ptr(starts), _ptr(lens), max_len, scale,
+                                    _ptr(oo), _ptr(ol), _ptr(out), _ptr(lse), _ptr(workspace),
+                                    workspace.numel() * workspace.element_size(), _stream(stream)))
+    return out, lse
 
 
 def bf16_scored_workspace_bytes(cache: Bf16Cache, max_len: int) -> int:
