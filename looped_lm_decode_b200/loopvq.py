@@ -174,13 +174,17 @@ def wait_limit_ns() -> int:
 
 
 def _ptr(t):
-    return None if t is None else C.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 def _stream(stream):
+    """The stream's handle; None: the current stream of the current GPU (read without making a Stream object,
+    which costs 3 microseconds a call)."""
     if stream is None:
+        if torch.cuda.is_initialized():
+            return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
         stream = torch.cuda.current_stream()
-    return C.c_void_p(stream.cuda_stream)
+    return stream.cuda_stream
 
 
 class Cache:
@@ -342,17 +346,40 @@ def merge2(out_a, lse_a, out_b, lse_b, out=None, lse=None, stream=None):
     return out, lse
 
 
-def _need(t: torch.Tensor, name: str, shape, dtypes, device):
+def _need(t: torch.Tensor, name: str, shape: tuple, dtypes: tuple, device):
     """Refuses an array that the kernels would read past or misread."""
-    if t.shape != tuple(shape) or t.dtype not in dtypes or not t.is_contiguous() or t.device != device:
+    if t.shape != shape or t.dtype not in dtypes or not t.is_contiguous() or t.device != device:
         raise LoopVQError(LOOPVQ_ERR_INVALID_ARG, f"{name} must be contiguous {list(shape)} of "
                           f"{' or '.join(str(d).replace('torch.', '') for d in dtypes)} on {device}: got "
                           f"{list(t.shape)} {t.dtype} on {t.device}")
 
 
+def _result(t, name: str, shape: tuple, like: torch.Tensor):
+    """An fp32 output: the caller's, or a new one."""
+    if t is None:
+        return like.new_empty(shape, dtype=torch.float32)
+    _need(t, name, shape, _F32, like.device)
+    return t
+
+
+def _on_stream(stream, *tensors):
+    """Memory made on the current stream and used on another is not reused before that stream is done with it."""
+    if stream is not None:
+        for t in tensors:
+            t.record_stream(stream)
+
+
+def _workspace(workspace, need: int, like: torch.Tensor):
+    if workspace is None:
+        workspace = like.new_empty(max(need, 16), dtype=torch.uint8)
+    elif workspace.device != like.device or not workspace.is_contiguous():
+        raise LoopVQError(LOOPVQ_ERR_INVALID_ARG, f"workspace must be contiguous memory on {like.device}")
+    return workspace, workspace.numel() * workspace.element_size()
+
+
 def _need_current(device):
     """The launch goes to the current GPU: memory of another one, or of the host, is refused."""
-    if device.type != "cuda" or device.index != torch.cuda.current_device():
+    if device.type != "cuda" or device.index != torch._C._cuda_getDevice():
         raise LoopVQError(LOOPVQ_ERR_INVALID_ARG, f"the cache is on {device}, which is not the current GPU")
     return device
 
@@ -377,19 +404,13 @@ def shared_workspace_bytes(cache: Cache, rows: int, max_len: int) -> int:
 
 
 def _shared_args(cache, q, starts, lens, other, out, lse, dev):
-    rows = q.shape[0]
-    _need(q, "q", (rows, cache.Hq, cache.D), _Q, dev)
+    rows, Hq, D = q.shape[0], cache.Hq, cache.D
+    _need(q, "q", (rows, Hq, D), _Q, dev)
     _need(lens, "lens", (cache.B,), _I32, dev)
     if starts is not None:
         _need(starts, "starts", (cache.B,), _I32, dev)
-    oo, ol = _need_other(other, rows, cache.Hq, cache.D, dev)
-    if out is None:
-        out = torch.empty((rows, cache.Hq, cache.D), dtype=torch.float32, device=dev)
-    if lse is None:
-        lse = torch.empty((rows, cache.Hq), dtype=torch.float32, device=dev)
-    _need(out, "out", (rows, cache.Hq, cache.D), _F32, dev)
-    _need(lse, "lse", (rows, cache.Hq), _F32, dev)
-    return rows, oo, ol, out, lse
+    oo, ol = _need_other(other, rows, Hq, D, dev)
+    return rows, oo, ol, _result(out, "out", (rows, Hq, D), q), _result(lse, "lse", (rows, Hq), q)
 
 
 def bf16_shared_attn(cache: Bf16Cache, seq: int, q: torch.Tensor, lens: torch.Tensor, max_len: int, starts=None,
@@ -401,12 +422,12 @@ def bf16_shared_attn(cache: Bf16Cache, seq: int, q: torch.Tensor, lens: torch.Te
     rows, oo, ol, out, lse = _shared_args(cache, q, starts, lens, other, out, lse, dev)
     if rows == 0:
         return out, lse
-    if workspace is None:
-        workspace = torch.empty(max(bf16_shared_workspace_bytes(cache, rows, max_len), 16), dtype=torch.uint8,
-                                device=dev)
-    _check(lib().loopvq_bf16_shared_attn(cache.ref(), seq, _ptr(q), rows, _ptr(starts), _ptr(lens), max_len, scale,
-                                         _ptr(oo), _ptr(ol), _ptr(out), _ptr(lse), _ptr(workspace),
-                                         workspace.numel() * workspace.element_size(), _stream(stream)))
+    L, ref = lib(), cache.ref()
+    workspace, n = _workspace(workspace, L.loopvq_bf16_shared_workspace_bytes(ref, rows, max_len), q)
+    _check(L.loopvq_bf16_shared_attn(ref, seq, q.data_ptr(), rows, _ptr(starts), lens.data_ptr(), max_len, scale,
+                                     _ptr(oo), _ptr(ol), out.data_ptr(), lse.data_ptr(), workspace.data_ptr(), n,
+                                     _stream(stream)))
+    _on_stream(stream, out, lse, workspace)
     return out, lse
 
 
@@ -417,11 +438,12 @@ def shared_attn(cache: Cache, layer: int, t: int, seq: int, q: torch.Tensor, len
     rows, oo, ol, out, lse = _shared_args(cache, q, starts, lens, other, out, lse, dev)
     if rows == 0:
         return out, lse
-    if workspace is None:
-        workspace = torch.empty(max(shared_workspace_bytes(cache, rows, max_len), 16), dtype=torch.uint8, device=dev)
-    _check(lib().loopvq_shared_attn(cache.ref(), layer, t, seq, _ptr(q), rows, _ptr(starts), _ptr(lens), max_len, scale,
-                                    _ptr(oo), _ptr(ol), _ptr(out), _ptr(lse), _ptr(workspace),
-                                    workspace.numel() * workspace.element_size(), _stream(stream)))
+    L, ref = lib(), cache.ref()
+    workspace, n = _workspace(workspace, L.loopvq_shared_workspace_bytes(ref, rows, max_len), q)
+    _check(L.loopvq_shared_attn(ref, layer, t, seq, q.data_ptr(), rows, _ptr(starts), lens.data_ptr(), max_len, scale,
+                                _ptr(oo), _ptr(ol), out.data_ptr(), lse.data_ptr(), workspace.data_ptr(), n,
+                                _stream(stream)))
+    _on_stream(stream, out, lse, workspace)
     return out, lse
 
 
@@ -449,18 +471,13 @@ def bf16_decode_attn_scored(cache: Bf16Cache, q: torch.Tensor, lens: torch.Tenso
         if t is not None:
             _need(t, name, (B, cache.Hkv, cache.Nmax), _F32, dev)
     oo, ol = _need_other(other, B, Hq, D, dev)
-    if out is None:
-        out = torch.empty((B, Hq, D), dtype=torch.float32, device=dev)
-    if lse is None:
-        lse = torch.empty((B, Hq), dtype=torch.float32, device=dev)
-    _need(out, "out", (B, Hq, D), _F32, dev)
-    _need(lse, "lse", (B, Hq), _F32, dev)
-    if workspace is None:
-        workspace = torch.empty(max(bf16_scored_workspace_bytes(cache, max_len), 16), dtype=torch.uint8, device=dev)
-    _check(lib().loopvq_bf16_decode_attn_scored(cache.ref(), _ptr(q), _ptr(starts), _ptr(lens), max_len, scale,
-                                                _ptr(oo), _ptr(ol), _ptr(score), _ptr(score_out), _ptr(out),
-                                                _ptr(lse), _ptr(workspace),
-                                                workspace.numel() * workspace.element_size(), _stream(stream)))
+    out, lse = _result(out, "out", (B, Hq, D), q), _result(lse, "lse", (B, Hq), q)
+    L, ref = lib(), cache.ref()
+    workspace, n = _workspace(workspace, L.loopvq_bf16_scored_workspace_bytes(ref, max_len), q)
+    _check(L.loopvq_bf16_decode_attn_scored(ref, q.data_ptr(), _ptr(starts), lens.data_ptr(), max_len, scale, _ptr(oo),
+                                            _ptr(ol), _ptr(score), score_out.data_ptr(), out.data_ptr(),
+                                            lse.data_ptr(), workspace.data_ptr(), n, _stream(stream)))
+    _on_stream(stream, out, lse, workspace)
     return out, lse, score_out
 
 
@@ -479,17 +496,18 @@ def bf16_evict(cache: Bf16Cache, score: torch.Tensor, pos: torch.Tensor, lens: t
     score_out = score if score_out is None else score_out
     pos_out = pos if pos_out is None else pos_out
     lens_out = lens if lens_out is None else lens_out
-    for t, name, shape, dt in ((score, "score", (B, H, N), _F32), (pos, "pos", (B, H, N), _I32),
-                               (lens, "lens", (B,), _I32), (next_pos, "next_pos", (B,), _I32),
-                               (score_out, "score_out", (B, H, N), _F32), (pos_out, "pos_out", (B, H, N), _I32),
-                               (lens_out, "lens_out", (B,), _I32)):
-        _need(t, name, shape, dt, dev)
-    if workspace is None:
-        workspace = torch.empty(max(bf16_evict_workspace_bytes(cache, max_len, budget), 16), dtype=torch.uint8,
-                                device=dev)
-    _check(lib().loopvq_bf16_evict(cache.ref(), _ptr(score), _ptr(pos), _ptr(lens), _ptr(next_pos), max_len, budget,
-                                   n_sink, n_recent, _ptr(score_out), _ptr(pos_out), _ptr(lens_out), _ptr(workspace),
-                                   workspace.numel() * workspace.element_size(), _stream(stream)))
+    for t, name in ((score, "score"), (score_out, "score_out")):
+        _need(t, name, (B, H, N), _F32, dev)
+    for t, name in ((pos, "pos"), (pos_out, "pos_out")):
+        _need(t, name, (B, H, N), _I32, dev)
+    for t, name in ((lens, "lens"), (next_pos, "next_pos"), (lens_out, "lens_out")):
+        _need(t, name, (B,), _I32, dev)
+    L, ref = lib(), cache.ref()
+    workspace, n = _workspace(workspace, L.loopvq_bf16_evict_workspace_bytes(ref, max_len, budget), lens)
+    _check(L.loopvq_bf16_evict(ref, score.data_ptr(), pos.data_ptr(), lens.data_ptr(), next_pos.data_ptr(), max_len,
+                               budget, n_sink, n_recent, score_out.data_ptr(), pos_out.data_ptr(),
+                               lens_out.data_ptr(), workspace.data_ptr(), n, _stream(stream)))
+    _on_stream(stream, workspace)
     return score_out, pos_out, lens_out
 
 
