@@ -245,7 +245,7 @@ size_t loopvq_shared_workspace_bytes(const loopvq_cache *cache, int rows, int ma
  * scale      <= 0 selects 1/sqrt(D).
  * other_out  fp32 [rows][Hq][D] and other_lse fp32 [rows][Hq]: the other part,
  *            or both NULL; a row with other_lse = -inf has no other tokens.  out
- *            may be other_out and lse may be other_lse.
+ *            may be other_out; lse may not overlap other_lse.
  * out        fp32 [rows][Hq][D]; lse fp32 [rows][Hq], may be NULL.  No tokens at
  *            all: zeros and -inf.
  * workspace  of at least loopvq_bf16_shared_workspace_bytes(cache, rows, max_len)

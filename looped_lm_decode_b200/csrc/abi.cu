@@ -298,7 +298,8 @@ static loopvq_status check_shared(int B, int Hkv, int Hq, int D, int Nmax, int s
     const size_t n = (size_t)rows * Hq;
     if (other_out) {
         LQ_TRY(check_same_or_apart(other_out, out, n * D * sizeof(float), "out"));
-        if (lse) LQ_TRY(check_same_or_apart(other_lse, lse, n * sizeof(float), "lse"));
+        if (lse && overlaps(lse, n * sizeof(float), other_lse, n * sizeof(float)))
+            return fail(LOOPVQ_ERR_INVALID_ARG, "lse overlaps other_lse");
     }
     return LOOPVQ_OK;
 }

@@ -57,6 +57,27 @@ unsigned long long wait_limit_ns();
 // graph capture.
 cudaError_t ensure_dynamic_smem(const void *kern, size_t bytes);
 
+// Programmatic dependent launch: a kernel launched by launch_pdl may be set up while the kernel before it in the
+// stream still runs; grid_wait() holds it until that kernel is done and its writes are visible, so it comes before the
+// first read or write of global memory.  grid_trigger() in a kernel lets the next one's set-up begin.
+__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void grid_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+template <typename... P, typename... A>
+inline cudaError_t launch_pdl(void (*kern)(P...), dim3 grid, unsigned threads, size_t smem, cudaStream_t s, const A &...args) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, P(args)...);
+}
+
 // Launchers (host); each returns a cudaError_t from the launch.
 cudaError_t launch_prepare(const loopvq_cache &cc, cudaStream_t s);
 cudaError_t launch_encode(const loopvq_cache &cc, int layer, int block, const void *xk, const void *xv,

@@ -7,8 +7,8 @@
 //
 // One CTA per (token split, KV head, up to 2 x 128 query rows).  Its warps:
 //   0-3, 4-7  softmax of stream 0 and stream 1: thread = query row = tensor-memory lane
-//   8         issues every product (one thread)
-//   9 ..      bf16 cache: one thread copies K and V tiles by TMA; coded cache: eight warps rebuild them
+//   8, 9      bf16 cache: one thread issues every product, one copies K and V tiles by TMA
+//   8-15, 16  coded cache: eight warps rebuild K and V tiles, one thread issues every product
 // A step is one product pair S = Q K^T, O += P V of 128 rows by one tile of tokens.  Steps alternate between two
 // streams, each with its own S, O, maximum and sum, so that the products of one stream run under the softmax of
 // the other: with up to 128 rows the streams take the tiles in turn (and give two partial results), with more
@@ -18,7 +18,7 @@
 // remainder of the first rounding in the second, 2^-18 of P at most), two products into the same accumulator; a
 // rebuilt, rotated key is split the same way.  bf16 queries, keys and values are exact.
 //
-// P overwrites S in place, 32 score columns becoming 16 + 16 columns of packed pairs.  The running maximum moves
+// P overwrites S in place, 16 score columns becoming 8 + 8 columns of packed pairs (one product's tokens).  The running maximum moves
 // only when a tile passes it by 2^8 (any reference is exact; it bounds P), so O is rarely rescaled.
 #include <cuda.h>
 
@@ -35,9 +35,10 @@ struct SharedArgs {
     const uint16_t *q;       // [rows][Hq][D]
     const int32_t *start;    // of the sequence, or null
     const int32_t *len;
-    float *ws_o;             // [nrec][rows * Hq][D], row = h * R + r
-    float2 *ws_ml;           // [nrec][rows * Hq]
+    float *ws_o;             // [nsplit][Hkv][D / 4][R][4]: a warp's 32 rows write 512 bytes in a run
+    float2 *ws_ml;           // [nsplit][Hkv][R]: maximum reference (log2 units), sum
     int rows, Hkv, Hq, R, qpk, max_len, nsplit;
+    int qshift;              // log2 of qpk
     float qscale;            // scale * log2(e)
     unsigned int *fault;
     unsigned long long wait_ns;
@@ -51,8 +52,12 @@ struct SharedArgs {
     int K;
 };
 
-// Shared-memory plan (bytes from a 1024-byte boundary).  NT tokens per tile, KP bf16 parts per key.
-template <int D, int MB, int C>
+// Shared-memory and tensor-memory plan.  NT tokens per tile, KP bf16 parts per key.
+// bf16 cache: the queries lie in shared memory (S and O fill the tensor memory at 128-token tiles).
+// Coded cache: 64-token tiles leave tensor memory for the queries, so the products read only the tiles from shared
+// memory, whose bandwidth they share with the rebuilding; and each 8-bit code's slice entry fills a row of 128 bytes
+// with copies of itself, one for every lane that a wavefront serves, so that gathers meet no bank conflict.
+template <int D, int MB, int C, bool PG>
 struct Plan {
     static constexpr bool coded = C != 0;
     static constexpr int NT = coded ? 64 : 128;
@@ -60,23 +65,29 @@ struct Plan {
     static constexpr int kPanel = NT * 128;                          // 64 channels of a tile
     static constexpr int kTile = (D / 64) * kPanel;
     static constexpr int kStage = (KP + 1) * kTile;                  // K parts, then V
-    static constexpr int kQ = (D / 64) * 128 * 128;                  // one row block
-    static constexpr int ST = D == 64 ? (coded ? 4 : 4) : (MB == 1 ? 3 : 2);
-    static constexpr int kTable = coded ? 256 * C * 2 : 0;           // one slice; K then V
+    static constexpr int kQ = coded ? 0 : (D / 64) * 128 * 128;      // one row block
+    static constexpr int ST = D == 64 ? 4 : (coded || MB == 1 ? 3 : 2);
+    static constexpr int kTable = coded && !PG ? 256 * 128 : 0;      // K slice, then V slice
     static constexpr int offQ = 0;
     static constexpr int offStage = MB * kQ;
     static constexpr int offTable = offStage + ST * kStage;
-    static constexpr int offBar = offTable + 2 * kTable;
+    static constexpr int offTurn = offTable + 2 * kTable;            // rope row 64: the turn from tile to tile
+    static constexpr int offBar = offTurn + (coded ? D * 4 : 0);
     static constexpr int kBars = 4 * ST + 7;
     static constexpr int offTmem = offBar + kBars * 8;
     static constexpr int kUsed = offTmem + 16;
     static constexpr int kAlloc = kUsed + 1024;
     static constexpr int kThreads = coded ? 9 * 32 + 256 : 320;
+    static constexpr int kMma = coded ? 16 : 8;                      // warps: products;
+    static constexpr int kCopy = coded ? 16 : 9;                     // copies (and the barriers' set-up);
+    static constexpr int kRebuild = 8;                               // the first of the rebuilding ones
+    static constexpr int colS = coded ? 64 : 128;                    // S of stream w at w * colS
+    static constexpr int colQ = coded ? 128 : 0;                     // coded: Q of row block w at 128 + 64 w
     static_assert(kAlloc <= 232448, "shared memory");
-    static_assert(kAlloc > 116 * 1024 || D == 64, "one CTA per SM: tensor memory is allocated whole");
+    static_assert(ST * kStage >= 128 * D * 4, "the streams' exchange reuses the tiles");
 };
 
-constexpr int kTmemCols = 512;                                       // S0 S1 at 0, 128; O0 O1 at 256, 384
+constexpr int kTmemCols = 512;                                       // O of stream w at 256 + 128 w
 
 // Rows n (128 bytes of 64 channels) of a panel: 16-byte chunk j lies at chunk j ^ (n & 7).
 __device__ __forceinline__ uint32_t sw128(int n, int chunk) { return (uint32_t)n * 128u + ((uint32_t)(chunk ^ (n & 7)) << 4); }
@@ -95,33 +106,24 @@ struct RowSoftmax {
     // odone: barrier (parity) of the stream's previous O += P V.
     __device__ __forceinline__ bool tile(uint32_t ts, uint32_t to, int lo, int hi, float qs, bool first, uint32_t odone,
                                          uint32_t odone_parity, uint64_t limit, volatile int *dead) {
-        // NT = 64 shares the register file with the rebuilding warps (96 a thread): 32 scores at a time, read from
-        // tensor memory once for the maximum and once for the exponentials; NT = 128 keeps them
-        constexpr bool keep = NT == 128;
-        uint32_t v[keep ? NT / 32 : 1][32];
+        // 32 scores at a time, read from tensor memory once for the maximum and once for the exponentials: a tile's
+        // scores in registers spill, and loops keep the code small enough for the instruction cache (a call of few
+        // tiles spent most of its time fetching the unrolled form: 3400 clocks for its first tile)
         const bool edge = lo > 0 || hi < NT;
-        auto mask = [&](uint32_t (&x)[32], int c) {
+        auto load = [&](uint32_t (&x)[32], int c) {
+            tc::tmem_ld32(ts + c, x);
+            tc::tmem_wait_ld(x);
             if (edge) {
 #pragma unroll
                 for (int k = 0; k < 32; ++k)
-                    if (c * 32 + k < lo || c * 32 + k >= hi) x[k] = 0xff800000u;
+                    if (c + k < lo || c + k >= hi) x[k] = 0xff800000u;
             }
         };
-        if constexpr (keep) {
-#pragma unroll
-            for (int c = 0; c < NT / 32; ++c) tc::tmem_ld32(ts + c * 32, v[c]);
-#pragma unroll
-            for (int c = 0; c < NT / 32; ++c) tc::tmem_wait_ld(v[c]);
-        }
         float a0 = -CUDART_INF_F, a1 = a0, a2 = a0, a3 = a0;
-#pragma unroll
-        for (int c = 0; c < NT / 32; ++c) {
-            uint32_t (&x)[32] = v[keep ? c : 0];
-            if constexpr (!keep) {
-                tc::tmem_ld32(ts + c * 32, x);
-                tc::tmem_wait_ld(x);
-            }
-            mask(x, c);
+#pragma unroll 1
+        for (int c = 0; c < NT; c += 32) {
+            uint32_t x[32];
+            load(x, c);
 #pragma unroll
             for (int k = 0; k < 32; k += 4) {
                 a0 = fmaxf(a0, __uint_as_float(x[k]));
@@ -153,26 +155,25 @@ struct RowSoftmax {
         }
         const float nm = m == -CUDART_INF_F ? 0.f : -m;
         float s0 = 0.f, s1 = 0.f;
+#pragma unroll 1
+        for (int c = 0; c < NT; c += 32) {
+            uint32_t x[32];
+            load(x, c);
 #pragma unroll
-        for (int c = 0; c < NT / 32; ++c) {
-            uint32_t (&x)[32] = v[keep ? c : 0];
-            if constexpr (!keep) {
-                tc::tmem_ld32(ts + c * 32, x);
-                tc::tmem_wait_ld(x);
-                mask(x, c);
-            }
-            uint32_t w[32];
+            for (int half = 0; half < 2; ++half) {
+                uint32_t w[16];
 #pragma unroll
-            for (int k = 0; k < 16; ++k) {
-                const float p0 = ex2(fmaf(__uint_as_float(x[2 * k]), qs, nm));
-                const float p1 = ex2(fmaf(__uint_as_float(x[2 * k + 1]), qs, nm));
-                s0 += p0;
-                s1 += p1;
-                const uint32_t hi2 = cvt_bf16x2(p1, p0);
-                w[k] = hi2;
-                w[16 + k] = cvt_bf16x2(p1 - bf16hi(hi2), p0 - bf16lo(hi2));
+                for (int k = 0; k < 8; ++k) {
+                    const float p0 = ex2(fmaf(__uint_as_float(x[half * 16 + 2 * k]), qs, nm));
+                    const float p1 = ex2(fmaf(__uint_as_float(x[half * 16 + 2 * k + 1]), qs, nm));
+                    s0 += p0;
+                    s1 += p1;
+                    const uint32_t hi2 = cvt_bf16x2(p1, p0);
+                    w[k] = hi2;
+                    w[8 + k] = cvt_bf16x2(p1 - bf16hi(hi2), p0 - bf16lo(hi2));
+                }
+                tc::tmem_st16(ts + c + half * 16, w);
             }
-            tc::tmem_st32(ts + c * 32, w);
         }
         l += s0 + s1;
         tc::tmem_wait_st();
@@ -184,10 +185,10 @@ struct RowSoftmax {
 // a coded one; PG: one codebook per channel group, whose slices (128 bytes per entry and more) do not fit beside
 // the tiles and are gathered from L2.
 template <int D, int MB, int C, bool PG>
-__global__ void __launch_bounds__(Plan<D, MB, C>::kThreads, 1)
+__global__ void __launch_bounds__(Plan<D, MB, C, PG>::kThreads, 1)
     shared_attn_kernel(const SharedArgs a, const __grid_constant__ CUtensorMap kmap,
                        const __grid_constant__ CUtensorMap vmap) {
-    using P = Plan<D, MB, PG ? 4 : C>;
+    using P = Plan<D, MB, C, PG>;
     constexpr bool coded = C != 0;
     constexpr int NT = P::NT, KP = P::KP, ST = P::ST, NPAN = D / 64;
 
@@ -210,6 +211,8 @@ __global__ void __launch_bounds__(Plan<D, MB, C>::kThreads, 1)
     const int split = blockIdx.x, h = blockIdx.y;
     const int r0 = blockIdx.z * (MB * 128);                          // first query row of this CTA
 
+    grid_trigger();
+    grid_wait();
     const int len = min(max(__ldg(a.len), 0), a.max_len);
     const int st = a.start ? min(max(__ldg(a.start), 0), len) : 0;
     const int tok0 = coded ? (st & ~3) : st;                         // index words come in tiles of 4 tokens
@@ -218,15 +221,10 @@ __global__ void __launch_bounds__(Plan<D, MB, C>::kThreads, 1)
     const int ntiles = (int)((long long)(split + 1) * tiles_all / a.nsplit) - t_first;
     const int tok_first = tok0 + t_first * NT;
     const int nsteps = ntiles * MB;                                  // step i: stream i & 1
-    const size_t RT = (size_t)a.rows * a.Hq;
-    // record of stream w: two row blocks share one record index, alternating tiles make two
-    auto record = [&](int w) { return MB == 2 ? (size_t)split : (size_t)split * 2 + w; };
+    const size_t rec = ((size_t)split * a.Hkv + h) * a.R;            // this split's records of the head
 
     if (ntiles == 0) {                                               // nothing in this split
-        for (int r = r0 + tid; r < min(r0 + MB * 128, a.R); r += P::kThreads) {
-            a.ws_ml[record(0) * RT + (size_t)h * a.R + r] = f2(-CUDART_INF_F, 0.f);
-            if (MB == 1) a.ws_ml[record(1) * RT + (size_t)h * a.R + r] = f2(-CUDART_INF_F, 0.f);
-        }
+        for (int r = r0 + tid; r < min(r0 + MB * 128, a.R); r += P::kThreads) a.ws_ml[rec + r] = f2(-CUDART_INF_F, 0.f);
         return;
     }
 
@@ -248,7 +246,7 @@ __global__ void __launch_bounds__(Plan<D, MB, C>::kThreads, 1)
                             h * a.head_rows + tok_first + t * NT, vfull(s));
     };
     int issued = 0;                                                  // tiles copied by the producer thread
-    if (warp == 9 && lane == 0) {
+    if (warp == P::kCopy && lane == 0) {
         for (int s = 0; s < ST; ++s) {
             tc::mbar_init(kfull(s), coded ? 8 : 1);
             tc::mbar_init(vfull(s), 1);
@@ -270,40 +268,87 @@ __global__ void __launch_bounds__(Plan<D, MB, C>::kThreads, 1)
             }
         }
     }
-    if (warp == 8) {
+    if (warp == P::kMma) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(tc::smem_u32(tmem_slot)),
                      "r"(kTmemCols));
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
     }
-    for (int it = tid; it < MB * 128 * (D / 8); it += P::kThreads) { // 16-byte chunks of the query rows
-        const int r = it / (D / 8), ch = it % (D / 8);
-        uint4 v = make_uint4(0, 0, 0, 0);
-        if (r0 + r < a.R) {
-            const int row = (r0 + r) / a.qpk, g = (r0 + r) % a.qpk;
-            v = *reinterpret_cast<const uint4 *>(a.q + ((size_t)row * a.Hq + h * a.qpk + g) * D + ch * 8);
+    // queries: rows of warps that have a real one (the others' lanes are never read), padding rows zero
+    auto q_row = [&](int r) {
+        return a.q + ((size_t)((r0 + r) >> a.qshift) * a.Hq + h * a.qpk + ((r0 + r) & (a.qpk - 1))) * D;
+    };
+    uint4 qv[coded ? D / 8 : 1];                                     // coded: this thread's query row
+    const int q_rows = min(MB * 128, (a.R - r0 + 31) & ~31);
+    if constexpr (!coded) {
+        for (int it = tid; it < q_rows * (D / 8); it += P::kThreads) {
+            const int r = it / (D / 8), ch = it % (D / 8);
+            const uint32_t dst = sQ + (r / 128) * P::kQ + (ch / 8) * (128 * 128) + sw128(r % 128, ch % 8);
+            const bool real = r0 + r < a.R;
+            cp_async16_zfill(dst, real ? q_row(r) + ch * 8 : a.q, real);
         }
-        sts128(sQ + (r / 128) * P::kQ + (ch / 8) * (128 * 128) + sw128(r % 128, ch % 8), v);
+        cp_async_commit();
+    } else {
+        if (tid < q_rows) {
+#pragma unroll
+            for (int c = 0; c < D / 8; ++c)
+                qv[c] = r0 + tid < a.R ? *reinterpret_cast<const uint4 *>(q_row(tid) + c * 8) : make_uint4(0, 0, 0, 0);
+        }
+        for (int i = tid; i < D; i += P::kThreads)                   // used from the second tile on: row 64 is there
+            reinterpret_cast<float *>(smem + P::offTurn)[i] = ntiles > 1 ? a.rope[(size_t)64 * D + i] : 0.f;
     }
     if constexpr (coded && !PG) {
         const uint16_t *src[2] = {a.slk + (size_t)h * a.K * C, a.slv + (size_t)h * a.K * C};
-        for (int it = tid; it < 2 * 256 * C / 4; it += P::kThreads) {
-            const int kv = it / (256 * C / 4), e = it % (256 * C / 4) * 4;
-            uint2 v = make_uint2(0, 0);                              // entries past K: zeros
-            if (e / C < a.K) v = *reinterpret_cast<const uint2 *>(src[kv] + e);
-            *reinterpret_cast<uint2 *>(smem + P::offTable + kv * P::kTable + e * 2) = v;
+#pragma unroll 4
+        for (int it = tid; it < 2 * 256 * 8; it += P::kThreads) {    // 16-byte pieces of the copies' rows
+            const int kv = it / 2048, e = it / 8 % 256, slot = it % 8;
+            uint4 v = make_uint4(0, 0, 0, 0);                        // entries past K: zeros
+            if (e < a.K) {
+                if constexpr (C == 4) {
+                    const uint2 x = *reinterpret_cast<const uint2 *>(src[kv] + e * 4);
+                    v = make_uint4(x.x, x.y, x.x, x.y);
+                } else {
+                    v = *reinterpret_cast<const uint4 *>(src[kv] + e * C + slot % (C / 8) * 8);
+                }
+            }
+            *reinterpret_cast<uint4 *>(smem + P::offTable + kv * P::kTable + e * 128 + slot * 16) = v;
         }
     }
+    cp_async_wait<0>();
     tc::fence_async_smem();
     tc::tc_fence_before();
     __syncthreads();
     tc::tc_fence_after();
     const uint32_t tmem = *tmem_slot;
+    if constexpr (coded) {
+        if (warp * 32 < q_rows) {                                    // the queries into tensor memory
+            uint32_t x[32];
+#pragma unroll
+            for (int c = 0; c < D / 2; c += 32) {
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    const uint4 v = qv[c / 4 + k];
+                    x[4 * k] = v.x;
+                    x[4 * k + 1] = v.y;
+                    x[4 * k + 2] = v.z;
+                    x[4 * k + 3] = v.w;
+                }
+                tc::tmem_st32(tmem + ((uint32_t)((warp & 3) * 32) << 16) + P::colQ + (warp >> 2) * 64 + c, x);
+            }
+            tc::tmem_wait_st();
+        }
+        tc::tc_fence_before();
+        __syncthreads();
+        tc::tc_fence_after();
+    }
 
     if (warp < 8) {
         // ---- softmax of stream w: 128 threads, one query row each
+        // 17 warps are launched with 96 registers each; the rebuilding warps' 32 running cosines and sines need more
+        // and the softmax less: 256 x 80 + 256 x 112 + 32 x 96 = 544 x 96
+        if constexpr (coded) asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
         const int w = warp >> 2, row = tid & 127;
         const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
-        const uint32_t ts = tmem + lane_base + w * 128, to = tmem + lane_base + 256 + w * 128;
+        const uint32_t ts = tmem + lane_base + w * P::colS, to = tmem + lane_base + 256 + w * 128;
         const int rq = r0 + (MB == 2 ? w * 128 : 0) + row;           // query row of this thread
         const bool any = __any_sync(0xffffffffu, rq < a.R);          // warps of padding only keep step
         RowSoftmax<D, NT> sm{-CUDART_INF_F, 0.f};
@@ -326,26 +371,75 @@ __global__ void __launch_bounds__(Plan<D, MB, C>::kThreads, 1)
             ok = __all_sync(0xffffffffu, tc::mbar_wait_or_dead(odone(w), (j - 1) & 1, a.wait_ns, dead));
             tc::tc_fence_after();
         }
-        if (any) {
-            const size_t rec = record(w) * RT + (size_t)h * a.R + rq;
-            if (rq < a.R)
-                a.ws_ml[rec] = !ok ? f2(0.f, CUDART_NAN_F) : j > 0 ? f2(sm.m, sm.l) : f2(-CUDART_INF_F, 0.f);
-            if (ok && j > 0) {
+        // with two streams of one row block, stream 1 hands its part to stream 0 through the tiles' memory, free by
+        // now (every product of both streams is done once both have waited): 16 bytes of 32 rows in a run
+        float c0 = 1.f, c1 = 0.f;
+        float4 *ex = reinterpret_cast<float4 *>(smem + P::offStage);
+        if constexpr (MB == 1) {
+            float *mls = reinterpret_cast<float *>(smem + P::offStage);   // first the rows' (m, l)
+            asm volatile("bar.sync 1, 256;" ::: "memory");
+            if (w == 1) {
+                mls[row] = !ok ? 0.f : j > 0 ? sm.m : -CUDART_INF_F;
+                mls[128 + row] = !ok ? CUDART_NAN_F : j > 0 ? sm.l : 0.f;
+            }
+            asm volatile("bar.sync 1, 256;" ::: "memory");
+            if (w == 0) {
+                const float m1 = mls[row], l1 = mls[128 + row];
+                if (j == 0) sm.m = -CUDART_INF_F;
+                const float top = fmaxf(sm.m, m1);
+                c0 = top == -CUDART_INF_F ? 0.f : ex2(sm.m - top);
+                c1 = top == -CUDART_INF_F ? 0.f : ex2(m1 - top);
+                sm.l = sm.l * c0 + l1 * c1;
+                sm.m = top;
+            }
+            asm volatile("bar.sync 1, 256;" ::: "memory");
+            if (w == 1 && any) {
 #pragma unroll 1
                 for (int c = 0; c < D; c += 32) {
                     uint32_t o[32];
-                    tc::tmem_ld32(to + c, o);
-                    tc::tmem_wait_ld(o);
-                    if (rq < a.R) {
-                        uint4 *dst = reinterpret_cast<uint4 *>(a.ws_o + rec * D + c);
+                    if (j > 0) {
+                        tc::tmem_ld32(to + c, o);
+                        tc::tmem_wait_ld(o);
+                    } else {
 #pragma unroll
-                        for (int k = 0; k < 8; ++k) dst[k] = make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+                        for (int k = 0; k < 32; ++k) o[k] = 0u;
+                    }
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        ex[(c / 4 + k) * 128 + row] =
+                            make_float4(__uint_as_float(o[4 * k]), __uint_as_float(o[4 * k + 1]),
+                                        __uint_as_float(o[4 * k + 2]), __uint_as_float(o[4 * k + 3]));
+                }
+            }
+            asm volatile("bar.sync 1, 256;" ::: "memory");
+        }
+        if (any && (MB == 2 || w == 0)) {
+            if (rq < a.R) a.ws_ml[rec + rq] = ok ? f2(sm.m, sm.l) : f2(0.f, CUDART_NAN_F);
+#pragma unroll 1
+            for (int c = 0; c < D; c += 32) {
+                uint32_t o[32];
+                tc::tmem_ld32(to + c, o);
+                tc::tmem_wait_ld(o);
+                if (rq < a.R) {
+                    float4 *dst = reinterpret_cast<float4 *>(a.ws_o) + (rec / a.R * (D / 4) + c / 4) * a.R + rq;
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        float4 x = make_float4(__uint_as_float(o[4 * k]), __uint_as_float(o[4 * k + 1]),
+                                               __uint_as_float(o[4 * k + 2]), __uint_as_float(o[4 * k + 3]));
+                        if constexpr (MB == 1) {
+                            const float4 y = ex[(c / 4 + k) * 128 + row];
+                            x.x = x.x * c0 + y.x * c1;
+                            x.y = x.y * c0 + y.y * c1;
+                            x.z = x.z * c0 + y.z * c1;
+                            x.w = x.w * c0 + y.w * c1;
+                        }
+                        dst[(size_t)k * a.R] = x;
                     }
                 }
             }
         }
         tc::tc_fence_before();
-    } else if (warp == 8) {
+    } else if (warp == P::kMma) {
         // ---- products
         constexpr uint32_t id_qk = tc::idesc_bf16(128, NT);
         constexpr uint32_t id_pv = tc::idesc_bf16(128, D) | (1u << 16);        // B: channels contiguous
@@ -359,15 +453,23 @@ __global__ void __launch_bounds__(Plan<D, MB, C>::kThreads, 1)
             if (!wait(kfull(s), (t / ST) & 1)) return;
             tc::tc_fence_after();
             if (lane == 0) {
-                const uint32_t qb = sQ + (MB == 2 ? (i & 1) * P::kQ : 0), kb = sStage + s * P::kStage;
+                const uint32_t kb = sStage + s * P::kStage, sd = tmem + (i & 1) * P::colS;
 #pragma unroll
                 for (int part = 0; part < KP; ++part)
 #pragma unroll
-                    for (int k = 0; k < D / 16; ++k)                 // 16 channels per product: 32 bytes of a row
-                        tc::mma_bf16(tmem + (i & 1) * 128,
-                                     tc::smem_desc_sw128(qb + (k / 4) * (128 * 128) + (k % 4) * 32, 16, 1024),
-                                     tc::smem_desc_sw128(kb + part * P::kTile + (k / 4) * P::kPanel + (k % 4) * 32, 16, 1024),
-                                     id_qk, part + k > 0);
+                    for (int k = 0; k < D / 16; ++k) {               // 16 channels per product: 32 bytes of a row
+                        const uint64_t kd = tc::smem_desc_sw128(
+                            kb + part * P::kTile + (k / 4) * P::kPanel + (k % 4) * 32, 16, 1024);
+                        if constexpr (coded) {
+                            tc::mma_bf16_ta(sd, tmem + P::colQ + (MB == 2 ? (i & 1) * 64 : 0) + k * 8, kd, id_qk,
+                                            part + k > 0);
+                        } else {
+                            tc::mma_bf16(sd,
+                                         tc::smem_desc_sw128(sQ + (MB == 2 ? (i & 1) * P::kQ : 0) +
+                                                             (k / 4) * (128 * 128) + (k % 4) * 32, 16, 1024),
+                                         kd, id_qk, part + k > 0);
+                        }
+                    }
                 if (!coded && (MB == 1 || (i & 1)) && t + ST < ntiles) tc::mma_commit(kempty(s));
                 tc::mma_commit(sfull(i & 1));
             }
@@ -394,12 +496,12 @@ __global__ void __launch_bounds__(Plan<D, MB, C>::kThreads, 1)
             if (!wait(pfull(w), (i >> 1) & 1)) break;
             tc::tc_fence_after();
             if (lane == 0) {
-                const uint32_t od = tmem + 256 + w * 128, pa = tmem + w * 128;
+                const uint32_t od = tmem + 256 + w * 128, pa = tmem + w * P::colS;
 #pragma unroll
                 for (int part = 0; part < 2; ++part)
 #pragma unroll
                     for (int k = 0; k < NT / 16; ++k)                // 16 tokens per product: 8 packed columns
-                        tc::mma_bf16_ta(od, pa + (k / 2) * 32 + part * 16 + (k % 2) * 8,
+                        tc::mma_bf16_ta(od, pa + k * 16 + part * 8,
                                         tc::smem_desc_sw128(vb + k * 2048, P::kPanel, 1024), id_pv,
                                         i > 1 || part + k > 0);
                 if ((MB == 1 || w == 1) && t + ST < ntiles) tc::mma_commit(vempty(s));
@@ -429,14 +531,26 @@ __global__ void __launch_bounds__(Plan<D, MB, C>::kThreads, 1)
         }
     } else {
         // ---- rebuilding: a warp takes 8 tokens of the tile, a lane one token and one piece of 8 + 8 channels
-        // (a RoPE pair each) at a time
+        // (8 RoPE pairs) at a time.  The 8 lanes of a 16-byte wavefront are tokens n and n ^ 4 by 4 pieces: their
+        // chunks of the swizzled rows lie in different banks, as do their copies of a code's entry.
+        // cos and sin turn from tile to tile by the fixed angle of 64 positions (4 flops a pair, where a row of the
+        // table per token would be 512 bytes from L2); every 8th tile they are read from the table again, so that
+        // no more than 8 roundings add up.
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 112;");
         constexpr int NP = D / (2 * C);
         constexpr int IT = D / 64;                                   // rounds of 4 pieces
         constexpr int NW = C == 4 ? 2 : 1;                           // index words per piece
-        const int rw = warp - 9, tl = lane & 7, pl = lane >> 3;
+        constexpr int kAnchor = 8;
+        const int rw = warp - P::kRebuild, pl = lane & 3, tl = ((lane >> 2) & 1) * 4 + (lane >> 3);
         const uint32_t *idx = a.idx + (size_t)h * a.idx_head;
-        const unsigned char *tab[2] = {smem + P::offTable, smem + P::offTable + P::kTable};
-        const uint16_t *gsl[2] = {a.slk + (size_t)h * a.K * D, a.slv + (size_t)h * a.K * D};
+        // a lane's copy of an entry: C = 4: 16 copies of 8 bytes, one per lane of a half warp; else C / 8 pieces of 16
+        // bytes per copy, the lanes of a quarter warp on 8 / (C / 8) copies
+        const uint32_t copy = C == 4 ? (lane & 15) * 8
+                              : C == 8 ? (lane & 7) * 16
+                              : C == 16 ? ((pl & 1) + 2 * ((pl >> 1) + 2 * ((lane >> 2) & 1))) * 16
+                                        : (pl + 4 * ((lane >> 2) & 1)) * 16;
+        const unsigned char *tab = smem + P::offTable + copy;
+        const float4 *turn = reinterpret_cast<const float4 *>(smem + P::offTurn);
         const int kmax = a.K - 1;
         auto load_words = [&](int t, uint32_t (&wd)[IT][NW]) {
             const int n = tok_first + t * NT + rw * 8 + tl;
@@ -453,46 +567,53 @@ __global__ void __launch_bounds__(Plan<D, MB, C>::kThreads, 1)
         auto gather = [&](int kv, int half, int piece, const uint32_t (&wd)[NW]) -> uint4 {
             const int sh = kv * 16 + half * 8;
             uint4 v;
+            const uint16_t *gsl = (kv ? a.slv : a.slk) + (size_t)h * a.K * D;
             if constexpr (C == 4) {
                 const int c0 = (wd[0] >> sh) & 255, c1 = (wd[NW - 1] >> sh) & 255;
                 uint2 x, y;
                 if constexpr (PG) {
                     const int g = half * NP + piece * 2;
-                    x = __ldg(reinterpret_cast<const uint2 *>(gsl[kv] + (size_t)min(c0, kmax) * D + g * C));
-                    y = __ldg(reinterpret_cast<const uint2 *>(gsl[kv] + (size_t)min(c1, kmax) * D + (g + 1) * C));
+                    x = __ldg(reinterpret_cast<const uint2 *>(gsl + (size_t)min(c0, kmax) * D + g * C));
+                    y = __ldg(reinterpret_cast<const uint2 *>(gsl + (size_t)min(c1, kmax) * D + (g + 1) * C));
                 } else {
-                    x = *reinterpret_cast<const uint2 *>(tab[kv] + c0 * 8);
-                    y = *reinterpret_cast<const uint2 *>(tab[kv] + c1 * 8);
+                    x = *reinterpret_cast<const uint2 *>(tab + kv * P::kTable + c0 * 128);
+                    y = *reinterpret_cast<const uint2 *>(tab + kv * P::kTable + c1 * 128);
                 }
                 v = make_uint4(x.x, x.y, y.x, y.y);
             } else {
-                const int c0 = (wd[0] >> sh) & 255, sub = piece % (C / 8);
+                const int c0 = (wd[0] >> sh) & 255;
                 if constexpr (PG) {
                     const int g = half * NP + piece / (C / 8);
-                    v = __ldg(reinterpret_cast<const uint4 *>(gsl[kv] + (size_t)min(c0, kmax) * D + g * C + sub * 8));
+                    v = __ldg(reinterpret_cast<const uint4 *>(gsl + (size_t)min(c0, kmax) * D + g * C + piece % (C / 8) * 8));
                 } else {
-                    v = *reinterpret_cast<const uint4 *>(tab[kv] + c0 * (C * 2) + sub * 16);
+                    v = *reinterpret_cast<const uint4 *>(tab + kv * P::kTable + c0 * 128);
                 }
             }
             return v;
         };
-        uint32_t wd[IT][NW];
+        uint32_t wd[IT][NW], nx[IT][NW];
         load_words(0, wd);
+        load_words(1, nx);
+        float2 cs[IT][4], sn[IT][4];                                 // of this lane's token and channels
         for (int t = 0; t < ntiles; ++t) {
             const int s = t % ST;
             const int nl = rw * 8 + tl, n = tok_first + t * NT + nl;
             const bool in = n >= st && n < len;
-            float4 cs[IT][2], sn[IT][2];
+            uint32_t n2[IT][NW];
+            load_words(t + 2, n2);                                   // two tiles ahead: a tile is shorter than a load
+            if (t % kAnchor == 0) {
+                const float4 *row = reinterpret_cast<const float4 *>(a.rope + (size_t)(n < len ? n : tok0) * D);
 #pragma unroll
-            for (int it = 0; it < IT; ++it) {
-                const float4 *rp = reinterpret_cast<const float4 *>(a.rope + (size_t)(in ? n : tok0) * D + (it * 4 + pl) * 8);
-                cs[it][0] = __ldg(rp);
-                cs[it][1] = __ldg(rp + 1);
-                sn[it][0] = __ldg(rp + D / 8);
-                sn[it][1] = __ldg(rp + D / 8 + 1);
+                for (int it = 0; it < IT; ++it)
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        const float4 c = __ldg(row + (it * 4 + pl) * 2 + k), x = __ldg(row + D / 8 + (it * 4 + pl) * 2 + k);
+                        cs[it][2 * k] = f2(c.x, c.y);
+                        cs[it][2 * k + 1] = f2(c.z, c.w);
+                        sn[it][2 * k] = f2(x.x, x.y);
+                        sn[it][2 * k + 1] = f2(x.z, x.w);
+                    }
             }
-            uint32_t nx[IT][NW];
-            load_words(t + 1, nx);
             if (t >= ST) {
                 const bool ok = tc::mbar_wait_or_dead(vempty(s), (t / ST - 1) & 1, a.wait_ns, dead);
                 if (!__all_sync(0xffffffffu, ok)) break;
@@ -502,33 +623,31 @@ __global__ void __launch_bounds__(Plan<D, MB, C>::kThreads, 1)
             for (int it = 0; it < IT; ++it) {
                 const int piece = it * 4 + pl;
                 const uint4 z = make_uint4(0, 0, 0, 0);
-                const uint4 v0 = in ? gather(1, 0, piece, wd[it]) : z, v1 = in ? gather(1, 1, piece, wd[it]) : z;
                 const uint4 k0 = in ? gather(0, 0, piece, wd[it]) : z, k1 = in ? gather(0, 1, piece, wd[it]) : z;
+                const uint4 v0 = in ? gather(1, 0, piece, wd[it]) : z, v1 = in ? gather(1, 1, piece, wd[it]) : z;
                 const uint32_t kl[4] = {k0.x, k0.y, k0.z, k0.w}, kh[4] = {k1.x, k1.y, k1.z, k1.w};
-                const float c8[8] = {cs[it][0].x, cs[it][0].y, cs[it][0].z, cs[it][0].w,
-                                     cs[it][1].x, cs[it][1].y, cs[it][1].z, cs[it][1].w};
-                const float s8[8] = {sn[it][0].x, sn[it][0].y, sn[it][0].z, sn[it][0].w,
-                                     sn[it][1].x, sn[it][1].y, sn[it][1].z, sn[it][1].w};
                 uint32_t ah[4], al[4], bh[4], bl[4];                 // rotated: bf16 parts of the low and high channels
+                const float2 minus = f2(-1.f, -1.f);
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
-                    const float2 x = unpack2(kl[k]), y = unpack2(kh[k]);
-                    const float ra0 = x.x * c8[2 * k] - y.x * s8[2 * k], ra1 = x.y * c8[2 * k + 1] - y.y * s8[2 * k + 1];
-                    const float rb0 = y.x * c8[2 * k] + x.x * s8[2 * k], rb1 = y.y * c8[2 * k + 1] + x.y * s8[2 * k + 1];
-                    ah[k] = cvt_bf16x2(ra1, ra0);
-                    al[k] = cvt_bf16x2(ra1 - bf16hi(ah[k]), ra0 - bf16lo(ah[k]));
-                    bh[k] = cvt_bf16x2(rb1, rb0);
-                    bl[k] = cvt_bf16x2(rb1 - bf16hi(bh[k]), rb0 - bf16lo(bh[k]));
+                    const float2 x = unpack2(kl[k]), y = unpack2(kh[k]), ny = unpack2(kh[k] ^ 0x80008000u);
+                    const float2 ra = __ffma2_rn(x, cs[it][k], __fmul2_rn(ny, sn[it][k]));
+                    const float2 rb = __ffma2_rn(y, cs[it][k], __fmul2_rn(x, sn[it][k]));
+                    ah[k] = cvt_bf16x2(ra.y, ra.x);
+                    bh[k] = cvt_bf16x2(rb.y, rb.x);
+                    const float2 da = __ffma2_rn(unpack2(ah[k]), minus, ra), db = __ffma2_rn(unpack2(bh[k]), minus, rb);
+                    al[k] = cvt_bf16x2(da.y, da.x);
+                    bl[k] = cvt_bf16x2(db.y, db.x);
                 }
                 // low channels 8 piece .., high channels D/2 + 8 piece ..
                 const uint32_t lo_at = sw128(nl, piece);
                 const uint32_t hi_at = D == 128 ? P::kPanel + sw128(nl, piece) : sw128(nl, piece + 4);
+                sts128(vb + lo_at, v0);
+                sts128(vb + hi_at, v1);
                 sts128(kb + lo_at, make_uint4(ah[0], ah[1], ah[2], ah[3]));
                 sts128(kb + hi_at, make_uint4(bh[0], bh[1], bh[2], bh[3]));
                 sts128(kb + P::kTile + lo_at, make_uint4(al[0], al[1], al[2], al[3]));
                 sts128(kb + P::kTile + hi_at, make_uint4(bl[0], bl[1], bl[2], bl[3]));
-                sts128(vb + lo_at, v0);
-                sts128(vb + hi_at, v1);
             }
             tc::fence_async_smem();
             __syncwarp();
@@ -536,7 +655,24 @@ __global__ void __launch_bounds__(Plan<D, MB, C>::kThreads, 1)
 #pragma unroll
             for (int it = 0; it < IT; ++it)
 #pragma unroll
-                for (int k = 0; k < NW; ++k) wd[it][k] = nx[it][k];
+                for (int k = 0; k < 2; ++k) {
+                    const float4 c64 = turn[(it * 4 + pl) * 2 + k], s64 = turn[D / 8 + (it * 4 + pl) * 2 + k];
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        const float2 c = cs[it][2 * k + j], x = sn[it][2 * k + j];
+                        const float2 tc2 = j ? f2(c64.z, c64.w) : f2(c64.x, c64.y);
+                        const float2 ts2 = j ? f2(s64.z, s64.w) : f2(s64.x, s64.y);
+                        cs[it][2 * k + j] = __ffma2_rn(c, tc2, __fmul2_rn(neg2(x), ts2));
+                        sn[it][2 * k + j] = __ffma2_rn(x, tc2, __fmul2_rn(c, ts2));
+                    }
+                }
+#pragma unroll
+            for (int it = 0; it < IT; ++it)
+#pragma unroll
+                for (int k = 0; k < NW; ++k) {
+                    wd[it][k] = nx[it][k];
+                    nx[it][k] = n2[it][k];
+                }
         }
     }
 
@@ -544,83 +680,117 @@ __global__ void __launch_bounds__(Plan<D, MB, C>::kThreads, 1)
     __syncthreads();
     if (*dead) {
         if (tid == 0) atomicOr(a.fault, kFaultAttnWait);
-        if (!coded && warp == 9 && lane == 0)                        // copies still in flight
+        if (!coded && warp == P::kCopy && lane == 0)                        // copies still in flight
             for (int t = issued > ST ? issued - ST : 0; t < issued; ++t) {
                 tc::mbar_wait_bounded(kfull(t % ST), (t / ST) & 1, tc::kDrainNs);
                 tc::mbar_wait_bounded(vfull(t % ST), (t / ST) & 1, tc::kDrainNs);
             }
-        if (warp == 8 && lane == 0) {                                // products still in flight
+        if (warp == P::kMma && lane == 0) {                          // products still in flight
             tc::mma_commit(drain);
             tc::mbar_wait_bounded(drain, 0, tc::kDrainNs);
         }
         __syncthreads();
     }
     tc::tc_fence_after();
-    if (warp == 8)
+    if (warp == P::kMma)
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols));
 }
 
-// Log-sum-exp merge of the records of every query row, and of another part over other tokens: one warp per row.
-// Row h * R + r of the records is query token r / qpk, head h * qpk + r % qpk.
+// Log-sum-exp merge of the splits' records of every query row, and of another part over other tokens.  The records
+// of a (split, KV head) are R * D / 4 elements of 16 bytes, row fastest; a CTA takes 32 of them, its 8 warps a share of
+// the splits each (all loads of a warp in flight at once: the merge is a chain of latencies, not of bytes), joined
+// through shared memory.  Row r of KV head h is query token r / qpk, head h * qpk + r % qpk.
 template <int D>
-__global__ void __launch_bounds__(256) shared_merge_kernel(const SharedArgs a, int nrec, const float *other_out,
+__global__ void __launch_bounds__(256) shared_merge_kernel(const SharedArgs a, const float *other_out,
                                                            const float *other_lse, float *out, float *lse) {
-    constexpr int V = D / 32;                                        // channels per lane
-    const size_t RT = (size_t)a.rows * a.Hq;
-    const size_t row = (size_t)blockIdx.x * 8 + (threadIdx.x >> 5);
-    const int lane = threadIdx.x & 31;
-    if (row >= RT) return;
-    const size_t r = row % a.R, h = row / a.R;
-    const size_t dst = (r / a.qpk) * a.Hq + h * a.qpk + r % a.qpk;
-    float mx = -CUDART_INF_F;
-    for (int i = lane; i < nrec; i += 32) mx = fmaxf(mx, a.ws_ml[(size_t)i * RT + row].x);
+    constexpr int W = 8, BATCH = 5;
+    __shared__ float4 s_acc[W][32];
+    __shared__ float2 s_ml[W][32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const size_t per_head = (size_t)a.R * (D / 4);
+    const size_t id = (size_t)blockIdx.x * 32 + lane;
+    const bool live = id < per_head * a.Hkv;
+    const int h = live ? (int)(id / per_head) : 0, e = live ? (int)(id % per_head) : 0;
+    const int c4 = e / a.R, r = e % a.R;
+    const size_t dst = (size_t)(r >> a.qshift) * a.Hq + h * a.qpk + (r & (a.qpk - 1));
+    grid_wait();
+    const float2 *ml = a.ws_ml + (size_t)h * a.R + r;
+    const float4 *o = reinterpret_cast<const float4 *>(a.ws_o) + (size_t)h * per_head + e;
+    const size_t step = (size_t)a.Hkv * a.R;                         // records of the next split
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    float mx = -CUDART_INF_F, sum = 0.f;
+    if (live) {
+        for (int i0 = warp; i0 < a.nsplit; i0 += W * BATCH) {
+            float2 x[BATCH];
+            float4 y[BATCH];
 #pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-    const float ol = other_lse ? other_lse[dst] * 1.44269504088896340736f : -CUDART_INF_F;
-    const float top = fmaxf(mx, ol);
-    float acc[V], sum = 0.f;
+            for (int k = 0; k < BATCH; ++k) {
+                const size_t i = (size_t)min(i0 + k * W, a.nsplit - 1) * step;
+                x[k] = ml[i];
+                y[k] = o[i * (D / 4)];
+            }
+            float top = mx;
 #pragma unroll
-    for (int k = 0; k < V; ++k) acc[k] = 0.f;
-    if (mx != -CUDART_INF_F) {
-#pragma unroll 4
-        for (int i = 0; i < nrec; ++i) {
-            const float2 ml = a.ws_ml[(size_t)i * RT + row];
-            if (ml.x == -CUDART_INF_F) continue;                     // a record without tokens was not written
-            const float w = ex2(ml.x - top);
-            sum += w * ml.y;
-            const float *o = a.ws_o + ((size_t)i * RT + row) * D + lane * V;
-            if constexpr (V == 4) {
-                const float4 x = *reinterpret_cast<const float4 *>(o);
-                acc[0] += w * x.x;
-                acc[1] += w * x.y;
-                acc[2] += w * x.z;
-                acc[3] += w * x.w;
-            } else {
-                const float2 x = *reinterpret_cast<const float2 *>(o);
-                acc[0] += w * x.x;
-                acc[1] += w * x.y;
+            for (int k = 0; k < BATCH; ++k) {
+                if (i0 + k * W >= a.nsplit) x[k] = f2(-CUDART_INF_F, 0.f);
+                top = fmaxf(top, x[k].x);
+            }
+            if (top == -CUDART_INF_F) continue;
+            const float corr = ex2(mx - top);
+            mx = top;
+            sum *= corr;
+            acc = make_float4(acc.x * corr, acc.y * corr, acc.z * corr, acc.w * corr);
+#pragma unroll
+            for (int k = 0; k < BATCH; ++k) {
+                if (x[k].x == -CUDART_INF_F) continue;               // a record without tokens has no O
+                const float w = ex2(x[k].x - top);
+                sum += w * x[k].y;
+                acc.x += w * y[k].x;
+                acc.y += w * y[k].y;
+                acc.z += w * y[k].z;
+                acc.w += w * y[k].w;
             }
         }
     }
-    float res[V];
-    const float wo = top == -CUDART_INF_F ? 0.f : ex2(ol - top);
-    const float total = sum + wo;
-    const float inv = total != 0.f ? 1.f / total : 0.f;              // no tokens at all: zeros
+    s_acc[warp][lane] = acc;
+    s_ml[warp][lane] = f2(mx, sum);
+    __syncthreads();
+    if (warp != 0 || !live) return;
+    const float ol = other_lse ? other_lse[dst] * 1.44269504088896340736f : -CUDART_INF_F;
+    float top = ol;
 #pragma unroll
-    for (int k = 0; k < V; ++k) {
-        float x = acc[k];
-        if (wo > 0.f) x += wo * other_out[dst * D + lane * V + k];
-        res[k] = x * inv;
+    for (int k = 0; k < W; ++k) top = fmaxf(top, s_ml[k][lane].x);
+    acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    float total = 0.f;
+    if (top != -CUDART_INF_F) {
+#pragma unroll
+        for (int k = 0; k < W; ++k) {
+            const float w = ex2(s_ml[k][lane].x - top);              // of no record: 0
+            const float4 y = s_acc[k][lane];
+            total += w * s_ml[k][lane].y;
+            acc.x += w * y.x;
+            acc.y += w * y.y;
+            acc.z += w * y.z;
+            acc.w += w * y.w;
+        }
+        const float wo = ex2(ol - top);
+        if (wo > 0.f) {
+            const float4 y = *reinterpret_cast<const float4 *>(other_out + dst * D + c4 * 4);
+            total += wo;
+            acc.x += wo * y.x;
+            acc.y += wo * y.y;
+            acc.z += wo * y.z;
+            acc.w += wo * y.w;
+        }
     }
-#pragma unroll
-    for (int k = 0; k < V; ++k) out[dst * D + lane * V + k] = res[k];
-    __syncwarp();                                                    // lse may be other_lse
-    if (lse != nullptr && lane == 0)
+    const float inv = total != 0.f ? 1.f / total : 0.f;              // no tokens at all: zeros
+    *reinterpret_cast<float4 *>(out + dst * D + c4 * 4) = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+    if (lse != nullptr && c4 == 0)
         lse[dst] = total == 0.f ? -CUDART_INF_F : (top + log2f(total)) * 0.69314718055994530942f;
 }
 
 struct SharedPlan {
-    int mb, nsplit, nrec, nz;
+    int mb, nsplit, nz;
 };
 
 // Splits: a CTA owns an SM (its tiles fill shared memory), so the splits that fill whole waves of 148 CTAs are
@@ -642,14 +812,13 @@ SharedPlan plan_shared(int Hkv, int R, int max_len, int nt) {
             p.nsplit = (int)ns;
         }
     }
-    p.nrec = p.nsplit * (p.mb == 1 ? 2 : 1);
     return p;
 }
 
 size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 
 size_t ws_bytes(const SharedPlan &p, size_t RT, int D) {
-    return align256(p.nrec * RT * D * sizeof(float)) + p.nrec * RT * sizeof(float2);
+    return align256(p.nsplit * RT * D * sizeof(float)) + p.nsplit * RT * sizeof(float2);
 }
 
 // cuTensorMapEncodeTiled through the runtime: the library does not link the driver.
@@ -688,12 +857,11 @@ cudaError_t make_map(CUtensorMap *m, const uint16_t *p, size_t rows, int D, int 
 template <int D, int MB, int C, bool PG>
 cudaError_t launch_t(const SharedArgs &a, const SharedPlan &p, const CUtensorMap &km, const CUtensorMap &vm,
                      cudaStream_t s) {
-    using PL = Plan<D, MB, PG ? 4 : C>;
+    using PL = Plan<D, MB, C, PG>;
     auto kern = shared_attn_kernel<D, MB, C, PG>;
     cudaError_t e = ensure_dynamic_smem((const void *)kern, PL::kAlloc);
     if (e != cudaSuccess) return e;
-    kern<<<dim3(p.nsplit, a.Hkv, p.nz), PL::kThreads, PL::kAlloc, s>>>(a, km, vm);
-    return cudaGetLastError();
+    return launch_pdl(kern, dim3(p.nsplit, a.Hkv, p.nz), PL::kThreads, PL::kAlloc, s, a, km, vm);
 }
 
 template <int C, bool PG>
@@ -705,12 +873,11 @@ cudaError_t launch_d(int D, const SharedArgs &a, const SharedPlan &p, const CUte
     return cudaErrorInvalidValue;
 }
 
-cudaError_t finish(const SharedArgs &a, const SharedPlan &p, int D, const SharedOther &o, float *out, float *lse,
+cudaError_t finish(const SharedArgs &a, int D, const SharedOther &o, float *out, float *lse,
                    cudaStream_t s) {
-    const unsigned blocks = (unsigned)(((size_t)a.rows * a.Hq + 7) / 8);
-    if (D == 128) shared_merge_kernel<128><<<blocks, 256, 0, s>>>(a, p.nrec, o.out, o.lse, out, lse);
-    else shared_merge_kernel<64><<<blocks, 256, 0, s>>>(a, p.nrec, o.out, o.lse, out, lse);
-    return cudaGetLastError();
+    const unsigned blocks = (unsigned)(((size_t)a.rows * a.Hq * (D / 4) + 31) / 32);
+    return launch_pdl(D == 128 ? shared_merge_kernel<128> : shared_merge_kernel<64>, dim3(blocks), 256, 0, s, a, o.out,
+                      o.lse, out, lse);
 }
 
 SharedArgs common_args(int rows, int Hkv, int Hq, int D, const SharedPlan &p, const uint16_t *q, const int32_t *start,
@@ -723,13 +890,14 @@ SharedArgs common_args(int rows, int Hkv, int Hq, int D, const SharedPlan &p, co
     a.Hkv = Hkv;
     a.Hq = Hq;
     a.qpk = Hq / Hkv;
+    while ((1 << a.qshift) < a.qpk) ++a.qshift;
     a.R = rows * a.qpk;
     a.max_len = max_len;
     a.nsplit = p.nsplit;
     a.qscale = scale * 1.44269504088896340736f;
     a.ws_o = reinterpret_cast<float *>(workspace);
     a.ws_ml = reinterpret_cast<float2 *>(reinterpret_cast<char *>(workspace) +
-                                         align256(p.nrec * (size_t)rows * Hq * D * sizeof(float)));
+                                         align256(p.nsplit * (size_t)rows * Hq * D * sizeof(float)));
     a.wait_ns = wait_limit_ns();
     return a;
 }
@@ -755,7 +923,7 @@ cudaError_t launch_bf16_shared(const loopvq_bf16_cache &c, int seq, const uint16
     if (e == cudaSuccess) e = make_map(&vm, c.v + at, map_rows, c.D, 128);
     if (e == cudaSuccess) e = launch_d<0, false>(c.D, a, p, km, vm, s);
     if (e != cudaSuccess) return e;
-    return finish(a, p, c.D, other, out, lse, s);
+    return finish(a, c.D, other, out, lse, s);
 }
 
 cudaError_t launch_shared(const loopvq_cache &cc, int layer, int t, int seq, const uint16_t *q, int rows,
@@ -782,7 +950,7 @@ cudaError_t launch_shared(const loopvq_cache &cc, int layer, int t, int seq, con
         default: return cudaErrorInvalidValue;
     }
     if (e != cudaSuccess) return e;
-    return finish(a, p, cc.D, other, out, lse, s);
+    return finish(a, cc.D, other, out, lse, s);
 }
 
 }  // namespace loopvq

@@ -269,7 +269,7 @@ def test_prefix_then_own_tokens_then_eviction():
         first = LQ.bf16_decode_attn(own, q, lens, n_own)
         out2, lse2 = shared(other=first)
         into = (first[0].clone(), first[1].clone())
-        out3, lse3 = shared(other=into, out=into[0], lse=into[1])    # in place
+        out3, lse3 = shared(other=into, out=into[0])                 # in place
         assert torch.equal(out2, out3) and torch.equal(lse2, lse3)
         for i in range(b):
             n = int(lens[i])
