@@ -8,7 +8,7 @@
 // One CTA per (token split, KV head, up to 2 x 128 query rows).  Its warps:
 //   0-3, 4-7  softmax of stream 0 and stream 1: thread = query row = tensor-memory lane
 //   8, 9      bf16 cache: one thread issues every product, one copies K and V tiles by TMA
-//   8-15, 16  coded cache: eight warps rebuild K and V tiles, one thread issues every product
+//   8-15, 16-18  coded cache: eight warps rebuild K tiles, one thread issues every product, two warps rebuild V tiles
 // A step is one product pair S = Q K^T, O += P V of 128 rows by one tile of tokens.  Steps alternate between two
 // streams, each with its own S, O, maximum and sum, so that the products of one stream run under the softmax of
 // the other: with up to 128 rows the streams take the tiles in turn (and give two partial results), with more
@@ -24,8 +24,7 @@
 
 #include <atomic>
 
-#include "decode_kernel.cuh"
-#include "tcgen05.cuh"
+#include "shared_rows.cuh"
 
 namespace loopvq {
 
@@ -55,8 +54,7 @@ struct SharedArgs {
 // Shared-memory and tensor-memory plan.  NT tokens per tile, KP bf16 parts per key.
 // bf16 cache: the queries lie in shared memory (S and O fill the tensor memory at 128-token tiles).
 // Coded cache: 64-token tiles leave tensor memory for the queries, so the products read only the tiles from shared
-// memory, whose bandwidth they share with the rebuilding; and each 8-bit code's slice entry fills a row of 128 bytes
-// with copies of itself, one for every lane that a wavefront serves, so that gathers meet no bank conflict.
+// memory, whose bandwidth they share with the rebuilding.
 template <int D, int MB, int C, bool PG>
 struct Plan {
     static constexpr bool coded = C != 0;
@@ -66,8 +64,8 @@ struct Plan {
     static constexpr int kTile = (D / 64) * kPanel;
     static constexpr int kStage = (KP + 1) * kTile;                  // K parts, then V
     static constexpr int kQ = coded ? 0 : (D / 64) * 128 * 128;      // one row block
-    static constexpr int ST = D == 64 ? 4 : (coded || MB == 1 ? 3 : 2);
-    static constexpr int kTable = coded && !PG ? 256 * 128 : 0;      // K slice, then V slice
+    static constexpr int ST = D == 64 || coded ? 4 : MB == 1 ? 3 : 2;
+    static constexpr int kTable = coded && !PG ? kTableBytes : 0;    // K slice, then V slice
     static constexpr int offQ = 0;
     static constexpr int offStage = MB * kQ;
     static constexpr int offTable = offStage + ST * kStage;
@@ -77,10 +75,10 @@ struct Plan {
     static constexpr int offTmem = offBar + kBars * 8;
     static constexpr int kUsed = offTmem + 16;
     static constexpr int kAlloc = kUsed + 1024;
-    static constexpr int kThreads = coded ? 9 * 32 + 256 : 320;
+    static constexpr int kThreads = coded ? 20 * 32 : 320;
     static constexpr int kMma = coded ? 16 : 8;                      // warps: products;
     static constexpr int kCopy = coded ? 16 : 9;                     // copies (and the barriers' set-up);
-    static constexpr int kRebuild = 8;                               // the first of the rebuilding ones
+    static constexpr int kRebuild = 8, kValues = 17;                 // the first of those that rebuild keys, values
     static constexpr int colS = coded ? 64 : 128;                    // S of stream w at w * colS
     static constexpr int colQ = coded ? 128 : 0;                     // coded: Q of row block w at 128 + 64 w
     static_assert(kAlloc <= 232448, "shared memory");
@@ -88,14 +86,6 @@ struct Plan {
 };
 
 constexpr int kTmemCols = 512;                                       // O of stream w at 256 + 128 w
-
-// Rows n (128 bytes of 64 channels) of a panel: 16-byte chunk j lies at chunk j ^ (n & 7).
-__device__ __forceinline__ uint32_t sw128(int n, int chunk) { return (uint32_t)n * 128u + ((uint32_t)(chunk ^ (n & 7)) << 4); }
-
-__device__ __forceinline__ void sts128(uint32_t addr, uint4 v) {
-    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
-                 : "memory");
-}
 
 // The running softmax of one query row of one stream, and what its thread does with a tile's scores.
 template <int D, int NT>
@@ -207,7 +197,7 @@ __global__ void __launch_bounds__(Plan<D, MB, C, PG>::kThreads, 1)
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + P::offTmem);
     volatile int *dead = reinterpret_cast<volatile int *>(smem + P::offTmem + 4);
 
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tc::uniform_warp();
     const int split = blockIdx.x, h = blockIdx.y;
     const int r0 = blockIdx.z * (MB * 128);                          // first query row of this CTA
 
@@ -249,7 +239,7 @@ __global__ void __launch_bounds__(Plan<D, MB, C, PG>::kThreads, 1)
     if (warp == P::kCopy && lane == 0) {
         for (int s = 0; s < ST; ++s) {
             tc::mbar_init(kfull(s), coded ? 8 : 1);
-            tc::mbar_init(vfull(s), 1);
+            tc::mbar_init(vfull(s), coded ? 2 : 1);
             tc::mbar_init(kempty(s), 1);
             tc::mbar_init(vempty(s), 1);
         }
@@ -296,23 +286,8 @@ __global__ void __launch_bounds__(Plan<D, MB, C, PG>::kThreads, 1)
         for (int i = tid; i < D; i += P::kThreads)                   // used from the second tile on: row 64 is there
             reinterpret_cast<float *>(smem + P::offTurn)[i] = ntiles > 1 ? a.rope[(size_t)64 * D + i] : 0.f;
     }
-    if constexpr (coded && !PG) {
-        const uint16_t *src[2] = {a.slk + (size_t)h * a.K * C, a.slv + (size_t)h * a.K * C};
-#pragma unroll 4
-        for (int it = tid; it < 2 * 256 * 8; it += P::kThreads) {    // 16-byte pieces of the copies' rows
-            const int kv = it / 2048, e = it / 8 % 256, slot = it % 8;
-            uint4 v = make_uint4(0, 0, 0, 0);                        // entries past K: zeros
-            if (e < a.K) {
-                if constexpr (C == 4) {
-                    const uint2 x = *reinterpret_cast<const uint2 *>(src[kv] + e * 4);
-                    v = make_uint4(x.x, x.y, x.x, x.y);
-                } else {
-                    v = *reinterpret_cast<const uint4 *>(src[kv] + e * C + slot % (C / 8) * 8);
-                }
-            }
-            *reinterpret_cast<uint4 *>(smem + P::offTable + kv * P::kTable + e * 128 + slot * 16) = v;
-        }
-    }
+    if constexpr (coded && !PG)
+        fill_tables<C>(smem + P::offTable, a.slk + (size_t)h * a.K * C, a.slv + (size_t)h * a.K * C, a.K, P::kThreads);
     cp_async_wait<0>();
     tc::fence_async_smem();
     tc::tc_fence_before();
@@ -343,8 +318,8 @@ __global__ void __launch_bounds__(Plan<D, MB, C, PG>::kThreads, 1)
 
     if (warp < 8) {
         // ---- softmax of stream w: 128 threads, one query row each
-        // 17 warps are launched with 96 registers each; the rebuilding warps' 32 running cosines and sines need more
-        // and the softmax less: 256 x 80 + 256 x 112 + 32 x 96 = 544 x 96
+        // 20 warps are launched with 96 registers each; the running cosines and sines of the warps that rebuild keys need
+        // more and the softmax less: 256 x 80 + 256 x 112 + 128 x 96 = 640 x 96
         if constexpr (coded) asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
         const int w = warp >> 2, row = tid & 127;
         const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
@@ -452,25 +427,22 @@ __global__ void __launch_bounds__(Plan<D, MB, C, PG>::kThreads, 1)
             const int t = MB == 2 ? i >> 1 : i, s = t % ST;
             if (!wait(kfull(s), (t / ST) & 1)) return;
             tc::tc_fence_after();
-            if (lane == 0) {
-                const uint32_t kb = sStage + s * P::kStage, sd = tmem + (i & 1) * P::colS;
+            if (tc::elect_one()) {
+                constexpr uint32_t hi = tc::desc_hi(1024, 2);
+                const uint32_t sd = tmem + (i & 1) * P::colS, k_lo = tc::desc_lo(sStage + s * P::kStage, 16);
+                const uint32_t q_lo = tc::desc_lo(sQ + (MB == 2 ? (i & 1) * P::kQ : 0), 16);
+                const uint32_t q_tm = tmem + P::colQ + (MB == 2 ? (i & 1) * 64 : 0);
 #pragma unroll
                 for (int part = 0; part < KP; ++part)
 #pragma unroll
                     for (int k = 0; k < D / 16; ++k) {               // 16 channels per product: 32 bytes of a row
-                        const uint64_t kd = tc::smem_desc_sw128(
-                            kb + part * P::kTile + (k / 4) * P::kPanel + (k % 4) * 32, 16, 1024);
-                        if constexpr (coded) {
-                            tc::mma_bf16_ta(sd, tmem + P::colQ + (MB == 2 ? (i & 1) * 64 : 0) + k * 8, kd, id_qk,
-                                            part + k > 0);
-                        } else {
-                            tc::mma_bf16(sd,
-                                         tc::smem_desc_sw128(sQ + (MB == 2 ? (i & 1) * P::kQ : 0) +
-                                                             (k / 4) * (128 * 128) + (k % 4) * 32, 16, 1024),
-                                         kd, id_qk, part + k > 0);
-                        }
+                        const uint32_t at = k_lo + (part * P::kTile + (k / 4) * P::kPanel + (k % 4) * 32) / 16;
+                        if constexpr (coded)
+                            tc::mma_ts(sd, q_tm + k * 8, at, hi, id_qk, part + k > 0);
+                        else
+                            tc::mma_ss(sd, q_lo + ((k / 4) * (128 * 128) + (k % 4) * 32) / 16, hi, at, hi, id_qk, part + k > 0);
                     }
-                if (!coded && (MB == 1 || (i & 1)) && t + ST < ntiles) tc::mma_commit(kempty(s));
+                if ((MB == 1 || (i & 1)) && t + ST < ntiles) tc::mma_commit(kempty(s));
                 tc::mma_commit(sfull(i & 1));
             }
             __syncwarp();
@@ -480,8 +452,8 @@ __global__ void __launch_bounds__(Plan<D, MB, C, PG>::kThreads, 1)
         for (int i = 0; ok && i < nsteps; ++i) {
             const int t = MB == 2 ? i >> 1 : i, s = t % ST, w = i & 1;
             const uint32_t vb = sStage + s * P::kStage + KP * P::kTile;
+            if (!wait(vfull(s), (t / ST) & 1)) break;
             if constexpr (!coded) {
-                if (!wait(vfull(s), (t / ST) & 1)) break;
                 // rows behind the last token may hold anything: 0 x that has to be 0
                 const int end = len - (tok_first + t * NT);
                 if (end < NT && (MB == 1 || w == 0)) {
@@ -495,15 +467,14 @@ __global__ void __launch_bounds__(Plan<D, MB, C, PG>::kThreads, 1)
             }
             if (!wait(pfull(w), (i >> 1) & 1)) break;
             tc::tc_fence_after();
-            if (lane == 0) {
-                const uint32_t od = tmem + 256 + w * 128, pa = tmem + w * P::colS;
+            if (tc::elect_one()) {
+                const uint32_t od = tmem + 256 + w * 128, pa = tmem + w * P::colS, v_lo = tc::desc_lo(vb, P::kPanel);
 #pragma unroll
                 for (int part = 0; part < 2; ++part)
 #pragma unroll
                     for (int k = 0; k < NT / 16; ++k)                // 16 tokens per product: 8 packed columns
-                        tc::mma_bf16_ta(od, pa + k * 16 + part * 8,
-                                        tc::smem_desc_sw128(vb + k * 2048, P::kPanel, 1024), id_pv,
-                                        i > 1 || part + k > 0);
+                        tc::mma_ts(od, pa + k * 16 + part * 8, v_lo + k * 128, tc::desc_hi(1024, 2), id_pv,
+                                   i > 1 || part + k > 0);
                 if ((MB == 1 || w == 1) && t + ST < ntiles) tc::mma_commit(vempty(s));
                 tc::mma_commit(odone(w));
             }
@@ -530,149 +501,27 @@ __global__ void __launch_bounds__(Plan<D, MB, C, PG>::kThreads, 1)
             }
         }
     } else {
-        // ---- rebuilding: a warp takes 8 tokens of the tile, a lane one token and one piece of 8 + 8 channels
-        // (8 RoPE pairs) at a time.  The 8 lanes of a 16-byte wavefront are tokens n and n ^ 4 by 4 pieces: their
-        // chunks of the swizzled rows lie in different banks, as do their copies of a code's entry.
-        // cos and sin turn from tile to tile by the fixed angle of 64 positions (4 flops a pair, where a row of the
-        // table per token would be 512 bytes from L2); every 8th tile they are read from the table again, so that
-        // no more than 8 roundings add up.
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 112;");
-        constexpr int NP = D / (2 * C);
-        constexpr int IT = D / 64;                                   // rounds of 4 pieces
-        constexpr int NW = C == 4 ? 2 : 1;                           // index words per piece
-        constexpr int kAnchor = 8;
-        const int rw = warp - P::kRebuild, pl = lane & 3, tl = ((lane >> 2) & 1) * 4 + (lane >> 3);
-        const uint32_t *idx = a.idx + (size_t)h * a.idx_head;
-        // a lane's copy of an entry: C = 4: 16 copies of 8 bytes, one per lane of a half warp; else C / 8 pieces of 16
-        // bytes per copy, the lanes of a quarter warp on 8 / (C / 8) copies
-        const uint32_t copy = C == 4 ? (lane & 15) * 8
-                              : C == 8 ? (lane & 7) * 16
-                              : C == 16 ? ((pl & 1) + 2 * ((pl >> 1) + 2 * ((lane >> 2) & 1))) * 16
-                                        : (pl + 4 * ((lane >> 2) & 1)) * 16;
-        const unsigned char *tab = smem + P::offTable + copy;
-        const float4 *turn = reinterpret_cast<const float4 *>(smem + P::offTurn);
-        const int kmax = a.K - 1;
-        auto load_words = [&](int t, uint32_t (&wd)[IT][NW]) {
-            const int n = tok_first + t * NT + rw * 8 + tl;
-#pragma unroll
-            for (int it = 0; it < IT; ++it)
-#pragma unroll
-                for (int k = 0; k < NW; ++k) {
-                    const int piece = it * 4 + pl;
-                    const int p = C == 4 ? piece * 2 + k : piece / (C / 8);
-                    wd[it][k] = (t < ntiles && n >= st && n < len) ? __ldg(idx + idx_word(n, p, NP)) : 0u;
-                }
-        };
-        // 8 channels of piece `piece` (half 0: the low channels, 1: their partners) from the codes of its words
-        auto gather = [&](int kv, int half, int piece, const uint32_t (&wd)[NW]) -> uint4 {
-            const int sh = kv * 16 + half * 8;
-            uint4 v;
-            const uint16_t *gsl = (kv ? a.slv : a.slk) + (size_t)h * a.K * D;
-            if constexpr (C == 4) {
-                const int c0 = (wd[0] >> sh) & 255, c1 = (wd[NW - 1] >> sh) & 255;
-                uint2 x, y;
-                if constexpr (PG) {
-                    const int g = half * NP + piece * 2;
-                    x = __ldg(reinterpret_cast<const uint2 *>(gsl + (size_t)min(c0, kmax) * D + g * C));
-                    y = __ldg(reinterpret_cast<const uint2 *>(gsl + (size_t)min(c1, kmax) * D + (g + 1) * C));
-                } else {
-                    x = *reinterpret_cast<const uint2 *>(tab + kv * P::kTable + c0 * 128);
-                    y = *reinterpret_cast<const uint2 *>(tab + kv * P::kTable + c1 * 128);
-                }
-                v = make_uint4(x.x, x.y, y.x, y.y);
-            } else {
-                const int c0 = (wd[0] >> sh) & 255;
-                if constexpr (PG) {
-                    const int g = half * NP + piece / (C / 8);
-                    v = __ldg(reinterpret_cast<const uint4 *>(gsl + (size_t)min(c0, kmax) * D + g * C + piece % (C / 8) * 8));
-                } else {
-                    v = *reinterpret_cast<const uint4 *>(tab + kv * P::kTable + c0 * 128);
-                }
-            }
-            return v;
-        };
-        uint32_t wd[IT][NW], nx[IT][NW];
-        load_words(0, wd);
-        load_words(1, nx);
-        float2 cs[IT][4], sn[IT][4];                                 // of this lane's token and channels
-        for (int t = 0; t < ntiles; ++t) {
-            const int s = t % ST;
-            const int nl = rw * 8 + tl, n = tok_first + t * NT + nl;
-            const bool in = n >= st && n < len;
-            uint32_t n2[IT][NW];
-            load_words(t + 2, n2);                                   // two tiles ahead: a tile is shorter than a load
-            if (t % kAnchor == 0) {
-                const float4 *row = reinterpret_cast<const float4 *>(a.rope + (size_t)(n < len ? n : tok0) * D);
-#pragma unroll
-                for (int it = 0; it < IT; ++it)
-#pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        const float4 c = __ldg(row + (it * 4 + pl) * 2 + k), x = __ldg(row + D / 8 + (it * 4 + pl) * 2 + k);
-                        cs[it][2 * k] = f2(c.x, c.y);
-                        cs[it][2 * k + 1] = f2(c.z, c.w);
-                        sn[it][2 * k] = f2(x.x, x.y);
-                        sn[it][2 * k + 1] = f2(x.z, x.w);
-                    }
-            }
-            if (t >= ST) {
-                const bool ok = tc::mbar_wait_or_dead(vempty(s), (t / ST - 1) & 1, a.wait_ns, dead);
-                if (!__all_sync(0xffffffffu, ok)) break;
-            }
-            const uint32_t kb = sStage + s * P::kStage, vb = kb + KP * P::kTile;
-#pragma unroll
-            for (int it = 0; it < IT; ++it) {
-                const int piece = it * 4 + pl;
-                const uint4 z = make_uint4(0, 0, 0, 0);
-                const uint4 k0 = in ? gather(0, 0, piece, wd[it]) : z, k1 = in ? gather(0, 1, piece, wd[it]) : z;
-                const uint4 v0 = in ? gather(1, 0, piece, wd[it]) : z, v1 = in ? gather(1, 1, piece, wd[it]) : z;
-                const uint32_t kl[4] = {k0.x, k0.y, k0.z, k0.w}, kh[4] = {k1.x, k1.y, k1.z, k1.w};
-                uint32_t ah[4], al[4], bh[4], bl[4];                 // rotated: bf16 parts of the low and high channels
-                const float2 minus = f2(-1.f, -1.f);
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const float2 x = unpack2(kl[k]), y = unpack2(kh[k]), ny = unpack2(kh[k] ^ 0x80008000u);
-                    const float2 ra = __ffma2_rn(x, cs[it][k], __fmul2_rn(ny, sn[it][k]));
-                    const float2 rb = __ffma2_rn(y, cs[it][k], __fmul2_rn(x, sn[it][k]));
-                    ah[k] = cvt_bf16x2(ra.y, ra.x);
-                    bh[k] = cvt_bf16x2(rb.y, rb.x);
-                    const float2 da = __ffma2_rn(unpack2(ah[k]), minus, ra), db = __ffma2_rn(unpack2(bh[k]), minus, rb);
-                    al[k] = cvt_bf16x2(da.y, da.x);
-                    bl[k] = cvt_bf16x2(db.y, db.x);
-                }
-                // low channels 8 piece .., high channels D/2 + 8 piece ..
-                const uint32_t lo_at = sw128(nl, piece);
-                const uint32_t hi_at = D == 128 ? P::kPanel + sw128(nl, piece) : sw128(nl, piece + 4);
-                sts128(vb + lo_at, v0);
-                sts128(vb + hi_at, v1);
-                sts128(kb + lo_at, make_uint4(ah[0], ah[1], ah[2], ah[3]));
-                sts128(kb + hi_at, make_uint4(bh[0], bh[1], bh[2], bh[3]));
-                sts128(kb + P::kTile + lo_at, make_uint4(al[0], al[1], al[2], al[3]));
-                sts128(kb + P::kTile + hi_at, make_uint4(bl[0], bl[1], bl[2], bl[3]));
-            }
-            tc::fence_async_smem();
-            __syncwarp();
-            if (lane == 0) tc::mbar_arrive(kfull(s));
-#pragma unroll
-            for (int it = 0; it < IT; ++it)
-#pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    const float4 c64 = turn[(it * 4 + pl) * 2 + k], s64 = turn[D / 8 + (it * 4 + pl) * 2 + k];
-#pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        const float2 c = cs[it][2 * k + j], x = sn[it][2 * k + j];
-                        const float2 tc2 = j ? f2(c64.z, c64.w) : f2(c64.x, c64.y);
-                        const float2 ts2 = j ? f2(s64.z, s64.w) : f2(s64.x, s64.y);
-                        cs[it][2 * k + j] = __ffma2_rn(c, tc2, __fmul2_rn(neg2(x), ts2));
-                        sn[it][2 * k + j] = __ffma2_rn(x, tc2, __fmul2_rn(c, ts2));
-                    }
-                }
-#pragma unroll
-            for (int it = 0; it < IT; ++it)
-#pragma unroll
-                for (int k = 0; k < NW; ++k) {
-                    wd[it][k] = nx[it][k];
-                    nx[it][k] = n2[it][k];
-                }
+        // ---- rebuilding
+        RebuildArgs b;
+        b.idx = a.idx + (size_t)h * a.idx_head;
+        b.slk = a.slk + (size_t)h * a.K * (PG ? D : C);
+        b.slv = a.slv + (size_t)h * a.K * (PG ? D : C);
+        b.rope = a.rope;
+        b.table = smem + P::offTable;
+        b.turn = smem + P::offTurn;
+        b.stages = sStage;
+        b.kfull = kfull(0);
+        b.vfull = vfull(0);
+        b.kempty = kempty(0);
+        b.vempty = vempty(0);
+        b.K = a.K;
+        b.wait_ns = a.wait_ns;
+        b.dead = dead;
+        if (warp < P::kRebuild + 8) {
+            asm volatile("setmaxnreg.inc.sync.aligned.u32 112;");
+            rebuild_keys<D, C, PG, ST>(b, warp - P::kRebuild, tok_first, ntiles, st, len);
+        } else if (warp < P::kValues + 2) {
+            rebuild_values<D, C, PG, ST>(b, warp - P::kValues, tok_first, ntiles, st, len);
         }
     }
 
@@ -696,12 +545,18 @@ __global__ void __launch_bounds__(Plan<D, MB, C, PG>::kThreads, 1)
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols));
 }
 
-// Log-sum-exp merge of the splits' records of every query row, and of another part over other tokens.  The records
-// of a (split, KV head) are R * D / 4 elements of 16 bytes, row fastest; a CTA takes 32 of them, its 8 warps a share of
+struct MergeArgs {
+    const float *ws_o;
+    const float2 *ws_ml;
+    int Hkv, Hq, R, qshift, nrec;
+};
+
+// Log-sum-exp merge of the records of every query row, and of another part over other tokens.  A KV head has R * D / 4
+// elements of 16 bytes in each of nrec records, row fastest or (ROWS) channels fastest; a CTA takes 32 of them, its 8 warps a share of
 // the splits each (all loads of a warp in flight at once: the merge is a chain of latencies, not of bytes), joined
 // through shared memory.  Row r of KV head h is query token r / qpk, head h * qpk + r % qpk.
-template <int D>
-__global__ void __launch_bounds__(256) shared_merge_kernel(const SharedArgs a, const float *other_out,
+template <int D, bool ROWS>
+__global__ void __launch_bounds__(256) shared_merge_kernel(const MergeArgs a, const float *other_out,
                                                            const float *other_lse, float *out, float *lse) {
     constexpr int W = 8, BATCH = 5;
     __shared__ float4 s_acc[W][32];
@@ -711,28 +566,29 @@ __global__ void __launch_bounds__(256) shared_merge_kernel(const SharedArgs a, c
     const size_t id = (size_t)blockIdx.x * 32 + lane;
     const bool live = id < per_head * a.Hkv;
     const int h = live ? (int)(id / per_head) : 0, e = live ? (int)(id % per_head) : 0;
-    const int c4 = e / a.R, r = e % a.R;
-    const size_t dst = (size_t)(r >> a.qshift) * a.Hq + h * a.qpk + (r & (a.qpk - 1));
+    const int c4 = ROWS ? e % (D / 4) : e / a.R, r = ROWS ? e / (D / 4) : e % a.R;
+    const int qpk = 1 << a.qshift;
+    const size_t dst = (size_t)(r >> a.qshift) * a.Hq + h * qpk + (r & (qpk - 1));
     grid_wait();
     const float2 *ml = a.ws_ml + (size_t)h * a.R + r;
     const float4 *o = reinterpret_cast<const float4 *>(a.ws_o) + (size_t)h * per_head + e;
-    const size_t step = (size_t)a.Hkv * a.R;                         // records of the next split
+    const size_t step = (size_t)a.Hkv * a.R;                         // elements of the next record
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
     float mx = -CUDART_INF_F, sum = 0.f;
     if (live) {
-        for (int i0 = warp; i0 < a.nsplit; i0 += W * BATCH) {
+        for (int i0 = warp; i0 < a.nrec; i0 += W * BATCH) {
             float2 x[BATCH];
             float4 y[BATCH];
 #pragma unroll
             for (int k = 0; k < BATCH; ++k) {
-                const size_t i = (size_t)min(i0 + k * W, a.nsplit - 1) * step;
+                const size_t i = (size_t)min(i0 + k * W, a.nrec - 1) * step;
                 x[k] = ml[i];
                 y[k] = o[i * (D / 4)];
             }
             float top = mx;
 #pragma unroll
             for (int k = 0; k < BATCH; ++k) {
-                if (i0 + k * W >= a.nsplit) x[k] = f2(-CUDART_INF_F, 0.f);
+                if (i0 + k * W >= a.nrec) x[k] = f2(-CUDART_INF_F, 0.f);
                 top = fmaxf(top, x[k].x);
             }
             if (top == -CUDART_INF_F) continue;
@@ -789,14 +645,20 @@ __global__ void __launch_bounds__(256) shared_merge_kernel(const SharedArgs a, c
         lse[dst] = total == 0.f ? -CUDART_INF_F : (top + log2f(total)) * 0.69314718055994530942f;
 }
 
+// Query rows of a KV head up to which tokens are the products' long side (shared_rows.cuh).
+constexpr int kFewRows = 32, kFewRowsCoded = 16;
+
 struct SharedPlan {
-    int mb, nsplit, nz;
+    bool few;                // shared_rows_kernel; else shared_attn_kernel with mb blocks of 128 rows
+    int mb, nsplit, nz, nrec;
 };
 
 // Splits: a CTA owns an SM (its tiles fill shared memory), so the splits that fill whole waves of 148 CTAs are
 // compared by waves x (tiles per split + set-up), the set-up and drain of a CTA counted as two tiles.
-SharedPlan plan_shared(int Hkv, int R, int max_len, int nt) {
+SharedPlan plan_shared(int Hkv, int R, int max_len, bool coded) {
     SharedPlan p{};
+    const int nt = coded ? 64 : 128;                                 // tokens per tile
+    p.few = R <= (coded ? kFewRowsCoded : kFewRows);
     p.mb = R > 128 ? 2 : 1;
     p.nz = (R + p.mb * 128 - 1) / (p.mb * 128);
     const long units = (long)Hkv * p.nz, tiles = (max_len + nt - 1) / nt;
@@ -812,13 +674,14 @@ SharedPlan plan_shared(int Hkv, int R, int max_len, int nt) {
             p.nsplit = (int)ns;
         }
     }
+    p.nrec = p.few ? 2 * p.nsplit : p.nsplit;                        // its two streams write a record each
     return p;
 }
 
 size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 
 size_t ws_bytes(const SharedPlan &p, size_t RT, int D) {
-    return align256(p.nsplit * RT * D * sizeof(float)) + p.nsplit * RT * sizeof(float2);
+    return align256(p.nrec * RT * D * sizeof(float)) + p.nrec * RT * sizeof(float2);
 }
 
 // cuTensorMapEncodeTiled through the runtime: the library does not link the driver.
@@ -864,20 +727,71 @@ cudaError_t launch_t(const SharedArgs &a, const SharedPlan &p, const CUtensorMap
     return launch_pdl(kern, dim3(p.nsplit, a.Hkv, p.nz), PL::kThreads, PL::kAlloc, s, a, km, vm);
 }
 
+template <int D, int NR, int C, bool PG, bool SCORES = false>
+cudaError_t launch_rows_t(const RowsArgs &a, const CUtensorMap &km, const CUtensorMap &vm, cudaStream_t s) {
+    using PL = RowsPlan<D, NR, C, PG>;
+    auto kern = shared_rows_kernel<D, NR, C, PG, SCORES>;
+    cudaError_t e = ensure_dynamic_smem((const void *)kern, PL::kAlloc);
+    if (e != cudaSuccess) return e;
+    const long items = (long)a.seqs * a.Hkv * a.nsplit;              // a coded cache: one KV head's slices per CTA
+    const unsigned grid = (unsigned)(C != 0 || items < 148 ? items : 148);
+    return launch_pdl(kern, dim3(grid), PL::kThreads, PL::kAlloc, s, a, km, vm);
+}
+
+RowsArgs rows_args(const SharedArgs &a) {
+    RowsArgs r{};
+    r.q = a.q;
+    r.starts = a.start;
+    r.lens = a.len;
+    r.ws_o = a.ws_o;
+    r.ws_ml = a.ws_ml;
+    r.seqs = 1;
+    r.Hkv = a.Hkv;
+    r.Hq = a.Hq;
+    r.R = a.R;
+    r.qshift = a.qshift;
+    r.max_len = a.max_len;
+    r.nsplit = a.nsplit;
+    r.sh = (size_t)a.R;
+    r.sr = 1;
+    r.ss = (size_t)a.Hkv * a.R;
+    r.qscale = a.qscale;
+    r.fault = a.fault;
+    r.wait_ns = a.wait_ns;
+    r.head_rows = a.head_rows;
+    r.idx = a.idx;
+    r.idx_head = a.idx_head;
+    r.slk = a.slk;
+    r.slv = a.slv;
+    r.rope = a.rope;
+    r.K = a.K;
+    return r;
+}
+
+template <int D, int C, bool PG>
+cudaError_t launch_p(const SharedArgs &a, const SharedPlan &p, const CUtensorMap &km, const CUtensorMap &vm,
+                     cudaStream_t s) {
+    if (p.few)
+        return a.R <= 16 ? launch_rows_t<D, 16, C, PG>(rows_args(a), km, vm, s)
+                         : launch_rows_t<D, 32, C, PG>(rows_args(a), km, vm, s);
+    return p.mb == 2 ? launch_t<D, 2, C, PG>(a, p, km, vm, s) : launch_t<D, 1, C, PG>(a, p, km, vm, s);
+}
+
 template <int C, bool PG>
 cudaError_t launch_d(int D, const SharedArgs &a, const SharedPlan &p, const CUtensorMap &km, const CUtensorMap &vm,
                      cudaStream_t s) {
-    if (D == 128)
-        return p.mb == 2 ? launch_t<128, 2, C, PG>(a, p, km, vm, s) : launch_t<128, 1, C, PG>(a, p, km, vm, s);
-    if (D == 64) return p.mb == 2 ? launch_t<64, 2, C, PG>(a, p, km, vm, s) : launch_t<64, 1, C, PG>(a, p, km, vm, s);
+    if (D == 128) return launch_p<128, C, PG>(a, p, km, vm, s);
+    if (D == 64) return launch_p<64, C, PG>(a, p, km, vm, s);
     return cudaErrorInvalidValue;
 }
 
-cudaError_t finish(const SharedArgs &a, int D, const SharedOther &o, float *out, float *lse,
+cudaError_t finish(const SharedArgs &a, const SharedPlan &p, int D, const SharedOther &o, float *out, float *lse,
                    cudaStream_t s) {
     const unsigned blocks = (unsigned)(((size_t)a.rows * a.Hq * (D / 4) + 31) / 32);
-    return launch_pdl(D == 128 ? shared_merge_kernel<128> : shared_merge_kernel<64>, dim3(blocks), 256, 0, s, a, o.out,
-                      o.lse, out, lse);
+    const MergeArgs m{a.ws_o, a.ws_ml, a.Hkv, a.Hq, a.R, a.qshift, p.nrec};
+    auto kern = D == 128 ? (p.few ? shared_merge_kernel<128, true> : shared_merge_kernel<128, false>)
+                         : (p.few ? shared_merge_kernel<64, true> : shared_merge_kernel<64, false>);
+    return launch_pdl(kern, dim3(blocks), 256, 0, s, m, o.out, o.lse, out, lse);
 }
 
 SharedArgs common_args(int rows, int Hkv, int Hq, int D, const SharedPlan &p, const uint16_t *q, const int32_t *start,
@@ -897,7 +811,7 @@ SharedArgs common_args(int rows, int Hkv, int Hq, int D, const SharedPlan &p, co
     a.qscale = scale * 1.44269504088896340736f;
     a.ws_o = reinterpret_cast<float *>(workspace);
     a.ws_ml = reinterpret_cast<float2 *>(reinterpret_cast<char *>(workspace) +
-                                         align256(p.nsplit * (size_t)rows * Hq * D * sizeof(float)));
+                                         align256(p.nrec * (size_t)rows * Hq * D * sizeof(float)));
     a.wait_ns = wait_limit_ns();
     return a;
 }
@@ -905,13 +819,13 @@ SharedArgs common_args(int rows, int Hkv, int Hq, int D, const SharedPlan &p, co
 }  // namespace
 
 size_t shared_ws_bytes(int Hkv, int Hq, int D, int rows, int max_len, bool coded) {
-    return ws_bytes(plan_shared(Hkv, rows * (Hq / Hkv), max_len, coded ? 64 : 128), (size_t)rows * Hq, D);
+    return ws_bytes(plan_shared(Hkv, rows * (Hq / Hkv), max_len, coded), (size_t)rows * Hq, D);
 }
 
 cudaError_t launch_bf16_shared(const loopvq_bf16_cache &c, int seq, const uint16_t *q, int rows, const int32_t *starts,
                                const int32_t *lens, int max_len, float scale, const SharedOther &other, float *out,
                                float *lse, void *workspace, cudaStream_t s) {
-    const SharedPlan p = plan_shared(c.Hkv, rows * (c.Hq / c.Hkv), max_len, 128);
+    const SharedPlan p = plan_shared(c.Hkv, rows * (c.Hq / c.Hkv), max_len, false);
     SharedArgs a = common_args(rows, c.Hkv, c.Hq, c.D, p, q, starts ? starts + seq : nullptr, lens + seq, max_len, scale,
                                workspace);
     cudaError_t e = fault_word_for_current_device(&a.fault);
@@ -923,13 +837,13 @@ cudaError_t launch_bf16_shared(const loopvq_bf16_cache &c, int seq, const uint16
     if (e == cudaSuccess) e = make_map(&vm, c.v + at, map_rows, c.D, 128);
     if (e == cudaSuccess) e = launch_d<0, false>(c.D, a, p, km, vm, s);
     if (e != cudaSuccess) return e;
-    return finish(a, c.D, other, out, lse, s);
+    return finish(a, p, c.D, other, out, lse, s);
 }
 
 cudaError_t launch_shared(const loopvq_cache &cc, int layer, int t, int seq, const uint16_t *q, int rows,
                           const int32_t *starts, const int32_t *lens, int max_len, float scale,
                           const SharedOther &other, float *out, float *lse, void *workspace, cudaStream_t s) {
-    const SharedPlan p = plan_shared(cc.Hkv, rows * (cc.Hq / cc.Hkv), max_len, 64);
+    const SharedPlan p = plan_shared(cc.Hkv, rows * (cc.Hq / cc.Hkv), max_len, true);
     SharedArgs a = common_args(rows, cc.Hkv, cc.Hq, cc.D, p, q, starts ? starts + seq : nullptr, lens + seq, max_len,
                                scale, workspace);
     cudaError_t e = fault_word_for_current_device(&a.fault);
@@ -950,7 +864,7 @@ cudaError_t launch_shared(const loopvq_cache &cc, int layer, int t, int seq, con
         default: return cudaErrorInvalidValue;
     }
     if (e != cudaSuccess) return e;
-    return finish(a, cc.D, other, out, lse, s);
+    return finish(a, p, cc.D, other, out, lse, s);
 }
 
 }  // namespace loopvq

@@ -1,0 +1,656 @@
+// Attention of few query rows over one sequence's tokens with the tokens along the tensor cores' long side.
+//
+// A tensor-core product has 128 rows (M) whether they are used or not, and its time goes with its columns (N).  For up
+// to 32 query rows of a KV head the tokens are the rows and the queries the columns:
+//   S^T [tokens x rows] = K Q^T,   O^T [channels x rows] = V^T P^T,
+// so that a tile of 128 tokens costs products of 16 or 32 columns instead of 128, and the softmax of a tile is spread
+// over 128 threads (thread = token = tensor-memory lane) instead of one thread per row.
+//
+// What differs from the kernel with rows as M:
+//  - P^T is an operand from shared memory: every thread writes its token's row of 16 or 32 probabilities, each in three
+//    bf16 parts (24 bits, all of an fp32 probability), side by side as columns.  The parts meet the same values in one
+//    product and have accumulators of their own, added when the result is read: V is read once for all of them, and the
+//    small parts are not cut to the large one's last place.
+//  - A row's maximum would be a reduction over lanes.  Any reference is exact, and fp32 and bf16 have 8 exponent bits, so
+//    the reference only has to keep exp2 in range: it is the score of a stream's first token and moves only when some
+//    score passes it by 2^40, which the warps of a stream agree on with one barrier vote per tile.
+//  - Sums are kept per (thread, row) and added over the lanes at the end (a product of ones and P would give them too, at
+//    8 more products a tile; every product takes 46 clocks or more, however few its columns).
+//
+// A CTA works through items (sequence, KV head, split) with its copies running ahead across them, so that a batch of
+// ragged sequences keeps every SM's copies in flight.  Warps: 0-3 and 4-7 softmax of the two streams that take the tiles
+// in turn; then the products' issuing warp, the copying one (bf16 cache: TMA; coded cache: eight warps that rebuild keys, two that rebuild values) and
+// one that loads the queries.
+#pragma once
+
+#include <cuda.h>
+
+#include "shared_rebuild.cuh"
+
+namespace loopvq {
+
+struct RowsArgs {
+    const uint16_t *q;               // [sequence][query token][Hq][D]
+    const int32_t *starts, *lens;    // of the sequences (starts may be null)
+    float *ws_o;                     // [record][D]
+    float2 *ws_ml;                   // [record]: maximum reference (log2 units), sum
+    float *ws_s;                     // scores in log2 units [sequence][Hq][sstride], or null
+    int sstride;
+    int seqs, Hkv, Hq, R, qshift;    // R = query rows per (sequence, KV head)
+    int max_len, nsplit;
+    int split_tiles;                 // tiles per split, or 0: a sequence's tiles in nsplit equal shares
+    // record of stream w of (sequence, KV head, split), row r: seq * sb + h * sh + r * sr + (2 * split + w) * ss
+    size_t sb, sh, sr, ss;
+    float qscale;                    // scale * log2(e)
+    unsigned int *fault;
+    unsigned long long wait_ns;
+    int head_rows, seq_rows;         // bf16 cache: rows of the tensor maps per KV head and per sequence
+    const uint32_t *idx;             // coded cache: as in SharedArgs
+    size_t idx_head;
+    const uint16_t *slk, *slv;
+    const float *rope;
+    int K;
+};
+
+// NT tokens per tile; KP bf16 parts per key; NR columns; three parts of P.
+template <int D, int NR, int C, bool PG>
+struct RowsPlan {
+    static constexpr bool coded = C != 0;
+    static constexpr int NT = coded ? 64 : 128;
+    static constexpr int KP = coded ? 2 : 1;
+    static constexpr int PARTS = 3;
+    static constexpr int kPanel = NT * 128;
+    static constexpr int kTile = (D / 64) * kPanel;
+    static constexpr int kStage = (KP + 1) * kTile;
+    static constexpr int kPart = NT * NR * 2;                        // one part of P
+    static constexpr int kP = PARTS * kPart;                         // of one stream
+    static constexpr int kQ = (D / 64) * NR * 128;
+    static constexpr int NQ = coded ? 1 : 2;                         // buffers of queries
+    static constexpr int ST = D == 64 ? 4 : coded || NR == 16 ? 3 : 2;
+    static constexpr int kTable = coded && !PG ? kTableBytes : 0;
+    static constexpr int offStage = 0;
+    static constexpr int offP = ST * kStage;
+    static constexpr int offQ = offP + 2 * kP;
+    static constexpr int offTable = offQ + NQ * kQ;
+    static constexpr int offTurn = offTable + 2 * kTable;
+    static constexpr int offRef = offTurn + (coded ? D * 4 : 0);     // per stream: references, their moves, maxima
+    static constexpr int kRef = 6 * NR * 4 + 16;
+    static constexpr int offBar = offRef + 2 * kRef;
+    static constexpr int kBars = 4 * ST + 2 * NQ + 7;
+    static constexpr int offTmem = offBar + kBars * 8;
+    static constexpr int kUsed = offTmem + 16;
+    static constexpr int kAlloc = kUsed + 1024;
+    static constexpr int kMma = coded ? 16 : 8, kCopy = 9, kRebuild = 8, kValues = 17, kQuery = coded ? 19 : 10;
+    static constexpr int kThreads = (kQuery + 1) * 32;
+    static constexpr int kCols = 256;                                // stream w: S at 32 w, O at 64 + 96 w
+    static_assert(kAlloc <= 232448, "shared memory");
+    static_assert(offStage % 1024 == 0 && offP % 1024 == 0 && offQ % 1024 == 0 && kP % 512 == 0, "swizzle atoms");
+    static_assert(PARTS * NR <= 96, "tensor memory");
+};
+
+// The row of P^T of token n: 16-byte chunk c of NR columns, swizzled by rows of 32 (NR = 16) or 64 (NR = 32) bytes.
+template <int NR>
+__device__ __forceinline__ uint32_t p_chunk(int n, int c) {
+    if constexpr (NR == 16) return (uint32_t)n * 32u + ((uint32_t)(c ^ ((n >> 2) & 1)) << 4);
+    else return (uint32_t)n * 64u + ((uint32_t)(c ^ ((n >> 1) & 3)) << 4);
+}
+
+// Barrier over the 128 threads of a stream, with a vote.
+__device__ __forceinline__ bool stream_any(int id, bool p) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.u32 p, %1, 0;\n\t"
+        "barrier.cta.red.or.pred q, %2, 128, p;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(r) : "r"((uint32_t)p), "r"(id) : "memory");
+    return r != 0;
+}
+__device__ __forceinline__ void stream_sync(int id) { asm volatile("barrier.cta.sync %0, 128;" ::"r"(id) : "memory"); }
+
+// fp32 bits as signed integers of the same order
+__device__ __forceinline__ int ordered(float x) {
+    const int i = __float_as_int(x);
+    return i ^ ((i >> 31) & 0x7fffffff);
+}
+__device__ __forceinline__ float unordered(int i) { return __int_as_float(i ^ ((i >> 31) & 0x7fffffff)); }
+
+// SCORES: every attended token's scores are kept (NR = 16 only).
+template <int D, int NR, int C, bool PG, bool SCORES>
+__global__ void __launch_bounds__(RowsPlan<D, NR, C, PG>::kThreads, 1)
+    shared_rows_kernel(const RowsArgs a, const __grid_constant__ CUtensorMap kmap,
+                       const __grid_constant__ CUtensorMap vmap) {
+    using P = RowsPlan<D, NR, C, PG>;
+    constexpr bool coded = C != 0;
+    constexpr int NT = P::NT, KP = P::KP, ST = P::ST, NQ = P::NQ, PARTS = P::PARTS, NPAN = D / 64;
+    constexpr float kFar = 40.f;                                     // log2 units a score may pass the reference by
+
+    extern __shared__ unsigned char smem_raw[];
+    const uint32_t base = (tc::smem_u32(smem_raw) + 1023u) & ~1023u;
+    unsigned char *smem = smem_raw + (base - tc::smem_u32(smem_raw));
+    const uint32_t sStage = base + P::offStage, bars = base + P::offBar;
+    auto kfull = [&](int s) { return bars + 8u * s; };
+    auto vfull = [&](int s) { return bars + 8u * (ST + s); };
+    auto kempty = [&](int s) { return bars + 8u * (2 * ST + s); };
+    auto vempty = [&](int s) { return bars + 8u * (3 * ST + s); };
+    auto qfull = [&](int b) { return bars + 8u * (4 * ST + b); };
+    auto qempty = [&](int b) { return bars + 8u * (4 * ST + NQ + b); };
+    auto sfull = [&](int w) { return bars + 8u * (4 * ST + 2 * NQ + w); };
+    auto pfull = [&](int w) { return bars + 8u * (4 * ST + 2 * NQ + 2 + w); };
+    auto odone = [&](int w) { return bars + 8u * (4 * ST + 2 * NQ + 4 + w); };
+    const uint32_t drain = bars + 8u * (4 * ST + 2 * NQ + 6);
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + P::offTmem);
+    volatile int *dead = reinterpret_cast<volatile int *>(smem + P::offTmem + 4);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tc::uniform_warp();
+
+    grid_trigger();
+    if (!coded && warp == P::kCopy && lane == 0) {
+        tc::prefetch_map(&kmap);
+        tc::prefetch_map(&vmap);
+    }
+    if (warp == P::kMma) {
+        if (lane == 0) {
+            for (int s = 0; s < ST; ++s) {
+                tc::mbar_init(kfull(s), coded ? 8 : 1);
+                tc::mbar_init(vfull(s), coded ? 2 : 1);
+                tc::mbar_init(kempty(s), 1);
+                tc::mbar_init(vempty(s), 1);
+            }
+            for (int b = 0; b < NQ; ++b) {
+                tc::mbar_init(qfull(b), 1);
+                tc::mbar_init(qempty(b), 1);
+            }
+            for (int w = 0; w < 2; ++w) {
+                tc::mbar_init(sfull(w), 1);
+                tc::mbar_init(pfull(w), 128);
+                tc::mbar_init(odone(w), 1);
+            }
+            tc::mbar_init(drain, 1);
+            *dead = 0;
+            asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        }
+        __syncwarp();
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(tc::smem_u32(tmem_slot)),
+                     "r"(P::kCols));
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    }
+    grid_wait();
+    if constexpr (coded) {                                           // an item's KV head is this CTA's: one item per CTA
+        if constexpr (!PG) {
+            const int h = (int)(blockIdx.x / a.nsplit) % a.Hkv;
+            fill_tables<C>(smem + P::offTable, a.slk + (size_t)h * a.K * C, a.slv + (size_t)h * a.K * C, a.K, P::kThreads);
+        }
+        for (int i = tid; i < D; i += P::kThreads)                   // row 64 is there when a second tile is
+            reinterpret_cast<float *>(smem + P::offTurn)[i] = a.max_len > 64 ? a.rope[(size_t)64 * D + i] : 0.f;
+    }
+    // ---- items of this CTA, the same walk in every role
+    struct Item {
+        int b, h, split, st, len, tok_first, ntiles;
+    };
+    const int nitems = coded ? (int)blockIdx.x + 1 : a.seqs * a.Hkv * a.nsplit;   // coded: one item per CTA
+    auto item_at = [&](int i) {
+        Item x;
+        x.split = i % a.nsplit;
+        x.h = i / a.nsplit % a.Hkv;
+        x.b = i / a.nsplit / a.Hkv;
+        x.len = min(max(__ldg(a.lens + x.b), 0), a.max_len);
+        x.st = a.starts ? min(max(__ldg(a.starts + x.b), 0), x.len) : 0;
+        const int tok0 = coded ? (x.st & ~3) : x.st;                 // index words come in tiles of 4 tokens
+        const int tiles = x.len > x.st ? (x.len - tok0 + NT - 1) / NT : 0;
+        int t0, t1;
+        if (a.split_tiles > 0) {
+            t0 = min(x.split * a.split_tiles, tiles);
+            t1 = min(t0 + a.split_tiles, tiles);
+        } else {
+            t0 = (int)((long long)x.split * tiles / a.nsplit);
+            t1 = (int)((long long)(x.split + 1) * tiles / a.nsplit);
+        }
+        x.ntiles = t1 - t0;
+        x.tok_first = tok0 + t0 * NT;
+        return x;
+    };
+    const Item item0 = item_at(blockIdx.x);                          // its lengths' latency runs under the set-up
+    tc::fence_async_smem();
+    tc::tc_fence_before();
+    __syncthreads();
+    tc::tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+
+    if (warp < 8) {
+        // ---- softmax of stream w: 128 threads, one token of a tile each
+        if constexpr (coded) asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+        const int w = warp >> 2, wq = warp & 3, bar = 1 + w;
+        // tile row and channel of this thread's lane: products of 64 rows use the first 16 lanes of every 32
+        const int token = NT == 128 ? wq * 32 + lane : lane < 16 ? wq * 16 + lane : -1;
+        const int chan = D == 128 ? wq * 32 + lane : lane < 16 ? wq * 16 + lane : -1;
+        const uint32_t lanes = tmem + ((uint32_t)(wq * 32) << 16);
+        const uint32_t ts = lanes + w * 32, to = lanes + 64 + w * 96;
+        const uint32_t sp = base + P::offP + w * P::kP;
+        float *ref = reinterpret_cast<float *>(smem + P::offRef + w * P::kRef);   // a row's reference, negated
+        float *corr = ref + NR;
+        float *wmax = ref + 2 * NR;                                  // [4][NR]: a warp's maxima, later its sums
+        volatile int *wok = reinterpret_cast<volatile int *>(ref + 6 * NR);
+        const int cols = (a.R + 15) & ~15;                           // columns in use (padding rows: zero queries)
+        int g = 0;                                                   // tiles of this CTA so far
+        bool ok = true;
+        for (int i = blockIdx.x; i < nitems; i += gridDim.x) {
+            const Item x = i == (int)blockIdx.x ? item0 : item_at(i);
+            const size_t rec = x.b * a.sb + x.h * a.sh + (size_t)(2 * x.split + w) * a.ss;
+            float l[NR];
+#pragma unroll
+            for (int r = 0; r < NR; ++r) l[r] = 0.f;
+            int j = 0;                                               // tiles of this stream in the item
+            for (int t = 0; ok && t < x.ntiles; ++t, ++g) {
+                if ((g & 1) != w) continue;
+                ok = __all_sync(0xffffffffu, tc::mbar_wait_or_dead(sfull(w), (g >> 1) & 1, a.wait_ns, dead));
+                tc::tc_fence_after();
+                const int n = x.tok_first + t * NT + token;
+                const bool in = token >= 0 && n >= x.st && n < x.len;
+                // 16 columns in the exponent's units relative to the reference
+                auto load = [&](int c, float (&v)[16]) {
+                    uint32_t s[16];
+                    tc::tmem_ld16(ts + c, s);
+                    tc::tmem_wait_ld16(s);
+#pragma unroll
+                    for (int k = 0; k < 16; k += 4) {
+                        const float4 nr = *reinterpret_cast<const float4 *>(ref + c + k);
+                        v[k] = fmaf(__uint_as_float(s[k]), a.qscale, nr.x);
+                        v[k + 1] = fmaf(__uint_as_float(s[k + 1]), a.qscale, nr.y);
+                        v[k + 2] = fmaf(__uint_as_float(s[k + 2]), a.qscale, nr.z);
+                        v[k + 3] = fmaf(__uint_as_float(s[k + 3]), a.qscale, nr.w);
+                    }
+                };
+                if (j == 0) {
+                    // an item's first tile: its first attended token gives the reference (0 if its score is no number)
+                    if (ok && wq == 0) {
+#pragma unroll 1
+                        for (int c = 0; c < cols; c += 16) {
+                            uint32_t s[16];
+                            tc::tmem_ld16(ts + c, s);
+                            tc::tmem_wait_ld16(s);
+                            if (token == max(x.st - (x.tok_first + t * NT), 0)) {
+#pragma unroll
+                                for (int k = 0; k < 16; ++k) {
+                                    const float v = __uint_as_float(s[k]) * a.qscale;
+                                    ref[c + k] = fabsf(v) < CUDART_INF_F ? -v : 0.f;
+                                }
+                            }
+                        }
+                    }
+                    stream_sync(bar);
+                }
+                float top = 0.f;
+                if (ok) {
+#pragma unroll
+                    for (int c = 0; c < NR; c += 16) {
+                        if (c < cols) {
+                            float v[16];
+                            load(c, v);
+#pragma unroll
+                            for (int k = 0; k < 16; ++k) top = fmaxf(top, v[k]);
+                        }
+                    }
+                }
+                if (stream_any(bar, !ok || (in && top > kFar))) {
+                    // rare: move the references to the maxima of this tile, and what was summed with them
+                    if (lane == 0) wok[wq] = ok;
+                    if (ok) {
+#pragma unroll 1
+                        for (int c = 0; c < cols; c += 16) {
+                            float v[16];
+                            load(c, v);
+#pragma unroll
+                            for (int k = 0; k < 16; ++k) {
+                                const int m = __reduce_max_sync(0xffffffffu, in ? ordered(v[k]) : ordered(0.f));
+                                if (lane == 0) wmax[wq * NR + c + k] = unordered(m);
+                            }
+                        }
+                    }
+                    stream_sync(bar);
+                    ok = wok[0] && wok[1] && wok[2] && wok[3];
+                    if (!ok) break;                                  // every warp of the stream alike
+                    const int r = tid % 128;
+                    if (r < cols) {                                  // how far the row's reference rises
+                        const float up = fmaxf(fmaxf(fmaxf(wmax[r], wmax[NR + r]), fmaxf(wmax[2 * NR + r], wmax[3 * NR + r])), 0.f);
+                        corr[r] = ex2(-up);
+                        ref[r] -= up;
+                    }
+                    stream_sync(bar);
+#pragma unroll
+                    for (int r2 = 0; r2 < NR; ++r2)
+                        if (r2 < cols) l[r2] *= corr[r2];
+                    if (j > 0) {
+                        bool done = tc::mbar_wait_or_dead(odone(w), ((g >> 1) - 1) & 1, a.wait_ns, dead);
+                        done = __all_sync(0xffffffffu, done);
+                        if (stream_any(bar, !done)) {
+                            ok = false;
+                            break;
+                        }
+                        tc::tc_fence_after();
+#pragma unroll 1
+                        for (int c = 0; c < PARTS * NR; c += 16) {
+                            uint32_t o[16];
+                            tc::tmem_ld16(to + c, o);
+                            tc::tmem_wait_ld16(o);
+#pragma unroll
+                            for (int k = 0; k < 16; ++k)
+                                o[k] = __float_as_uint(__uint_as_float(o[k]) * corr[(c + k) % NR]);
+                            tc::tmem_st16(to + c, o);
+                        }
+                        tc::tmem_wait_st();
+                    }
+                }
+                if constexpr (SCORES) {
+                    uint32_t s[16];
+                    tc::tmem_ld16(ts, s);
+                    tc::tmem_wait_ld16(s);
+                    float *sc = a.ws_s + ((size_t)x.b * a.Hq + x.h * a.R) * a.sstride + n;
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        if (in && k < a.R) sc[(size_t)k * a.sstride] = __uint_as_float(s[k]) * a.qscale;
+                }
+#pragma unroll
+                for (int c = 0; c < NR; c += 16) {
+                    if (c < cols) {
+                        float v[16];
+                        load(c, v);
+#pragma unroll
+                        for (int half = 0; half < 2; ++half) {
+                            uint32_t p1[4], p2[4], p3[4];
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) {
+                                float2 p = f2(ex2(v[half * 8 + 2 * k]), ex2(v[half * 8 + 2 * k + 1]));
+                                if (!in) p = f2(0.f, 0.f);
+                                l[c + half * 8 + 2 * k] += p.x;
+                                l[c + half * 8 + 2 * k + 1] += p.y;
+                                p1[k] = cvt_bf16x2(p.y, p.x);
+                                const float2 d = f2(p.x - bf16lo(p1[k]), p.y - bf16hi(p1[k]));
+                                p2[k] = cvt_bf16x2(d.y, d.x);
+                                p3[k] = cvt_bf16x2(d.y - bf16hi(p2[k]), d.x - bf16lo(p2[k]));
+                            }
+                            if (token >= 0) {
+                                const uint32_t at = sp + p_chunk<NR>(token, c / 8 + half);
+                                sts128(at, make_uint4(p1[0], p1[1], p1[2], p1[3]));
+                                sts128(at + P::kPart, make_uint4(p2[0], p2[1], p2[2], p2[3]));
+                                sts128(at + 2 * P::kPart, make_uint4(p3[0], p3[1], p3[2], p3[3]));
+                            }
+                        }
+                    }
+                }
+                tc::fence_async_smem();
+                tc::tc_fence_before();
+                tc::mbar_arrive(pfull(w));
+                ++j;
+            }
+            if (ok && j > 0) {
+                // the item's last step of this stream: g counts tiles of both
+                const int last = (g - 1 - (((g - 1) & 1) != w)) >> 1;
+                ok = __all_sync(0xffffffffu, tc::mbar_wait_or_dead(odone(w), last & 1, a.wait_ns, dead));
+                tc::tc_fence_after();
+            }
+            // sums over the lanes, scattered so that lane r ends with row r; then the records: (reference, sum), and
+            // channels in runs of 128 bytes
+#pragma unroll
+            for (int o = NR / 2; o >= 1; o >>= 1) {
+#pragma unroll
+                for (int r = 0; r < o; ++r) {
+                    const bool up = (lane & o) != 0;
+                    const float keep = up ? l[o + r] : l[r], give = up ? l[r] : l[o + r];
+                    l[r] = keep + __shfl_xor_sync(0xffffffffu, give, o);
+                }
+            }
+            if constexpr (NR == 16) l[0] += __shfl_xor_sync(0xffffffffu, l[0], 16);
+            if (lane < NR) wmax[wq * NR + lane] = l[0];
+            if (lane == 0) wok[wq] = ok;
+            stream_sync(bar);
+            const bool all_ok = wok[0] && wok[1] && wok[2] && wok[3];
+            if (tid % 128 < a.R) {
+                const int r = tid % 128;
+                const float sum = wmax[r] + wmax[NR + r] + wmax[2 * NR + r] + wmax[3 * NR + r];
+                // (a row whose every score is -inf has no weight)
+                a.ws_ml[rec + r * a.sr] = !all_ok             ? f2(0.f, CUDART_NAN_F)
+                                          : j > 0 && sum != 0.f ? f2(-ref[r], sum)
+                                                              : f2(-CUDART_INF_F, 0.f);
+            }
+            if (all_ok && j > 0) {
+#pragma unroll 1
+                for (int c = 0; c < cols; c += 16) {
+                    uint32_t o[16], y[16], z[16];
+                    tc::tmem_ld16(to + c, o);
+                    tc::tmem_ld16(to + NR + c, y);
+                    tc::tmem_ld16(to + 2 * NR + c, z);
+                    tc::tmem_wait_ld16(o);
+                    tc::tmem_wait_ld16(y);
+                    tc::tmem_wait_ld16(z);
+                    float *dst = a.ws_o + (rec + c * a.sr) * D + chan;
+                    const size_t step = a.sr * D;
+#pragma unroll
+                    for (int k = 0; k < 16; ++k)
+                        if (chan >= 0 && c + k < a.R)
+                            dst[k * step] = __uint_as_float(o[k]) + (__uint_as_float(y[k]) + __uint_as_float(z[k]));
+                }
+            }
+            tc::tc_fence_before();
+            stream_sync(bar);                                        // the next item writes ref again
+            ok = all_ok;
+            if (!ok) {                                               // the records of the items left: NaN
+                for (int i2 = i + gridDim.x; i2 < nitems; i2 += gridDim.x) {
+                    const Item z = item_at(i2);
+                    if (tid % 128 < a.R)
+                        a.ws_ml[z.b * a.sb + z.h * a.sh + (tid % 128) * a.sr + (size_t)(2 * z.split + w) * a.ss] =
+                            f2(0.f, CUDART_NAN_F);
+                }
+                break;
+            }
+        }
+    } else if (warp == P::kMma) {
+        // ---- products.  QK of step g + 2 follows PV of step g: S and P of its stream are free then
+        constexpr uint32_t id_qk = tc::idesc_bf16(NT, NR);
+        constexpr uint32_t id_pv = tc::idesc_bf16(D, PARTS * NR) | (1u << 15) | (1u << 16);   // both: contraction outside
+        int total = 0, items = 0;                                    // what will not be used again is not freed
+        for (int i = blockIdx.x + lane * gridDim.x; i < nitems; i += 32 * gridDim.x) {
+            const int nt = item_at(i).ntiles;
+            total += nt;
+            items += nt > 0;
+        }
+#pragma unroll
+        for (int o = 16; o >= 1; o >>= 1) {
+            total += __shfl_xor_sync(0xffffffffu, total, o);
+            items += __shfl_xor_sync(0xffffffffu, items, o);
+        }
+        auto ready = [&](uint32_t b, uint32_t parity) { return __all_sync(0xffffffffu, tc::mbar_test(b, parity)); };
+        // two walks over the tiles: S runs up to two steps ahead
+        struct Walk {
+            int i, it, t, ntiles, end;                               // item, its number among those with tiles; tile,
+        };                                                           // tiles, tokens from the first to the length
+        auto next_item = [&](Walk &v) {
+            for (v.i += gridDim.x; v.i < nitems; v.i += gridDim.x) {
+                const Item x = v.i == (int)blockIdx.x ? item0 : item_at(v.i);
+                v.ntiles = x.ntiles;
+                v.end = x.len - x.tok_first;
+                if (x.ntiles > 0) break;
+            }
+            v.t = 0;
+            ++v.it;
+        };
+        Walk s, p;
+        s.i = (int)blockIdx.x - (int)gridDim.x;
+        s.it = -1;
+        next_item(s);
+        p = s;
+        auto qk = [&](int g) {
+            const int sg = g % ST;
+            if (s.t == 0 && !ready(qfull(s.it % NQ), (s.it / NQ) & 1)) return false;
+            if (!ready(kfull(sg), (g / ST) & 1)) return false;
+            tc::tc_fence_after();
+            const bool last = s.t + 1 == s.ntiles;
+            if (tc::elect_one()) {
+                constexpr uint32_t hi = tc::desc_hi(1024, 2);
+                const uint32_t k_lo = tc::desc_lo(sStage + sg * P::kStage, 16);
+                const uint32_t q_lo = tc::desc_lo(base + P::offQ + (s.it % NQ) * P::kQ, 16);
+#pragma unroll
+                for (int part = 0; part < KP; ++part)
+#pragma unroll
+                    for (int k = 0; k < D / 16; ++k)                 // 16 channels per product: 32 bytes of a row
+                        tc::mma_ss(tmem + (g & 1) * 32,
+                                   k_lo + (part * P::kTile + (k / 4) * P::kPanel + (k % 4) * 32) / 16, hi,
+                                   q_lo + ((k / 4) * (NR * 128) + (k % 4) * 32) / 16, hi, id_qk, part + k > 0);
+                if (g + ST < total) tc::mma_commit(kempty(sg));
+                if (last && s.it + NQ < items) tc::mma_commit(qempty(s.it % NQ));
+                tc::mma_commit(sfull(g & 1));
+            }
+            __syncwarp();
+            if (last) next_item(s);
+            else ++s.t;
+            return true;
+        };
+        auto pv = [&](int g) {
+            const int sg = g % ST, w = g & 1;
+            const uint32_t vb = sStage + sg * P::kStage + KP * P::kTile;
+            if (!ready(pfull(w), (g >> 1) & 1) || !ready(vfull(sg), (g / ST) & 1)) return false;
+            if constexpr (!coded) {
+                // rows behind the last token may hold anything: 0 x that has to be 0
+                const int end = p.end - p.t * NT;
+                if (end < NT) {
+                    for (int it = lane; it < (NT - end) * (D / 8); it += 32) {
+                        const int n = end + it / (D / 8), ch = it % (D / 8);
+                        sts128(vb + (ch / 8) * P::kPanel + n * 128 + (ch % 8) * 16, make_uint4(0, 0, 0, 0));
+                    }
+                    tc::fence_async_smem();
+                    __syncwarp();
+                }
+            }
+            tc::tc_fence_after();
+            if (tc::elect_one()) {
+                const uint32_t p_lo = tc::desc_lo(base + P::offP + w * P::kP, P::kPart), v_lo = tc::desc_lo(vb, P::kPanel);
+                const bool first = p.t < 2;                          // of this stream in the item: O holds nothing yet
+#pragma unroll
+                for (int k = 0; k < NT / 16; ++k)                    // 16 tokens per product
+                    tc::mma_ss(tmem + 64 + w * 96, v_lo + k * 128, tc::desc_hi(1024, 2), p_lo + k * (2 * NR),
+                               tc::desc_hi(8 * NR * 2, NR == 16 ? 6 : 4), id_pv, !first || k > 0);
+                if (g + ST < total) tc::mma_commit(vempty(sg));
+                tc::mma_commit(odone(w));
+            }
+            __syncwarp();
+            if (p.t + 1 == p.ntiles) next_item(p);
+            else ++p.t;
+            return true;
+        };
+        // whichever product is ready goes first: one that waits for its copy must not hold up another whose tile,
+        // once read, makes room for the next copy
+        int gs = 0, gp = 0;
+        uint64_t t0 = tc::globaltimer();
+        while (gp < total) {
+            bool went = gs < total && gs < gp + 2 && qk(gs);
+            gs += went;
+            if (gp < gs && pv(gp)) {
+                ++gp;
+                went = true;
+            }
+            if (went) {
+                t0 = tc::globaltimer();
+            } else if (*dead || tc::globaltimer() - t0 > a.wait_ns) {
+                *dead = 1;
+                break;
+            }
+        }
+    } else if (warp == P::kQuery) {
+        // ---- queries: NR rows (those past R zero), swizzled rows of 64 channels
+        int it = 0;
+        for (int i = blockIdx.x; i < nitems; i += gridDim.x) {
+            const Item x = i == (int)blockIdx.x ? item0 : item_at(i);
+            if (x.ntiles == 0) continue;
+            if (it >= NQ &&
+                !__all_sync(0xffffffffu, tc::mbar_wait_or_dead(qempty(it % NQ), (it / NQ - 1) & 1, a.wait_ns, dead)))
+                break;
+            const uint32_t qb = base + P::offQ + (it % NQ) * P::kQ;
+            const int tokens = a.R >> a.qshift, qpk = 1 << a.qshift;
+            for (int e = lane; e < NR * (D / 8); e += 32) {
+                const int r = e / (D / 8), ch = e % (D / 8);
+                const bool real = r < a.R;
+                const uint16_t *src =
+                    a.q + (((size_t)x.b * tokens + (r >> a.qshift)) * a.Hq + x.h * qpk + (r & (qpk - 1))) * D + ch * 8;
+                cp_async16_zfill(qb + (ch / 8) * (NR * 128) + sw128(r, ch % 8), real ? src : a.q, real);
+            }
+            cp_async_commit();
+            cp_async_wait<0>();
+            tc::fence_async_smem();
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(qfull(it % NQ));
+            ++it;
+        }
+    } else if constexpr (!coded) {
+        // ---- copies
+        if (lane == 0) {
+            int g = 0;
+            bool ok = true;
+            for (int i = blockIdx.x; ok && i < nitems; i += gridDim.x) {
+                const Item x = i == (int)blockIdx.x ? item0 : item_at(i);
+                const int y = x.b * a.seq_rows + x.h * a.head_rows + x.tok_first;
+                for (int t = 0; t < x.ntiles; ++t, ++g) {
+                    const int sg = g % ST;
+                    const uint32_t kb = sStage + sg * P::kStage, vb = kb + KP * P::kTile;
+                    if (g >= ST && !(ok = tc::mbar_wait_or_dead(kempty(sg), (g / ST - 1) & 1, a.wait_ns, dead))) break;
+                    tc::mbar_expect_tx(kfull(sg), P::kTile);
+#pragma unroll
+                    for (int c = 0; c < NPAN; ++c) tc::tma_load_2d(kb + c * P::kPanel, &kmap, c * 64, y + t * NT, kfull(sg));
+                    if (g >= ST) ok = tc::mbar_wait_or_dead(vempty(sg), (g / ST - 1) & 1, a.wait_ns, dead);
+                    tc::mbar_expect_tx(vfull(sg), P::kTile);         // also when giving up: the drain waits for both
+#pragma unroll
+                    for (int c = 0; c < NPAN; ++c) tc::tma_load_2d(vb + c * P::kPanel, &vmap, c * 64, y + t * NT, vfull(sg));
+                    if (!ok) {
+                        ++g;
+                        break;
+                    }
+                }
+            }
+            *reinterpret_cast<volatile int *>(smem + P::offTmem + 8) = g;          // tiles copied, for the drain
+        }
+    } else {
+        // ---- rebuilding
+        RebuildArgs b;
+        b.idx = a.idx + (size_t)item0.h * a.idx_head;
+        b.slk = a.slk + (size_t)item0.h * a.K * (PG ? D : C);
+        b.slv = a.slv + (size_t)item0.h * a.K * (PG ? D : C);
+        b.rope = a.rope;
+        b.table = smem + P::offTable;
+        b.turn = smem + P::offTurn;
+        b.stages = sStage;
+        b.kfull = kfull(0);
+        b.vfull = vfull(0);
+        b.kempty = kempty(0);
+        b.vempty = vempty(0);
+        b.K = a.K;
+        b.wait_ns = a.wait_ns;
+        b.dead = dead;
+        if (warp < P::kRebuild + 8) {
+            asm volatile("setmaxnreg.inc.sync.aligned.u32 112;");
+            rebuild_keys<D, C, PG, ST>(b, warp - P::kRebuild, item0.tok_first, item0.ntiles, item0.st, item0.len);
+        } else {
+            rebuild_values<D, C, PG, ST>(b, warp - P::kValues, item0.tok_first, item0.ntiles, item0.st, item0.len);
+        }
+    }
+
+    // ---- all done (or given up): free the tensor memory
+    __syncthreads();
+    if (*dead) {
+        if (tid == 0) atomicOr(a.fault, kFaultAttnWait);
+        if (!coded && warp == P::kCopy && lane == 0) {               // copies still in flight
+            const int n = *reinterpret_cast<volatile int *>(smem + P::offTmem + 8);
+            for (int t = n > ST ? n - ST : 0; t < n; ++t) {
+                tc::mbar_wait_bounded(kfull(t % ST), (t / ST) & 1, tc::kDrainNs);
+                tc::mbar_wait_bounded(vfull(t % ST), (t / ST) & 1, tc::kDrainNs);
+            }
+        }
+        if (warp == P::kMma && lane == 0) {                          // products still in flight
+            tc::mma_commit(drain);
+            tc::mbar_wait_bounded(drain, 0, tc::kDrainNs);
+        }
+        __syncthreads();
+    }
+    tc::tc_fence_after();
+    if (warp == P::kMma)
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(P::kCols));
+}
+
+}  // namespace loopvq
