@@ -427,11 +427,12 @@ __global__ void __launch_bounds__(Plan<D, MB, C, PG>::kThreads, 1)
             const int t = MB == 2 ? i >> 1 : i, s = t % ST;
             if (!wait(kfull(s), (t / ST) & 1)) return;
             tc::tc_fence_after();
+            constexpr uint32_t hi = tc::desc_hi(1024, 2);
+            const uint32_t sd = tc::uniform(tmem + (i & 1) * P::colS);
+            const uint32_t k_lo = tc::uniform(tc::desc_lo(sStage + s * P::kStage, 16));
+            const uint32_t q_lo = tc::uniform(tc::desc_lo(sQ + (MB == 2 ? (i & 1) * P::kQ : 0), 16));
+            const uint32_t q_tm = tc::uniform(tmem + P::colQ + (MB == 2 ? (i & 1) * 64 : 0));
             if (tc::elect_one()) {
-                constexpr uint32_t hi = tc::desc_hi(1024, 2);
-                const uint32_t sd = tmem + (i & 1) * P::colS, k_lo = tc::desc_lo(sStage + s * P::kStage, 16);
-                const uint32_t q_lo = tc::desc_lo(sQ + (MB == 2 ? (i & 1) * P::kQ : 0), 16);
-                const uint32_t q_tm = tmem + P::colQ + (MB == 2 ? (i & 1) * 64 : 0);
 #pragma unroll
                 for (int part = 0; part < KP; ++part)
 #pragma unroll
@@ -467,14 +468,15 @@ __global__ void __launch_bounds__(Plan<D, MB, C, PG>::kThreads, 1)
             }
             if (!wait(pfull(w), (i >> 1) & 1)) break;
             tc::tc_fence_after();
+            const uint32_t od = tc::uniform(tmem + 256 + w * 128), pa = tc::uniform(tmem + w * P::colS);
+            const uint32_t v_lo = tc::uniform(tc::desc_lo(vb, P::kPanel)), more = tc::uniform(i > 1);
             if (tc::elect_one()) {
-                const uint32_t od = tmem + 256 + w * 128, pa = tmem + w * P::colS, v_lo = tc::desc_lo(vb, P::kPanel);
 #pragma unroll
                 for (int part = 0; part < 2; ++part)
 #pragma unroll
                     for (int k = 0; k < NT / 16; ++k)                // 16 tokens per product: 8 packed columns
                         tc::mma_ts(od, pa + k * 16 + part * 8, v_lo + k * 128, tc::desc_hi(1024, 2), id_pv,
-                                   i > 1 || part + k > 0);
+                                   part + k > 0 ? 1u : more);
                 if ((MB == 1 || w == 1) && t + ST < ntiles) tc::mma_commit(vempty(s));
                 tc::mma_commit(odone(w));
             }

@@ -254,20 +254,26 @@ __device__ __forceinline__ bool rebuild_values(const RebuildArgs &b, int vw, int
         if (!__all_sync(0xffffffffu, tc::mbar_wait_or_dead(b.vempty + 8u * s, par, b.wait_ns, b.dead))) return false;
         const uint32_t vb = b.stages + (uint32_t)s * (3 * kTile) + 2 * kTile;
 #pragma unroll
-        for (int g = 0; g < 4; ++g) {
-            const bool in = n + g * 8 >= st && n + g * 8 < len;
-            const int nl = n0 + g * 8;
+        for (int g0 = 0; g0 < 4; g0 += 2) {                          // loads of two groups before their stores
+            uint4 v[2][IT][2];
 #pragma unroll
-            for (int it = 0; it < IT; ++it) {
-                const int piece = it * 4 + pl;
-                uint4 v0 = make_uint4(0, 0, 0, 0), v1 = v0;
-                if (in) {
-                    v0 = gather_piece<D, C, PG>(b, tab, b.slv, 16, 0, piece, wd[g][it][0], wd[g][it][NW - 1]);
-                    v1 = gather_piece<D, C, PG>(b, tab, b.slv, 24, 1, piece, wd[g][it][0], wd[g][it][NW - 1]);
+            for (int g = 0; g < 2; ++g)
+#pragma unroll
+                for (int it = 0; it < IT; ++it) {
+                    const int m = n + (g0 + g) * 8, piece = it * 4 + pl;
+                    const uint32_t w0 = wd[g0 + g][it][0], w1 = wd[g0 + g][it][NW - 1];
+                    v[g][it][0] = gather_piece<D, C, PG>(b, tab, b.slv, 16, 0, piece, w0, w1);
+                    v[g][it][1] = gather_piece<D, C, PG>(b, tab, b.slv, 24, 1, piece, w0, w1);
+                    if (m < st || m >= len) v[g][it][0] = v[g][it][1] = make_uint4(0, 0, 0, 0);
                 }
-                sts128(vb + sw128(nl, piece), v0);
-                sts128(vb + (D == 128 ? (64 * 128) + sw128(nl, piece) : sw128(nl, piece + 4)), v1);
-            }
+#pragma unroll
+            for (int g = 0; g < 2; ++g)
+#pragma unroll
+                for (int it = 0; it < IT; ++it) {
+                    const int nl = n0 + (g0 + g) * 8, piece = it * 4 + pl;
+                    sts128(vb + sw128(nl, piece), v[g][it][0]);
+                    sts128(vb + (D == 128 ? (64 * 128) + sw128(nl, piece) : sw128(nl, piece + 4)), v[g][it][1]);
+                }
         }
         n += 64;
         wp += 64 * NP;

@@ -484,15 +484,16 @@ __global__ void __launch_bounds__(RowsPlan<D, NR, C, PG>::kThreads, 1)
             if (!ready(kfull(sg), (g / ST) & 1)) return false;
             tc::tc_fence_after();
             const bool last = s.t + 1 == s.ntiles;
+            constexpr uint32_t hi = tc::desc_hi(1024, 2);
+            const uint32_t k_lo = tc::uniform(tc::desc_lo(sStage + sg * P::kStage, 16));
+            const uint32_t q_lo = tc::uniform(tc::desc_lo(base + P::offQ + (s.it % NQ) * P::kQ, 16));
+            const uint32_t sd = tc::uniform(tmem + (g & 1) * 32);
             if (tc::elect_one()) {
-                constexpr uint32_t hi = tc::desc_hi(1024, 2);
-                const uint32_t k_lo = tc::desc_lo(sStage + sg * P::kStage, 16);
-                const uint32_t q_lo = tc::desc_lo(base + P::offQ + (s.it % NQ) * P::kQ, 16);
 #pragma unroll
                 for (int part = 0; part < KP; ++part)
 #pragma unroll
                     for (int k = 0; k < D / 16; ++k)                 // 16 channels per product: 32 bytes of a row
-                        tc::mma_ss(tmem + (g & 1) * 32,
+                        tc::mma_ss(sd,
                                    k_lo + (part * P::kTile + (k / 4) * P::kPanel + (k % 4) * 32) / 16, hi,
                                    q_lo + ((k / 4) * (NR * 128) + (k % 4) * 32) / 16, hi, id_qk, part + k > 0);
                 if (g + ST < total) tc::mma_commit(kempty(sg));
@@ -521,13 +522,14 @@ __global__ void __launch_bounds__(RowsPlan<D, NR, C, PG>::kThreads, 1)
                 }
             }
             tc::tc_fence_after();
+            const uint32_t p_lo = tc::uniform(tc::desc_lo(base + P::offP + w * P::kP, P::kPart));
+            const uint32_t v_lo = tc::uniform(tc::desc_lo(vb, P::kPanel)), od = tc::uniform(tmem + 64 + w * 96);
+            const uint32_t more = tc::uniform(p.t >= 2);             // else O of this stream holds nothing of the item yet
             if (tc::elect_one()) {
-                const uint32_t p_lo = tc::desc_lo(base + P::offP + w * P::kP, P::kPart), v_lo = tc::desc_lo(vb, P::kPanel);
-                const bool first = p.t < 2;                          // of this stream in the item: O holds nothing yet
 #pragma unroll
                 for (int k = 0; k < NT / 16; ++k)                    // 16 tokens per product
-                    tc::mma_ss(tmem + 64 + w * 96, v_lo + k * 128, tc::desc_hi(1024, 2), p_lo + k * (2 * NR),
-                               tc::desc_hi(8 * NR * 2, NR == 16 ? 6 : 4), id_pv, !first || k > 0);
+                    tc::mma_ss(od, v_lo + k * 128, tc::desc_hi(1024, 2), p_lo + k * (2 * NR),
+                               tc::desc_hi(8 * NR * 2, NR == 16 ? 6 : 4), id_pv, k > 0 ? 1u : more);
                 if (g + ST < total) tc::mma_commit(vempty(sg));
                 tc::mma_commit(odone(w));
             }

@@ -122,6 +122,7 @@ __device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.a
 // product needs in uniform registers is then computed there (moved over from a lane's registers, every product took 130
 // clocks and more to issue).
 __device__ __forceinline__ int uniform_warp() { return __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0); }
+__device__ __forceinline__ uint32_t uniform(uint32_t x) { return __shfl_sync(0xffffffffu, x, 0); }
 __device__ __forceinline__ bool elect_one() {
     uint32_t p;
     asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
