@@ -362,7 +362,7 @@ loopvq_status loopvq_shared_attn(const loopvq_cache *cc, int layer, int t, int s
 
 size_t loopvq_bf16_scored_workspace_bytes(const loopvq_bf16_cache *c, int max_len) {
     if (check_bf16(c) != LOOPVQ_OK || max_len < 0 || max_len > c->Nmax) return 0;
-    return loopvq::bf16_scored_ws_bytes(*c, max_len);
+    return loopvq::plan_scored(*c, max_len).ws_bytes;
 }
 
 loopvq_status loopvq_bf16_decode_attn_scored(const loopvq_bf16_cache *c, const uint16_t *q, const int32_t *starts,
@@ -393,7 +393,7 @@ loopvq_status loopvq_bf16_decode_attn_scored(const loopvq_bf16_cache *c, const u
         LQ_TRY(check_same_or_apart(score_in, score_out, (size_t)c->B * c->Hkv * c->Nmax * sizeof(float), "score_out"));
     const loopvq::DecodePlan plan = loopvq::plan_bf16(*c, max_len);
     if (plan.nsplit > 65535) return fail(LOOPVQ_ERR_UNSUPPORTED, "too many splits");
-    const size_t need = loopvq::bf16_scored_ws_bytes(*c, max_len);
+    const size_t need = loopvq::plan_scored(*c, max_len).ws_bytes;
     if (!workspace || ws_bytes < need)
         return fail(LOOPVQ_ERR_WORKSPACE, "workspace of %zu bytes needed, %zu given", need,
                     workspace ? ws_bytes : (size_t)0);

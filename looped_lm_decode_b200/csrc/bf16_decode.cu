@@ -17,7 +17,7 @@
 // slots of a CTA are combined in shared memory as in the coded kernel.
 // Keys in the cache are already rotated (RoPE at write time), so no rotation
 // happens here.
-#include "decode_kernel.cuh"
+#include "shared_rows.cuh"
 
 namespace loopvq {
 
@@ -37,6 +37,7 @@ struct Bf16Args {
     const float *other_lse;  // [B][Hq]
     const float *score_in;   // [B][Hkv][Nmax], or null for zeros
     float *score_out;        // [B][Hkv][Nmax]
+    int row_ctas;            // CTAs of the tensor-core kernel whose pieces are merged; 0: the split kernel's splits
 };
 
 // 16-byte copy that reads src_bytes (16 or 0) and zero-fills the rest
@@ -67,6 +68,7 @@ __global__ void __launch_bounds__(WARPS * 32, MINB) bf16_split_kernel(const Bf16
     static_assert(NL >= 8 && NL <= 16, "slot width");
 
     extern __shared__ __align__(128) unsigned char smem[];
+    if constexpr (SCORED) grid_trigger();                  // the merge is launched behind it
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int split = blockIdx.x, h = blockIdx.y, b = blockIdx.z;
     const int len = min(max(__ldg(a.lens + b), 0), a.max_len);
@@ -303,25 +305,53 @@ constexpr int kScoreChunk = 2048;                          // tokens per CTA
 template <int D, int QPK>
 __global__ void __launch_bounds__(kScoreThreads) bf16_scored_merge_kernel(const Bf16Args a, float *out, float *lse) {
     const int h = blockIdx.y, b = blockIdx.z, tid = threadIdx.x;
+    grid_wait();
     const int len = min(max(__ldg(a.lens + b), 0), a.max_len);
     const int st = a.starts ? min(max(__ldg(a.starts + b), 0), len) : 0;
     const bool last = blockIdx.x == gridDim.x - 1;         // writes out and lse
     const int n0 = (int)blockIdx.x * kScoreChunk;
     if (!last && (n0 >= len || n0 + kScoreChunk <= st)) return;
-    const int ns = len > st ? (len - (st & ~3) + a.split_len - 1) / a.split_len : 0;
+    // this (sequence, KV head)'s records: row g of record i is at rec0 + g * rec_g + i * rec_i
+    __shared__ long long s_rec[2];
+    size_t rec0, rec_g, rec_i;
+    int ns;
+    if (a.row_ctas > 0) {
+        if (tid < 32) {
+            const RowTiles sp = row_space(a.starts, a.lens, a.max_len, a.B, tid, b);
+            const long long T = sp.per_head * a.Hkv, first = h * sp.per_head + sp.before;
+            const int tiles = row_tiles(a.starts, a.lens, a.max_len, b);
+            if (tid == 0) {
+                const long long G = min((long long)a.row_ctas, T);
+                const long long c0 = tiles ? cta_of_tile(first, T, G) : 0;
+                const long long c1 = tiles ? cta_of_tile(first + tiles - 1, T, G) : -1;
+                s_rec[0] = ((long long)h * a.B + b + c0) * 2 * QPK;
+                s_rec[1] = 2 * (c1 - c0 + 1);
+            }
+        }
+        __syncthreads();
+        rec0 = (size_t)s_rec[0];
+        ns = (int)s_rec[1];
+        rec_g = 1;
+        rec_i = QPK;
+    } else {
+        rec0 = ((size_t)b * a.Hq + h * QPK) * a.nsplit;
+        ns = len > st ? (len - (st & ~3) + a.split_len - 1) / a.split_len : 0;
+        rec_g = a.nsplit;
+        rec_i = 1;
+    }
 
     // log-sum-exps of the query heads: one warp per head, in log2 units
     __shared__ float s_mx[QPK], s_l2[QPK];                 // own maximum; joint log2-sum-exp2
     __shared__ float s_scale[QPK], s_other[QPK];           // factors of the own sum and of the other part
     for (int g = tid >> 5; g < QPK; g += kScoreThreads / 32) {
         const size_t bh = (size_t)b * a.Hq + h * QPK + g;
-        const float2 *ml = a.ws_ml + bh * a.nsplit;
+        const float2 *ml = a.ws_ml + rec0 + g * rec_g;
         float mx = -CUDART_INF_F, sum = 0.f;
-        for (int sp = tid & 31; sp < ns; sp += 32) mx = fmaxf(mx, ml[sp].x);
+        for (int sp = tid & 31; sp < ns; sp += 32) mx = fmaxf(mx, ml[sp * rec_i].x);
 #pragma unroll
         for (int o = 16; o >= 1; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
         if (mx != -CUDART_INF_F)
-            for (int sp = tid & 31; sp < ns; sp += 32) sum += ml[sp].y * ex2(ml[sp].x - mx);
+            for (int sp = tid & 31; sp < ns; sp += 32) sum += ml[sp * rec_i].y * ex2(ml[sp * rec_i].x - mx);
 #pragma unroll
         for (int o = 16; o >= 1; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
         if ((tid & 31) == 0) {
@@ -347,11 +377,14 @@ __global__ void __launch_bounds__(kScoreThreads) bf16_scored_merge_kernel(const 
         for (int it = tid; it < QPK * D; it += kScoreThreads) {
             const int g = it / D, d = it % D;
             const size_t bh = (size_t)b * a.Hq + h * QPK + g;
-            const float2 *ml = a.ws_ml + bh * a.nsplit;
-            const float *o = a.ws_o + bh * a.nsplit * D + d;
+            const float2 *ml = a.ws_ml + rec0 + g * rec_g;
+            const float *o = a.ws_o + (rec0 + g * rec_g) * D + d;
             float acc = 0.f;
-            for (int sp = 0; sp < ns; ++sp)
-                if (s_mx[g] != -CUDART_INF_F) acc += o[(size_t)sp * D] * ex2(ml[sp].x - s_mx[g]);
+#pragma unroll 4
+            for (int sp = 0; sp < ns; ++sp) {
+                const float x = ml[sp * rec_i].x, y = o[sp * rec_i * D];
+                acc += x != -CUDART_INF_F ? y * ex2(x - s_mx[g]) : 0.f;   // a record without tokens has no output
+            }
             float r = acc * s_scale[g];
             if (s_other[g] > 0.f) r += s_other[g] * a.other_out[bh * D + d];
             out[bh * D + d] = r;
@@ -427,8 +460,7 @@ static cudaError_t launch_bf16_scored_t(const Bf16Args &a, float *out, float *ls
         if (e != cudaSuccess) return e;
     }
     const unsigned chunks = (unsigned)((a.max_len + kScoreChunk - 1) / kScoreChunk) + 1;
-    bf16_scored_merge_kernel<D, QPK><<<dim3(chunks, a.Hkv, a.B), kScoreThreads, 0, s>>>(a, out, lse);
-    return cudaGetLastError();
+    return launch_pdl(bf16_scored_merge_kernel<D, QPK>, dim3(chunks, a.Hkv, a.B), kScoreThreads, 0, s, a, out, lse);
 }
 
 template <int D>
@@ -443,9 +475,21 @@ static cudaError_t dispatch_bf16(int qpk, const Bf16Args &a, float *out, float *
     }
 }
 
-size_t bf16_scored_ws_bytes(const loopvq_bf16_cache &c, int max_len) {
-    const size_t base = (plan_bf16(c, max_len).ws_bytes + 255) & ~(size_t)255;
-    return base + (size_t)c.B * c.Hq * (((size_t)max_len + 3) & ~(size_t)3) * sizeof(float);
+// Query heads per KV head from which the scored form runs on the tensor cores: the split kernel's fp32 products grow
+// with them (D 128, 16 sequences of up to 16384 tokens, 4 KV heads, us: 1 head  ; 2 heads  ; 4 heads  ; 8 heads  ).
+constexpr int kScoredRows = 2;
+
+ScoredPlan plan_scored(const loopvq_bf16_cache &c, int max_len) {
+    ScoredPlan p{};
+    const size_t heads = (size_t)c.B * c.Hq;
+    p.rows = c.Hq / c.Hkv >= kScoredRows && (int64_t)c.B * c.Hkv * c.Nmax + 128 <= INT32_MAX;
+    // records of D values: every segment has at most a piece more than the CTAs that it spans
+    const size_t records = p.rows ? ((size_t)c.B * c.Hkv + kRowCtas) * 2 * (c.Hq / c.Hkv)
+                                  : heads * plan_bf16(c, max_len).nsplit;
+    p.off_ml = (records * c.D * sizeof(float) + 255) & ~(size_t)255;
+    p.off_s = (p.off_ml + records * sizeof(float2) + 255) & ~(size_t)255;
+    p.ws_bytes = p.off_s + heads * (((size_t)max_len + 3) & ~(size_t)3) * sizeof(float);
+    return p;
 }
 
 cudaError_t launch_bf16_decode(const loopvq_bf16_cache &c, const DecodePlan &plan, const uint16_t *q,
@@ -469,13 +513,23 @@ cudaError_t launch_bf16_decode(const loopvq_bf16_cache &c, const DecodePlan &pla
     a.nsplit = plan.nsplit;
     a.qscale = scale * 1.44269504088896340736f;
     if (sc != nullptr) {
-        a.ws_s = reinterpret_cast<float *>(reinterpret_cast<char *>(workspace) +
-                                           ((plan.ws_bytes + 255) & ~(size_t)255));
+        const ScoredPlan sp = plan_scored(c, max_len);
+        a.ws_ml = reinterpret_cast<float2 *>(reinterpret_cast<char *>(workspace) + sp.off_ml);
+        a.ws_s = reinterpret_cast<float *>(reinterpret_cast<char *>(workspace) + sp.off_s);
         a.sstride = (max_len + 3) & ~3;
         a.other_out = sc->other_out;
         a.other_lse = sc->other_lse;
         a.score_in = sc->score_in;
         a.score_out = sc->score_out;
+        if (sp.rows) {
+            a.row_ctas = kRowCtas;
+            a.nsplit = 0;                                  // no split kernel
+            if (max_len > 0) {
+                const cudaError_t e = launch_rows_scored(c, q, starts, lens, max_len, a.qscale, a.ws_o, a.ws_ml, a.ws_s,
+                                                         a.sstride, s);
+                if (e != cudaSuccess) return e;
+            }
+        }
     }
     const int qpk = c.Hq / c.Hkv;
     if (c.D == 128) return dispatch_bf16<128>(qpk, a, out, lse, s);

@@ -123,10 +123,15 @@ struct Bf16Scored {
     const float *score_in;   // null: zeros
     float *score_out;
 };
+// The scored form's workspace: records of the tensor-core kernel's pieces (rows) or of the split kernel's splits.
+struct ScoredPlan {
+    bool rows;
+    size_t off_ml, off_s, ws_bytes;
+};
+ScoredPlan plan_scored(const loopvq_bf16_cache &c, int max_len);
 cudaError_t launch_bf16_decode(const loopvq_bf16_cache &c, const DecodePlan &plan, const uint16_t *q,
                                const int32_t *starts, const int32_t *lens, int max_len, float scale, float *out,
                                float *lse, void *workspace, cudaStream_t s, const Bf16Scored *sc = nullptr);
-size_t bf16_scored_ws_bytes(const loopvq_bf16_cache &c, int max_len);
 // Attention of many query tokens over one sequence (shared_attn.cu), with another part to merge in (or nulls).
 struct SharedOther {
     const float *out, *lse;
@@ -138,6 +143,10 @@ cudaError_t launch_bf16_shared(const loopvq_bf16_cache &c, int seq, const uint16
 cudaError_t launch_shared(const loopvq_cache &cc, int layer, int t, int seq, const uint16_t *q, int rows,
                           const int32_t *starts, const int32_t *lens, int max_len, float scale,
                           const SharedOther &other, float *out, float *lse, void *workspace, cudaStream_t s);
+constexpr int kRowCtas = 148;
+cudaError_t launch_rows_scored(const loopvq_bf16_cache &c, const uint16_t *q, const int32_t *starts, const int32_t *lens,
+                               int max_len, float qscale, float *ws_o, float2 *ws_ml, float *ws_s, int sstride,
+                               cudaStream_t s);
 // Eviction (evict.cu).  Workspace: per (sequence, KV head) a count, the emptied slots and the moved tokens' slots.
 struct EvictArgs {
     uint16_t *k, *v;         // [B][Hkv][Nmax][D]

@@ -735,8 +735,7 @@ cudaError_t launch_rows_t(const RowsArgs &a, const CUtensorMap &km, const CUtens
     auto kern = shared_rows_kernel<D, NR, C, PG, SCORES>;
     cudaError_t e = ensure_dynamic_smem((const void *)kern, PL::kAlloc);
     if (e != cudaSuccess) return e;
-    const long items = (long)a.seqs * a.Hkv * a.nsplit;              // a coded cache: one KV head's slices per CTA
-    const unsigned grid = (unsigned)(C != 0 || items < 148 ? items : 148);
+    const unsigned grid = a.nsplit > 0 ? (unsigned)(a.Hkv * a.nsplit) : kRowCtas;
     return launch_pdl(kern, dim3(grid), PL::kThreads, PL::kAlloc, s, a, km, vm);
 }
 
@@ -755,7 +754,6 @@ RowsArgs rows_args(const SharedArgs &a) {
     r.max_len = a.max_len;
     r.nsplit = a.nsplit;
     r.sh = (size_t)a.R;
-    r.sr = 1;
     r.ss = (size_t)a.Hkv * a.R;
     r.qscale = a.qscale;
     r.fault = a.fault;
@@ -819,6 +817,41 @@ SharedArgs common_args(int rows, int Hkv, int Hq, int D, const SharedPlan &p, co
 }
 
 }  // namespace
+
+// Decode attention of every sequence's one query token on the rows kernel, scores kept (the scored decode with grouped
+// heads): records of pieces (two streams of Hq / Hkv rows each) and scores for the caller's merge.
+cudaError_t launch_rows_scored(const loopvq_bf16_cache &c, const uint16_t *q, const int32_t *starts, const int32_t *lens,
+                               int max_len, float qscale, float *ws_o, float2 *ws_ml, float *ws_s, int sstride,
+                               cudaStream_t s) {
+    RowsArgs a{};
+    a.q = q;
+    a.starts = starts;
+    a.lens = lens;
+    a.ws_o = ws_o;
+    a.ws_ml = ws_ml;
+    a.ws_s = ws_s;
+    a.sstride = sstride;
+    a.seqs = c.B;
+    a.Hkv = c.Hkv;
+    a.Hq = c.Hq;
+    a.R = c.Hq / c.Hkv;
+    while ((1 << a.qshift) < a.R) ++a.qshift;
+    a.max_len = max_len;
+    a.ss = (size_t)a.R;
+    a.qscale = qscale;
+    a.wait_ns = wait_limit_ns();
+    a.head_rows = c.Nmax;
+    a.seq_rows = c.Hkv * c.Nmax;
+    cudaError_t e = fault_word_for_current_device(&a.fault);
+    if (e != cudaSuccess) return e;
+    CUtensorMap km, vm;
+    const size_t rows = (size_t)c.B * c.Hkv * c.Nmax;
+    e = make_map(&km, c.k, rows, c.D, 128);
+    if (e == cudaSuccess) e = make_map(&vm, c.v, rows, c.D, 128);
+    if (e != cudaSuccess) return e;
+    return c.D == 128 ? launch_rows_t<128, 16, 0, false, true>(a, km, vm, s)
+                      : launch_rows_t<64, 16, 0, false, true>(a, km, vm, s);
+}
 
 size_t shared_ws_bytes(int Hkv, int Hq, int D, int rows, int max_len, bool coded) {
     return ws_bytes(plan_shared(Hkv, rows * (Hq / Hkv), max_len, coded), (size_t)rows * Hq, D);

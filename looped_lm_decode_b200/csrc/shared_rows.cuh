@@ -37,10 +37,11 @@ struct RowsArgs {
     float *ws_s;                     // scores in log2 units [sequence][Hq][sstride], or null
     int sstride;
     int seqs, Hkv, Hq, R, qshift;    // R = query rows per (sequence, KV head)
-    int max_len, nsplit;
-    int split_tiles;                 // tiles per split, or 0: a sequence's tiles in nsplit equal shares
-    // record of stream w of (sequence, KV head, split), row r: seq * sb + h * sh + r * sr + (2 * split + w) * ss
-    size_t sb, sh, sr, ss;
+    int max_len;
+    int nsplit;                      // one sequence: its tiles in nsplit equal shares per KV head.  0: the tiles of all
+                                     // (KV head, sequence) segments end to end, in equal shares per CTA (RowTiles)
+    // record of stream w of split x (or, with nsplit = 0, of piece x), row r: (2 * x + w) * ss + h * sh + r (sh = 0 then)
+    size_t sh, ss;
     float qscale;                    // scale * log2(e)
     unsigned int *fault;
     unsigned long long wait_ns;
@@ -51,6 +52,31 @@ struct RowsArgs {
     const float *rope;
     int K;
 };
+
+// The tile space of a batch of ragged sequences: segment s = h * B + b holds the 128-token tiles of sequence b from its
+// start; all segments lie end to end and CTA c of G = min(CTAs, T) takes tiles [c T / G, (c + 1) T / G), so that every
+// CTA has the same work whatever the lengths, and the others none.  The part of segment s in CTA c is piece s + c (both only rise along the space, so no two
+// pieces share a number), and the pieces of a segment are consecutive.
+struct RowTiles {
+    long long per_head, before;      // tiles of a KV head; those of the sequences before b
+};
+__device__ __forceinline__ int row_tiles(const int32_t *starts, const int32_t *lens, int max_len, int b) {
+    const int len = min(max(__ldg(lens + b), 0), max_len);
+    const int st = starts ? min(max(__ldg(starts + b), 0), len) : 0;
+    return (len - st + 127) >> 7;
+}
+__device__ __forceinline__ RowTiles row_space(const int32_t *starts, const int32_t *lens, int max_len, int seqs, int lane,
+                                              int b) {               // one warp
+    RowTiles r{0, 0};
+    for (int i = lane; i < seqs; i += 32) {
+        const int t = row_tiles(starts, lens, max_len, i);
+        r.per_head += t;
+        r.before += i < b ? t : 0;
+    }
+    r.per_head = warp_sum64(r.per_head);
+    r.before = warp_sum64(r.before);
+    return r;
+}
 
 // NT tokens per tile; KP bf16 parts per key; NR columns; three parts of P.
 template <int D, int NR, int C, bool PG>
@@ -75,7 +101,8 @@ struct RowsPlan {
     static constexpr int offTurn = offTable + 2 * kTable;
     static constexpr int offRef = offTurn + (coded ? D * 4 : 0);     // per stream: references, their moves, maxima
     static constexpr int kRef = 6 * NR * 4 + 16;
-    static constexpr int offBar = offRef + 2 * kRef;
+    static constexpr int offInfo = offRef + 2 * kRef;                // this CTA's first piece
+    static constexpr int offBar = offInfo + 32;
     static constexpr int kBars = 4 * ST + 2 * NQ + 7;
     static constexpr int offTmem = offBar + kBars * 8;
     static constexpr int kUsed = offTmem + 16;
@@ -177,44 +204,98 @@ __global__ void __launch_bounds__(RowsPlan<D, NR, C, PG>::kThreads, 1)
     grid_wait();
     if constexpr (coded) {                                           // an item's KV head is this CTA's: one item per CTA
         if constexpr (!PG) {
-            const int h = (int)(blockIdx.x / a.nsplit) % a.Hkv;
+            const int h = blockIdx.x / a.nsplit;
             fill_tables<C>(smem + P::offTable, a.slk + (size_t)h * a.K * C, a.slv + (size_t)h * a.K * C, a.K, P::kThreads);
         }
         for (int i = tid; i < D; i += P::kThreads)                   // row 64 is there when a second tile is
             reinterpret_cast<float *>(smem + P::offTurn)[i] = a.max_len > 64 ? a.rope[(size_t)64 * D + i] : 0.f;
     }
-    // ---- items of this CTA, the same walk in every role
+    // ---- items of this CTA, the same walk in every role: one split, or the pieces of its share of the tile space
     struct Item {
-        int b, h, split, st, len, tok_first, ntiles;
+        int b, h, st, len, tok_first, ntiles;
+        size_t rec;                                                  // of stream 0, row 0
+        long long left;                                              // tiles of the CTA from this item on
     };
-    const int nitems = coded ? (int)blockIdx.x + 1 : a.seqs * a.Hkv * a.nsplit;   // coded: one item per CTA
-    auto item_at = [&](int i) {
+    auto item_of = [&](int b, int h, long long skip, long long most) {
         Item x;
-        x.split = i % a.nsplit;
-        x.h = i / a.nsplit % a.Hkv;
-        x.b = i / a.nsplit / a.Hkv;
-        x.len = min(max(__ldg(a.lens + x.b), 0), a.max_len);
-        x.st = a.starts ? min(max(__ldg(a.starts + x.b), 0), x.len) : 0;
+        x.b = b;
+        x.h = h;
+        x.len = min(max(__ldg(a.lens + b), 0), a.max_len);
+        x.st = a.starts ? min(max(__ldg(a.starts + b), 0), x.len) : 0;
         const int tok0 = coded ? (x.st & ~3) : x.st;                 // index words come in tiles of 4 tokens
         const int tiles = x.len > x.st ? (x.len - tok0 + NT - 1) / NT : 0;
-        int t0, t1;
-        if (a.split_tiles > 0) {
-            t0 = min(x.split * a.split_tiles, tiles);
-            t1 = min(t0 + a.split_tiles, tiles);
-        } else {
-            t0 = (int)((long long)x.split * tiles / a.nsplit);
-            t1 = (int)((long long)(x.split + 1) * tiles / a.nsplit);
-        }
-        x.ntiles = t1 - t0;
-        x.tok_first = tok0 + t0 * NT;
+        x.tok_first = tok0 + (int)skip * NT;
+        x.ntiles = (int)min((long long)tiles - skip, most);
+        x.left = most;
+        x.rec = (size_t)(h * a.seqs + b + (int)blockIdx.x) * 2 * a.ss;
         return x;
     };
-    const Item item0 = item_at(blockIdx.x);                          // its lengths' latency runs under the set-up
+    Item item0;
+    if (a.nsplit > 0) {
+        const int split = blockIdx.x % a.nsplit, h = blockIdx.x / a.nsplit;
+        item0 = item_of(0, h, 0, INT32_MAX);
+        const long long tiles = item0.ntiles;
+        const int t0 = (int)(split * tiles / a.nsplit);
+        item0.ntiles = (int)((split + 1) * tiles / a.nsplit) - t0;
+        item0.left = item0.ntiles;
+        item0.tok_first += t0 * NT;
+        item0.rec = (size_t)(2 * split) * a.ss + h * a.sh;
+    } else if (warp == 0) {
+        const RowTiles sp = row_space(a.starts, a.lens, a.max_len, a.seqs, lane, 0);
+        const long long T = sp.per_head * a.Hkv, G = min((long long)gridDim.x, T);
+        const bool any = blockIdx.x < G;
+        const long long x0 = any ? cta_first_tile(blockIdx.x, T, G) : 0, x1 = any ? cta_first_tile(blockIdx.x + 1, T, G) : 0;
+        long long *info = reinterpret_cast<long long *>(smem + P::offInfo);
+        if (lane == 0) info[0] = x1 - x0;
+        if (x0 < x1) {
+            const long long h = x0 / sp.per_head, r = x0 - h * sp.per_head;
+            long long carry = 0;
+            for (int b0 = 0; b0 < a.seqs; b0 += 32) {                // the sequence that holds tile r of the head
+                const long long t = b0 + lane < a.seqs ? row_tiles(a.starts, a.lens, a.max_len, b0 + lane) : 0;
+                long long inc = t;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const long long y = __shfl_up_sync(0xffffffffu, inc, o);
+                    if (lane >= o) inc += y;
+                }
+                inc += carry;
+                const unsigned hit = __ballot_sync(0xffffffffu, inc > r);
+                if (hit) {
+                    if (lane == __ffs(hit) - 1) {
+                        info[1] = (h << 32) | (long long)(b0 + lane);
+                        info[2] = r - (inc - t);
+                    }
+                    break;
+                }
+                carry = __shfl_sync(0xffffffffu, inc, 31);
+            }
+        }
+    }
     tc::fence_async_smem();
     tc::tc_fence_before();
     __syncthreads();
     tc::tc_fence_after();
     const uint32_t tmem = *tmem_slot;
+    if (a.nsplit == 0) {
+        const long long *info = reinterpret_cast<const long long *>(smem + P::offInfo);
+        item0.ntiles = 0;
+        item0.left = info[0];
+        if (info[0] > 0) item0 = item_of((int)(info[1] & 0xffffffff), (int)(info[1] >> 32), info[2], info[0]);
+    }
+    // the next item with tiles; false behind the last
+    auto advance = [&](Item &x) {
+        const long long left = x.left - x.ntiles;
+        if (coded || left <= 0) return false;
+        int b = x.b, h = x.h;
+        do {
+            if (++b == a.seqs) {
+                b = 0;
+                ++h;
+            }
+            x = item_of(b, h, 0, left);
+        } while (x.ntiles == 0);
+        return true;
+    };
 
     if (warp < 8) {
         // ---- softmax of stream w: 128 threads, one token of a tile each
@@ -233,9 +314,9 @@ __global__ void __launch_bounds__(RowsPlan<D, NR, C, PG>::kThreads, 1)
         const int cols = (a.R + 15) & ~15;                           // columns in use (padding rows: zero queries)
         int g = 0;                                                   // tiles of this CTA so far
         bool ok = true;
-        for (int i = blockIdx.x; i < nitems; i += gridDim.x) {
-            const Item x = i == (int)blockIdx.x ? item0 : item_at(i);
-            const size_t rec = x.b * a.sb + x.h * a.sh + (size_t)(2 * x.split + w) * a.ss;
+        Item x = item0;
+        for (bool more = a.nsplit > 0 || x.left > 0; more; more = advance(x)) {
+            const size_t rec = x.rec + w * a.ss;
             float l[NR];
 #pragma unroll
             for (int r = 0; r < NR; ++r) l[r] = 0.f;
@@ -408,7 +489,7 @@ __global__ void __launch_bounds__(RowsPlan<D, NR, C, PG>::kThreads, 1)
                 const int r = tid % 128;
                 const float sum = wmax[r] + wmax[NR + r] + wmax[2 * NR + r] + wmax[3 * NR + r];
                 // (a row whose every score is -inf has no weight)
-                a.ws_ml[rec + r * a.sr] = !all_ok             ? f2(0.f, CUDART_NAN_F)
+                a.ws_ml[rec + r] = !all_ok             ? f2(0.f, CUDART_NAN_F)
                                           : j > 0 && sum != 0.f ? f2(-ref[r], sum)
                                                               : f2(-CUDART_INF_F, 0.f);
             }
@@ -422,24 +503,19 @@ __global__ void __launch_bounds__(RowsPlan<D, NR, C, PG>::kThreads, 1)
                     tc::tmem_wait_ld16(o);
                     tc::tmem_wait_ld16(y);
                     tc::tmem_wait_ld16(z);
-                    float *dst = a.ws_o + (rec + c * a.sr) * D + chan;
-                    const size_t step = a.sr * D;
+                    float *dst = a.ws_o + (rec + c) * D + chan;
 #pragma unroll
                     for (int k = 0; k < 16; ++k)
                         if (chan >= 0 && c + k < a.R)
-                            dst[k * step] = __uint_as_float(o[k]) + (__uint_as_float(y[k]) + __uint_as_float(z[k]));
+                            dst[k * D] = __uint_as_float(o[k]) + (__uint_as_float(y[k]) + __uint_as_float(z[k]));
                 }
             }
             tc::tc_fence_before();
             stream_sync(bar);                                        // the next item writes ref again
             ok = all_ok;
             if (!ok) {                                               // the records of the items left: NaN
-                for (int i2 = i + gridDim.x; i2 < nitems; i2 += gridDim.x) {
-                    const Item z = item_at(i2);
-                    if (tid % 128 < a.R)
-                        a.ws_ml[z.b * a.sb + z.h * a.sh + (tid % 128) * a.sr + (size_t)(2 * z.split + w) * a.ss] =
-                            f2(0.f, CUDART_NAN_F);
-                }
+                while (advance(x))
+                    if (tid % 128 < a.R) a.ws_ml[x.rec + w * a.ss + tid % 128] = f2(0.f, CUDART_NAN_F);
                 break;
             }
         }
@@ -447,43 +523,21 @@ __global__ void __launch_bounds__(RowsPlan<D, NR, C, PG>::kThreads, 1)
         // ---- products.  QK of step g + 2 follows PV of step g: S and P of its stream are free then
         constexpr uint32_t id_qk = tc::idesc_bf16(NT, NR);
         constexpr uint32_t id_pv = tc::idesc_bf16(D, PARTS * NR) | (1u << 15) | (1u << 16);   // both: contraction outside
-        int total = 0, items = 0;                                    // what will not be used again is not freed
-        for (int i = blockIdx.x + lane * gridDim.x; i < nitems; i += 32 * gridDim.x) {
-            const int nt = item_at(i).ntiles;
-            total += nt;
-            items += nt > 0;
-        }
-#pragma unroll
-        for (int o = 16; o >= 1; o >>= 1) {
-            total += __shfl_xor_sync(0xffffffffu, total, o);
-            items += __shfl_xor_sync(0xffffffffu, items, o);
-        }
+        const long long total = item0.left;                          // what will not be used again is not freed
         auto ready = [&](uint32_t b, uint32_t parity) { return __all_sync(0xffffffffu, tc::mbar_test(b, parity)); };
         // two walks over the tiles: S runs up to two steps ahead
         struct Walk {
-            int i, it, t, ntiles, end;                               // item, its number among those with tiles; tile,
-        };                                                           // tiles, tokens from the first to the length
-        auto next_item = [&](Walk &v) {
-            for (v.i += gridDim.x; v.i < nitems; v.i += gridDim.x) {
-                const Item x = v.i == (int)blockIdx.x ? item0 : item_at(v.i);
-                v.ntiles = x.ntiles;
-                v.end = x.len - x.tok_first;
-                if (x.ntiles > 0) break;
-            }
-            v.t = 0;
-            ++v.it;
+            Item x;
+            int it, t;                                               // the item's number, its tile
         };
-        Walk s, p;
-        s.i = (int)blockIdx.x - (int)gridDim.x;
-        s.it = -1;
-        next_item(s);
-        p = s;
-        auto qk = [&](int g) {
+        Walk s{item0, 0, 0}, p{item0, 0, 0};
+        auto qk = [&](long long g64) {
+            const int g = (int)g64;
             const int sg = g % ST;
             if (s.t == 0 && !ready(qfull(s.it % NQ), (s.it / NQ) & 1)) return false;
             if (!ready(kfull(sg), (g / ST) & 1)) return false;
             tc::tc_fence_after();
-            const bool last = s.t + 1 == s.ntiles;
+            const bool last = s.t + 1 == s.x.ntiles;
             constexpr uint32_t hi = tc::desc_hi(1024, 2);
             const uint32_t k_lo = tc::uniform(tc::desc_lo(sStage + sg * P::kStage, 16));
             const uint32_t q_lo = tc::uniform(tc::desc_lo(base + P::offQ + (s.it % NQ) * P::kQ, 16));
@@ -497,21 +551,26 @@ __global__ void __launch_bounds__(RowsPlan<D, NR, C, PG>::kThreads, 1)
                                    k_lo + (part * P::kTile + (k / 4) * P::kPanel + (k % 4) * 32) / 16, hi,
                                    q_lo + ((k / 4) * (NR * 128) + (k % 4) * 32) / 16, hi, id_qk, part + k > 0);
                 if (g + ST < total) tc::mma_commit(kempty(sg));
-                if (last && s.it + NQ < items) tc::mma_commit(qempty(s.it % NQ));
+                if (last && g + 1 < total) tc::mma_commit(qempty(s.it % NQ));
                 tc::mma_commit(sfull(g & 1));
             }
             __syncwarp();
-            if (last) next_item(s);
-            else ++s.t;
+            ++s.t;
+            if (last) {
+                advance(s.x);
+                s.t = 0;
+                ++s.it;
+            }
             return true;
         };
-        auto pv = [&](int g) {
+        auto pv = [&](long long g64) {
+            const int g = (int)g64;
             const int sg = g % ST, w = g & 1;
             const uint32_t vb = sStage + sg * P::kStage + KP * P::kTile;
             if (!ready(pfull(w), (g >> 1) & 1) || !ready(vfull(sg), (g / ST) & 1)) return false;
             if constexpr (!coded) {
                 // rows behind the last token may hold anything: 0 x that has to be 0
-                const int end = p.end - p.t * NT;
+                const int end = p.x.len - (p.x.tok_first + p.t * NT);
                 if (end < NT) {
                     for (int it = lane; it < (NT - end) * (D / 8); it += 32) {
                         const int n = end + it / (D / 8), ch = it % (D / 8);
@@ -534,13 +593,15 @@ __global__ void __launch_bounds__(RowsPlan<D, NR, C, PG>::kThreads, 1)
                 tc::mma_commit(odone(w));
             }
             __syncwarp();
-            if (p.t + 1 == p.ntiles) next_item(p);
-            else ++p.t;
+            if (++p.t == p.x.ntiles) {
+                advance(p.x);
+                p.t = 0;
+            }
             return true;
         };
         // whichever product is ready goes first: one that waits for its copy must not hold up another whose tile,
         // once read, makes room for the next copy
-        int gs = 0, gp = 0;
+        long long gs = 0, gp = 0;
         uint64_t t0 = tc::globaltimer();
         while (gp < total) {
             bool went = gs < total && gs < gp + 2 && qk(gs);
@@ -559,9 +620,8 @@ __global__ void __launch_bounds__(RowsPlan<D, NR, C, PG>::kThreads, 1)
     } else if (warp == P::kQuery) {
         // ---- queries: NR rows (those past R zero), swizzled rows of 64 channels
         int it = 0;
-        for (int i = blockIdx.x; i < nitems; i += gridDim.x) {
-            const Item x = i == (int)blockIdx.x ? item0 : item_at(i);
-            if (x.ntiles == 0) continue;
+        Item x = item0;
+        for (bool more = x.left > 0; more; more = advance(x)) {
             if (it >= NQ &&
                 !__all_sync(0xffffffffu, tc::mbar_wait_or_dead(qempty(it % NQ), (it / NQ - 1) & 1, a.wait_ns, dead)))
                 break;
@@ -586,8 +646,8 @@ __global__ void __launch_bounds__(RowsPlan<D, NR, C, PG>::kThreads, 1)
         if (lane == 0) {
             int g = 0;
             bool ok = true;
-            for (int i = blockIdx.x; ok && i < nitems; i += gridDim.x) {
-                const Item x = i == (int)blockIdx.x ? item0 : item_at(i);
+            Item x = item0;
+            for (bool more = x.left > 0; ok && more; more = advance(x)) {
                 const int y = x.b * a.seq_rows + x.h * a.head_rows + x.tok_first;
                 for (int t = 0; t < x.ntiles; ++t, ++g) {
                     const int sg = g % ST;
