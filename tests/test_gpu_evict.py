@@ -196,10 +196,18 @@ def test_evict_protected_positions(n_sink, n_recent, budget):
     run_evict(2, 3, 128, 200, [200, 150], budget, n_sink, n_recent, False, "ties")
 
 
-@pytest.mark.parametrize("nmax", [4096, 4097, 49152, 49153, 60001])
-def test_evict_long(nmax):
-    """Both sides of the sizes where the selection changes its threads or keeps its keys elsewhere."""
-    run_evict(1, 1, 64, nmax, [nmax], nmax // 3, 8, 64, True, "ties")
+@pytest.mark.parametrize("scores", ["skewed", "ties", "equal"])
+@pytest.mark.parametrize("nmax", [1280, 1281, 2560, 2561, 5120, 5121, 10240, 10241, 20480, 20481, 40960, 40961, 60001])
+def test_evict_long(nmax, scores):
+    """Both sides of the sizes where the selection takes more registers, more CTAs, or its keys from memory again."""
+    run_evict(2, 1, 64, nmax, [nmax, nmax - 7], nmax // 3, 8, 64, True, scores)
+
+
+@pytest.mark.parametrize("hkv,in_place", [(1, True), (8, True), (8, False), (9, True), (16, False)])
+@pytest.mark.parametrize("budget", [1024, 1300, 1700])
+def test_evict_few_and_many_rows(hkv, in_place, budget):
+    """Steps that one launch does, with clusters of a sequence's heads and without, and those that two do."""
+    run_evict(3, hkv, 128, 1800, [1800, budget + 1, budget], budget, 4, 32, in_place, "ties")
 
 
 def test_evict_equal_positions_and_clamped_lengths():
