@@ -355,9 +355,10 @@ def _need(t: torch.Tensor, name: str, shape: tuple, dtypes: tuple, device):
 
 
 def _result(t, name: str, shape: tuple, like: torch.Tensor):
-    """An fp32 output: the caller's, or a new one."""
+    """An fp32 output: the caller's, or a new one (torch.empty_strided takes half the time of torch.empty)."""
     if t is None:
-        return like.new_empty(shape, dtype=torch.float32)
+        strides = (shape[1] * shape[2], shape[2], 1) if len(shape) == 3 else (shape[1], 1)
+        return torch.empty_strided(shape, strides, dtype=torch.float32, device=like.device)
     _need(t, name, shape, _F32, like.device)
     return t
 
@@ -369,10 +370,25 @@ def _on_stream(stream, *tensors):
             t.record_stream(stream)
 
 
+_sizes = {}
+
+
+def _ws_size(fn, ref, *key):
+    """A workspace size, which goes by the shapes alone, from the library the first time (a call of its own costs as much
+    as a kernel launch's host side)."""
+    n = _sizes.get(key)
+    if n is None:
+        if len(_sizes) >= 4096:
+            _sizes.clear()
+        n = _sizes[key] = fn(ref, *key[6:])
+    return n
+
+
 def _workspace(workspace, need: int, like: torch.Tensor):
     if workspace is None:
-        workspace = like.new_empty(max(need, 16), dtype=torch.uint8)
-    elif workspace.device != like.device or not workspace.is_contiguous():
+        need = max(need, 16)
+        return torch.empty_strided((need,), (1,), dtype=torch.uint8, device=like.device), need
+    if workspace.device != like.device or not workspace.is_contiguous():
         raise LoopVQError(LOOPVQ_ERR_INVALID_ARG, f"workspace must be contiguous memory on {like.device}")
     return workspace, workspace.numel() * workspace.element_size()
 
@@ -423,7 +439,8 @@ def bf16_shared_attn(cache: Bf16Cache, seq: int, q: torch.Tensor, lens: torch.Te
     if rows == 0:
         return out, lse
     L, ref = lib(), cache.ref()
-    workspace, n = _workspace(workspace, L.loopvq_bf16_shared_workspace_bytes(ref, rows, max_len), q)
+    workspace, n = _workspace(workspace, _ws_size(L.loopvq_bf16_shared_workspace_bytes, ref, "bf16", cache.B, cache.Hkv, cache.Hq,
+                                             cache.D, cache.Nmax, rows, max_len), q)
     _check(L.loopvq_bf16_shared_attn(ref, seq, q.data_ptr(), rows, _ptr(starts), lens.data_ptr(), max_len, scale,
                                      _ptr(oo), _ptr(ol), out.data_ptr(), lse.data_ptr(), workspace.data_ptr(), n,
                                      _stream(stream)))
@@ -439,7 +456,8 @@ def shared_attn(cache: Cache, layer: int, t: int, seq: int, q: torch.Tensor, len
     if rows == 0:
         return out, lse
     L, ref = lib(), cache.ref()
-    workspace, n = _workspace(workspace, L.loopvq_shared_workspace_bytes(ref, rows, max_len), q)
+    workspace, n = _workspace(workspace, _ws_size(L.loopvq_shared_workspace_bytes, ref, "coded", cache.B, cache.Hkv, cache.Hq,
+                                             cache.D, cache.Nmax, rows, max_len), q)
     _check(L.loopvq_shared_attn(ref, layer, t, seq, q.data_ptr(), rows, _ptr(starts), lens.data_ptr(), max_len, scale,
                                 _ptr(oo), _ptr(ol), out.data_ptr(), lse.data_ptr(), workspace.data_ptr(), n,
                                 _stream(stream)))
@@ -473,7 +491,8 @@ def bf16_decode_attn_scored(cache: Bf16Cache, q: torch.Tensor, lens: torch.Tenso
     oo, ol = _need_other(other, B, Hq, D, dev)
     out, lse = _result(out, "out", (B, Hq, D), q), _result(lse, "lse", (B, Hq), q)
     L, ref = lib(), cache.ref()
-    workspace, n = _workspace(workspace, L.loopvq_bf16_scored_workspace_bytes(ref, max_len), q)
+    workspace, n = _workspace(workspace, _ws_size(L.loopvq_bf16_scored_workspace_bytes, ref, "scored", B, cache.Hkv, Hq, D,
+                                             cache.Nmax, max_len), q)
     _check(L.loopvq_bf16_decode_attn_scored(ref, q.data_ptr(), _ptr(starts), lens.data_ptr(), max_len, scale, _ptr(oo),
                                             _ptr(ol), _ptr(score), score_out.data_ptr(), out.data_ptr(),
                                             lse.data_ptr(), workspace.data_ptr(), n, _stream(stream)))
@@ -503,7 +522,8 @@ def bf16_evict(cache: Bf16Cache, score: torch.Tensor, pos: torch.Tensor, lens: t
     for t, name in ((lens, "lens"), (next_pos, "next_pos"), (lens_out, "lens_out")):
         _need(t, name, (B,), _I32, dev)
     L, ref = lib(), cache.ref()
-    workspace, n = _workspace(workspace, L.loopvq_bf16_evict_workspace_bytes(ref, max_len, budget), lens)
+    workspace, n = _workspace(workspace, _ws_size(L.loopvq_bf16_evict_workspace_bytes, ref, "evict", B, H, cache.Hq, cache.D, N,
+                                             max_len, budget), lens)
     _check(L.loopvq_bf16_evict(ref, score.data_ptr(), pos.data_ptr(), lens.data_ptr(), next_pos.data_ptr(), max_len,
                                budget, n_sink, n_recent, score_out.data_ptr(), pos_out.data_ptr(),
                                lens_out.data_ptr(), workspace.data_ptr(), n, _stream(stream)))
