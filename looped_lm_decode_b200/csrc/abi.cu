@@ -305,6 +305,7 @@ static loopvq_status check_shared(int B, int Hkv, int Hq, int D, int Nmax, int s
 }
 
 static loopvq_status check_ws(const void *workspace, size_t given, size_t need) {
+    if (need == 0) return LOOPVQ_OK;
     if (!workspace || given < need)
         return fail(LOOPVQ_ERR_WORKSPACE, "workspace of %zu bytes needed, %zu given", need, workspace ? given : (size_t)0);
     if (!aligned16(workspace)) return fail(LOOPVQ_ERR_INVALID_ARG, "workspace is not 16-byte aligned");
@@ -393,11 +394,7 @@ loopvq_status loopvq_bf16_decode_attn_scored(const loopvq_bf16_cache *c, const u
         LQ_TRY(check_same_or_apart(score_in, score_out, (size_t)c->B * c->Hkv * c->Nmax * sizeof(float), "score_out"));
     const loopvq::DecodePlan plan = loopvq::plan_bf16(*c, max_len);
     if (plan.nsplit > 65535) return fail(LOOPVQ_ERR_UNSUPPORTED, "too many splits");
-    const size_t need = loopvq::plan_scored(*c, max_len).ws_bytes;
-    if (!workspace || ws_bytes < need)
-        return fail(LOOPVQ_ERR_WORKSPACE, "workspace of %zu bytes needed, %zu given", need,
-                    workspace ? ws_bytes : (size_t)0);
-    if (!aligned16(workspace)) return fail(LOOPVQ_ERR_INVALID_ARG, "workspace is not 16-byte aligned");
+    LQ_TRY(check_ws(workspace, ws_bytes, loopvq::plan_scored(*c, max_len).ws_bytes));
     const loopvq::Bf16Scored sc{other_out, other_lse, score_in, score_out};
     cudaError_t e = loopvq::launch_bf16_decode(*c, plan, q, starts, lens, max_len, scale, out, lse, workspace,
                                                (cudaStream_t)stream, &sc);

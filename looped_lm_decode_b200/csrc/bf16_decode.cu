@@ -482,7 +482,11 @@ constexpr int kScoredRows = 2;
 ScoredPlan plan_scored(const loopvq_bf16_cache &c, int max_len) {
     ScoredPlan p{};
     const size_t heads = (size_t)c.B * c.Hq;
-    p.rows = c.Hq / c.Hkv >= kScoredRows && (int64_t)c.B * c.Hkv * c.Nmax + 128 <= INT32_MAX;
+    const bool fits = (int64_t)c.B * c.Hkv * c.Nmax + 128 <= INT32_MAX;   // rows of the tensor maps
+    // few tokens on no more (sequence, KV head) pairs than SMs: one launch, whatever the heads
+    p.direct = fits && max_len <= kDirectTiles * 128 && c.B * c.Hkv <= kRowCtas;
+    if (p.direct) return p;
+    p.rows = fits && c.Hq / c.Hkv >= kScoredRows;
     // records of D values: every segment has at most a piece more than the CTAs that it spans
     const size_t records = p.rows ? ((size_t)c.B * c.Hkv + kRowCtas) * 2 * (c.Hq / c.Hkv)
                                   : heads * plan_bf16(c, max_len).nsplit;
@@ -514,6 +518,8 @@ cudaError_t launch_bf16_decode(const loopvq_bf16_cache &c, const DecodePlan &pla
     a.qscale = scale * 1.44269504088896340736f;
     if (sc != nullptr) {
         const ScoredPlan sp = plan_scored(c, max_len);
+        if (sp.direct)
+            return launch_rows_scored(c, q, starts, lens, max_len, a.qscale, *sc, out, lse, nullptr, nullptr, nullptr, 0, s);
         a.ws_ml = reinterpret_cast<float2 *>(reinterpret_cast<char *>(workspace) + sp.off_ml);
         a.ws_s = reinterpret_cast<float *>(reinterpret_cast<char *>(workspace) + sp.off_s);
         a.sstride = (max_len + 3) & ~3;
@@ -525,8 +531,8 @@ cudaError_t launch_bf16_decode(const loopvq_bf16_cache &c, const DecodePlan &pla
             a.row_ctas = kRowCtas;
             a.nsplit = 0;                                  // no split kernel
             if (max_len > 0) {
-                const cudaError_t e = launch_rows_scored(c, q, starts, lens, max_len, a.qscale, a.ws_o, a.ws_ml, a.ws_s,
-                                                         a.sstride, s);
+                const cudaError_t e = launch_rows_scored(c, q, starts, lens, max_len, a.qscale, *sc, out, lse,
+                                                         a.ws_o, a.ws_ml, a.ws_s, a.sstride, s);
                 if (e != cudaSuccess) return e;
             }
         }

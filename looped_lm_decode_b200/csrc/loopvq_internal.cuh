@@ -126,6 +126,7 @@ struct Bf16Scored {
 // The scored form's workspace: records of the tensor-core kernel's pieces (rows) or of the split kernel's splits.
 struct ScoredPlan {
     bool rows;
+    bool direct;             // on the tensor cores in one launch, without a workspace
     size_t off_ml, off_s, ws_bytes;
 };
 ScoredPlan plan_scored(const loopvq_bf16_cache &c, int max_len);
@@ -145,8 +146,8 @@ cudaError_t launch_shared(const loopvq_cache &cc, int layer, int t, int seq, con
                           const SharedOther &other, float *out, float *lse, void *workspace, cudaStream_t s);
 constexpr int kRowCtas = 148;
 cudaError_t launch_rows_scored(const loopvq_bf16_cache &c, const uint16_t *q, const int32_t *starts, const int32_t *lens,
-                               int max_len, float qscale, float *ws_o, float2 *ws_ml, float *ws_s, int sstride,
-                               cudaStream_t s);
+                               int max_len, float qscale, const Bf16Scored &sc, float *out, float *lse, float *ws_o,
+                               float2 *ws_ml, float *ws_s, int sstride, cudaStream_t s);
 // Eviction (evict.cu).  Workspace: per (sequence, KV head) a count, the emptied slots and the moved tokens' slots.
 struct EvictArgs {
     uint16_t *k, *v;         // [B][Hkv][Nmax][D]

@@ -652,6 +652,7 @@ constexpr int kFewRows = 32, kFewRowsCoded = 16;
 
 struct SharedPlan {
     bool few;                // shared_rows_kernel; else shared_attn_kernel with mb blocks of 128 rows
+    bool direct;             // one CTA per KV head, which writes the result itself
     int mb, nsplit, nz, nrec;
 };
 
@@ -676,14 +677,17 @@ SharedPlan plan_shared(int Hkv, int R, int max_len, bool coded) {
             p.nsplit = (int)ns;
         }
     }
-    p.nrec = p.few ? 2 * p.nsplit : p.nsplit;                        // its two streams write a record each
+    // few tiles: a head on one CTA takes about as long as its tiles on several and the merge of their records, and has
+    // one launch and no workspace
+    p.direct = p.few && tiles <= kDirectTiles;
+    p.nrec = p.direct ? 0 : p.few ? 2 * p.nsplit : p.nsplit;         // a CTA's two streams write a record each
     return p;
 }
 
 size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 
 size_t ws_bytes(const SharedPlan &p, size_t RT, int D) {
-    return align256(p.nrec * RT * D * sizeof(float)) + p.nrec * RT * sizeof(float2);
+    return p.nrec == 0 ? 0 : align256(p.nrec * RT * D * sizeof(float)) + p.nrec * RT * sizeof(float2);
 }
 
 // cuTensorMapEncodeTiled through the runtime: the library does not link the driver.
@@ -729,18 +733,22 @@ cudaError_t launch_t(const SharedArgs &a, const SharedPlan &p, const CUtensorMap
     return launch_pdl(kern, dim3(p.nsplit, a.Hkv, p.nz), PL::kThreads, PL::kAlloc, s, a, km, vm);
 }
 
-template <int D, int NR, int C, bool PG, bool SCORES = false>
+template <int D, int NR, int C, bool PG, bool SCORES, bool DIRECT>
 cudaError_t launch_rows_t(const RowsArgs &a, const CUtensorMap &km, const CUtensorMap &vm, cudaStream_t s) {
     using PL = RowsPlan<D, NR, C, PG>;
-    auto kern = shared_rows_kernel<D, NR, C, PG, SCORES>;
+    auto kern = shared_rows_kernel<D, NR, C, PG, SCORES, DIRECT>;
     cudaError_t e = ensure_dynamic_smem((const void *)kern, PL::kAlloc);
     if (e != cudaSuccess) return e;
-    const unsigned grid = a.nsplit > 0 ? (unsigned)(a.Hkv * a.nsplit) : kRowCtas;
+    const unsigned grid = DIRECT ? (unsigned)(a.seqs * a.Hkv) : a.nsplit > 0 ? (unsigned)(a.Hkv * a.nsplit) : kRowCtas;
     return launch_pdl(kern, dim3(grid), PL::kThreads, PL::kAlloc, s, a, km, vm);
 }
 
-RowsArgs rows_args(const SharedArgs &a) {
+RowsArgs rows_args(const SharedArgs &a, const SharedOther &o, float *out, float *lse) {
     RowsArgs r{};
+    r.other_out = o.out;
+    r.other_lse = o.lse;
+    r.out = out;
+    r.lse = lse;
     r.q = a.q;
     r.starts = a.start;
     r.lens = a.len;
@@ -770,18 +778,24 @@ RowsArgs rows_args(const SharedArgs &a) {
 
 template <int D, int C, bool PG>
 cudaError_t launch_p(const SharedArgs &a, const SharedPlan &p, const CUtensorMap &km, const CUtensorMap &vm,
-                     cudaStream_t s) {
-    if (p.few)
-        return a.R <= 16 ? launch_rows_t<D, 16, C, PG>(rows_args(a), km, vm, s)
-                         : launch_rows_t<D, 32, C, PG>(rows_args(a), km, vm, s);
+                     const SharedOther &o, float *out, float *lse, cudaStream_t s) {
+    if (p.few) {
+        const RowsArgs r = rows_args(a, o, out, lse);
+        if (a.R <= 16)
+            return p.direct ? launch_rows_t<D, 16, C, PG, false, true>(r, km, vm, s)
+                            : launch_rows_t<D, 16, C, PG, false, false>(r, km, vm, s);
+        if constexpr (C == 0)
+            return p.direct ? launch_rows_t<D, 32, C, PG, false, true>(r, km, vm, s)
+                            : launch_rows_t<D, 32, C, PG, false, false>(r, km, vm, s);
+    }
     return p.mb == 2 ? launch_t<D, 2, C, PG>(a, p, km, vm, s) : launch_t<D, 1, C, PG>(a, p, km, vm, s);
 }
 
 template <int C, bool PG>
 cudaError_t launch_d(int D, const SharedArgs &a, const SharedPlan &p, const CUtensorMap &km, const CUtensorMap &vm,
-                     cudaStream_t s) {
-    if (D == 128) return launch_p<128, C, PG>(a, p, km, vm, s);
-    if (D == 64) return launch_p<64, C, PG>(a, p, km, vm, s);
+                     const SharedOther &o, float *out, float *lse, cudaStream_t s) {
+    if (D == 128) return launch_p<128, C, PG>(a, p, km, vm, o, out, lse, s);
+    if (D == 64) return launch_p<64, C, PG>(a, p, km, vm, o, out, lse, s);
     return cudaErrorInvalidValue;
 }
 
@@ -818,11 +832,12 @@ SharedArgs common_args(int rows, int Hkv, int Hq, int D, const SharedPlan &p, co
 
 }  // namespace
 
-// Decode attention of every sequence's one query token on the rows kernel, scores kept (the scored decode with grouped
-// heads): records of pieces (two streams of Hq / Hkv rows each) and scores for the caller's merge.
+// Decode attention of every sequence's one query token on the rows kernel, scores kept.  ws_o null: DIRECT, which also
+// writes out, lse and the scores; else records of pieces (two streams of Hq / Hkv rows each) and scores in log2 units
+// for the caller's merge.
 cudaError_t launch_rows_scored(const loopvq_bf16_cache &c, const uint16_t *q, const int32_t *starts, const int32_t *lens,
-                               int max_len, float qscale, float *ws_o, float2 *ws_ml, float *ws_s, int sstride,
-                               cudaStream_t s) {
+                               int max_len, float qscale, const Bf16Scored &sc, float *out, float *lse, float *ws_o,
+                               float2 *ws_ml, float *ws_s, int sstride, cudaStream_t s) {
     RowsArgs a{};
     a.q = q;
     a.starts = starts;
@@ -842,6 +857,12 @@ cudaError_t launch_rows_scored(const loopvq_bf16_cache &c, const uint16_t *q, co
     a.wait_ns = wait_limit_ns();
     a.head_rows = c.Nmax;
     a.seq_rows = c.Hkv * c.Nmax;
+    a.other_out = sc.other_out;
+    a.other_lse = sc.other_lse;
+    a.out = out;
+    a.lse = lse;
+    a.score_in = sc.score_in;
+    a.score_out = sc.score_out;
     cudaError_t e = fault_word_for_current_device(&a.fault);
     if (e != cudaSuccess) return e;
     CUtensorMap km, vm;
@@ -849,8 +870,11 @@ cudaError_t launch_rows_scored(const loopvq_bf16_cache &c, const uint16_t *q, co
     e = make_map(&km, c.k, rows, c.D, 128);
     if (e == cudaSuccess) e = make_map(&vm, c.v, rows, c.D, 128);
     if (e != cudaSuccess) return e;
-    return c.D == 128 ? launch_rows_t<128, 16, 0, false, true>(a, km, vm, s)
-                      : launch_rows_t<64, 16, 0, false, true>(a, km, vm, s);
+    if (ws_o == nullptr)
+        return c.D == 128 ? launch_rows_t<128, 16, 0, false, true, true>(a, km, vm, s)
+                          : launch_rows_t<64, 16, 0, false, true, true>(a, km, vm, s);
+    return c.D == 128 ? launch_rows_t<128, 16, 0, false, true, false>(a, km, vm, s)
+                      : launch_rows_t<64, 16, 0, false, true, false>(a, km, vm, s);
 }
 
 size_t shared_ws_bytes(int Hkv, int Hq, int D, int rows, int max_len, bool coded) {
@@ -870,8 +894,8 @@ cudaError_t launch_bf16_shared(const loopvq_bf16_cache &c, int seq, const uint16
     CUtensorMap km, vm;
     e = make_map(&km, c.k + at, map_rows, c.D, 128);
     if (e == cudaSuccess) e = make_map(&vm, c.v + at, map_rows, c.D, 128);
-    if (e == cudaSuccess) e = launch_d<0, false>(c.D, a, p, km, vm, s);
-    if (e != cudaSuccess) return e;
+    if (e == cudaSuccess) e = launch_d<0, false>(c.D, a, p, km, vm, other, out, lse, s);
+    if (e != cudaSuccess || p.direct) return e;
     return finish(a, p, c.D, other, out, lse, s);
 }
 
@@ -892,13 +916,13 @@ cudaError_t launch_shared(const loopvq_cache &cc, int layer, int t, int seq, con
     CUtensorMap none{};
     const bool pg = ncb_of(cc) > 1;
     switch (cc.c) {
-        case 4: e = pg ? launch_d<4, true>(cc.D, a, p, none, none, s) : launch_d<4, false>(cc.D, a, p, none, none, s); break;
-        case 8: e = pg ? launch_d<8, true>(cc.D, a, p, none, none, s) : launch_d<8, false>(cc.D, a, p, none, none, s); break;
-        case 16: e = pg ? launch_d<16, true>(cc.D, a, p, none, none, s) : launch_d<16, false>(cc.D, a, p, none, none, s); break;
-        case 32: e = pg ? launch_d<32, true>(cc.D, a, p, none, none, s) : launch_d<32, false>(cc.D, a, p, none, none, s); break;
+        case 4: e = pg ? launch_d<4, true>(cc.D, a, p, none, none, other, out, lse, s) : launch_d<4, false>(cc.D, a, p, none, none, other, out, lse, s); break;
+        case 8: e = pg ? launch_d<8, true>(cc.D, a, p, none, none, other, out, lse, s) : launch_d<8, false>(cc.D, a, p, none, none, other, out, lse, s); break;
+        case 16: e = pg ? launch_d<16, true>(cc.D, a, p, none, none, other, out, lse, s) : launch_d<16, false>(cc.D, a, p, none, none, other, out, lse, s); break;
+        case 32: e = pg ? launch_d<32, true>(cc.D, a, p, none, none, other, out, lse, s) : launch_d<32, false>(cc.D, a, p, none, none, other, out, lse, s); break;
         default: return cudaErrorInvalidValue;
     }
-    if (e != cudaSuccess) return e;
+    if (e != cudaSuccess || p.direct) return e;
     return finish(a, p, cc.D, other, out, lse, s);
 }
 

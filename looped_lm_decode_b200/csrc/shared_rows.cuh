@@ -46,6 +46,11 @@ struct RowsArgs {
     unsigned int *fault;
     unsigned long long wait_ns;
     int head_rows, seq_rows;         // bf16 cache: rows of the tensor maps per KV head and per sequence
+    // written by the kernel itself where a CTA has all tokens of its rows (DIRECT)
+    const float *other_out, *other_lse;
+    float *out, *lse;                // lse may be null
+    const float *score_in;           // [sequence][Hkv][head_rows], or null for zeros
+    float *score_out;
     const uint32_t *idx;             // coded cache: as in SharedArgs
     size_t idx_head;
     const uint16_t *slk, *slv;
@@ -113,6 +118,7 @@ struct RowsPlan {
     static_assert(kAlloc <= 232448, "shared memory");
     static_assert(offStage % 1024 == 0 && offP % 1024 == 0 && offQ % 1024 == 0 && kP % 512 == 0, "swizzle atoms");
     static_assert(PARTS * NR <= 96, "tensor memory");
+    static_assert(2 * kP >= NR * D * 4, "the streams' merge");
 };
 
 // The row of P^T of token n: 16-byte chunk c of NR columns, swizzled by rows of 32 (NR = 16) or 64 (NR = 32) bytes.
@@ -133,6 +139,7 @@ __device__ __forceinline__ bool stream_any(int id, bool p) {
         : "=r"(r) : "r"((uint32_t)p), "r"(id) : "memory");
     return r != 0;
 }
+__device__ __forceinline__ void both_sync() { asm volatile("barrier.cta.sync 3, 256;" ::: "memory"); }
 __device__ __forceinline__ void stream_sync(int id) { asm volatile("barrier.cta.sync %0, 128;" ::"r"(id) : "memory"); }
 
 // fp32 bits as signed integers of the same order
@@ -142,8 +149,13 @@ __device__ __forceinline__ int ordered(float x) {
 }
 __device__ __forceinline__ float unordered(int i) { return __int_as_float(i ^ ((i >> 31) & 0x7fffffff)); }
 
+// Tiles up to which a CTA takes all tokens of its rows.
+constexpr int kDirectTiles = 8;
+
 // SCORES: every attended token's scores are kept (NR = 16 only).
-template <int D, int NR, int C, bool PG, bool SCORES>
+// DIRECT: grid = sequences x KV heads; a CTA has all tokens of its rows, merges its two streams and the other part, writes
+// out and lse, and (SCORES) adds the weights of the tokens, whose scores stayed in registers: no records, no second launch.
+template <int D, int NR, int C, bool PG, bool SCORES, bool DIRECT>
 __global__ void __launch_bounds__(RowsPlan<D, NR, C, PG>::kThreads, 1)
     shared_rows_kernel(const RowsArgs a, const __grid_constant__ CUtensorMap kmap,
                        const __grid_constant__ CUtensorMap vmap) {
@@ -204,7 +216,7 @@ __global__ void __launch_bounds__(RowsPlan<D, NR, C, PG>::kThreads, 1)
     grid_wait();
     if constexpr (coded) {                                           // an item's KV head is this CTA's: one item per CTA
         if constexpr (!PG) {
-            const int h = blockIdx.x / a.nsplit;
+            const int h = DIRECT ? blockIdx.x % a.Hkv : blockIdx.x / a.nsplit;
             fill_tables<C>(smem + P::offTable, a.slk + (size_t)h * a.K * C, a.slv + (size_t)h * a.K * C, a.K, P::kThreads);
         }
         for (int i = tid; i < D; i += P::kThreads)                   // row 64 is there when a second tile is
@@ -231,7 +243,10 @@ __global__ void __launch_bounds__(RowsPlan<D, NR, C, PG>::kThreads, 1)
         return x;
     };
     Item item0;
-    if (a.nsplit > 0) {
+    if constexpr (DIRECT) {
+        item0 = item_of(blockIdx.x / a.Hkv, blockIdx.x % a.Hkv, 0, INT32_MAX);
+        item0.left = item0.ntiles;
+    } else if (a.nsplit > 0) {
         const int split = blockIdx.x % a.nsplit, h = blockIdx.x / a.nsplit;
         item0 = item_of(0, h, 0, INT32_MAX);
         const long long tiles = item0.ntiles;
@@ -276,7 +291,7 @@ __global__ void __launch_bounds__(RowsPlan<D, NR, C, PG>::kThreads, 1)
     __syncthreads();
     tc::tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    if (a.nsplit == 0) {
+    if (!DIRECT && a.nsplit == 0) {
         const long long *info = reinterpret_cast<const long long *>(smem + P::offInfo);
         item0.ntiles = 0;
         item0.left = info[0];
@@ -285,7 +300,7 @@ __global__ void __launch_bounds__(RowsPlan<D, NR, C, PG>::kThreads, 1)
     // the next item with tiles; false behind the last
     auto advance = [&](Item &x) {
         const long long left = x.left - x.ntiles;
-        if (coded || left <= 0) return false;
+        if (coded || DIRECT || left <= 0) return false;
         int b = x.b, h = x.h;
         do {
             if (++b == a.seqs) {
@@ -311,15 +326,28 @@ __global__ void __launch_bounds__(RowsPlan<D, NR, C, PG>::kThreads, 1)
         float *corr = ref + NR;
         float *wmax = ref + 2 * NR;                                  // [4][NR]: a warp's maxima, later its sums
         volatile int *wok = reinterpret_cast<volatile int *>(ref + 6 * NR);
+        // 16 rows of O from their three accumulators
+        auto read_o = [](uint32_t at, int c, float (&v)[16]) {
+            uint32_t o[16], y[16], z[16];
+            tc::tmem_ld16(at + c, o);
+            tc::tmem_ld16(at + NR + c, y);
+            tc::tmem_ld16(at + 2 * NR + c, z);
+            tc::tmem_wait_ld16(o);
+            tc::tmem_wait_ld16(y);
+            tc::tmem_wait_ld16(z);
+#pragma unroll
+            for (int k = 0; k < 16; ++k) v[k] = __uint_as_float(o[k]) + (__uint_as_float(y[k]) + __uint_as_float(z[k]));
+        };
         const int cols = (a.R + 15) & ~15;                           // columns in use (padding rows: zero queries)
         int g = 0;                                                   // tiles of this CTA so far
         bool ok = true;
         Item x = item0;
-        for (bool more = a.nsplit > 0 || x.left > 0; more; more = advance(x)) {
+        for (bool more = DIRECT || a.nsplit > 0 || x.left > 0; more; more = advance(x)) {
             const size_t rec = x.rec + w * a.ss;
             float l[NR];
 #pragma unroll
             for (int r = 0; r < NR; ++r) l[r] = 0.f;
+            float kept[SCORES && DIRECT ? kDirectTiles / 2 : 1][8] = {};   // this token's scores in the stream's tiles
             int j = 0;                                               // tiles of this stream in the item
             for (int t = 0; ok && t < x.ntiles; ++t, ++g) {
                 if ((g & 1) != w) continue;
@@ -425,10 +453,19 @@ __global__ void __launch_bounds__(RowsPlan<D, NR, C, PG>::kThreads, 1)
                     uint32_t s[16];
                     tc::tmem_ld16(ts, s);
                     tc::tmem_wait_ld16(s);
-                    float *sc = a.ws_s + ((size_t)x.b * a.Hq + x.h * a.R) * a.sstride + n;
+                    if constexpr (DIRECT) {
 #pragma unroll
-                    for (int k = 0; k < 8; ++k)
-                        if (in && k < a.R) sc[(size_t)k * a.sstride] = __uint_as_float(s[k]) * a.qscale;
+                        for (int q = 0; q < kDirectTiles / 2; ++q)
+                            if (j == q) {
+#pragma unroll
+                                for (int k = 0; k < 8; ++k) kept[q][k] = __uint_as_float(s[k]) * a.qscale;
+                            }
+                    } else {
+                        float *sc = a.ws_s + ((size_t)x.b * a.Hq + x.h * a.R) * a.sstride + n;
+#pragma unroll
+                        for (int k = 0; k < 8; ++k)
+                            if (in && k < a.R) sc[(size_t)k * a.sstride] = __uint_as_float(s[k]) * a.qscale;
+                    }
                 }
 #pragma unroll
                 for (int c = 0; c < NR; c += 16) {
@@ -485,35 +522,115 @@ __global__ void __launch_bounds__(RowsPlan<D, NR, C, PG>::kThreads, 1)
             if (lane == 0) wok[wq] = ok;
             stream_sync(bar);
             const bool all_ok = wok[0] && wok[1] && wok[2] && wok[3];
-            if (tid % 128 < a.R) {
-                const int r = tid % 128;
-                const float sum = wmax[r] + wmax[NR + r] + wmax[2 * NR + r] + wmax[3 * NR + r];
-                // (a row whose every score is -inf has no weight)
-                a.ws_ml[rec + r] = !all_ok             ? f2(0.f, CUDART_NAN_F)
-                                          : j > 0 && sum != 0.f ? f2(-ref[r], sum)
-                                                              : f2(-CUDART_INF_F, 0.f);
-            }
-            if (all_ok && j > 0) {
+            if constexpr (DIRECT) {
+                // ---- merge of the streams: stream 1 hands its part over through the memory of both P, which every
+                // product has read by now
+                float *part = reinterpret_cast<float *>(smem + P::offP);           // [NR][D]
+                const float *ref1 = reinterpret_cast<const float *>(smem + P::offRef + P::kRef);
+                float *coef = reinterpret_cast<float *>(smem + P::offRef) + 2 * NR;  // c0, c1, other's; joint log2-sum-exp2
+                if (tid % 128 < a.R) {
+                    const int r = tid % 128;
+                    const float sum = wmax[r] + wmax[NR + r] + wmax[2 * NR + r] + wmax[3 * NR + r];
+                    corr[r] = !all_ok ? CUDART_NAN_F : j > 0 ? sum : 0.f;
+                }
+                both_sync();
+                if (w == 1 && j > 0) {
 #pragma unroll 1
-                for (int c = 0; c < cols; c += 16) {
-                    uint32_t o[16], y[16], z[16];
-                    tc::tmem_ld16(to + c, o);
-                    tc::tmem_ld16(to + NR + c, y);
-                    tc::tmem_ld16(to + 2 * NR + c, z);
-                    tc::tmem_wait_ld16(o);
-                    tc::tmem_wait_ld16(y);
-                    tc::tmem_wait_ld16(z);
-                    float *dst = a.ws_o + (rec + c) * D + chan;
+                    for (int c = 0; c < cols; c += 16) {
+                        float o[16];
+                        read_o(to, c, o);
 #pragma unroll
-                    for (int k = 0; k < 16; ++k)
-                        if (chan >= 0 && c + k < a.R)
-                            dst[k * D] = __uint_as_float(o[k]) + (__uint_as_float(y[k]) + __uint_as_float(z[k]));
+                        for (int k = 0; k < 16; ++k)
+                            if (chan >= 0 && c + k < a.R) part[(c + k) * D + chan] = o[k];
+                    }
+                }
+                auto dst = [&](int r) {
+                    return (size_t)(x.b * (a.R >> a.qshift) + (r >> a.qshift)) * a.Hq + (x.h << a.qshift) +
+                           (r & ((1 << a.qshift) - 1));
+                };
+                if (w == 0 && tid < a.R) {
+                    const int r = tid;
+                    const float s0 = corr[r], s1 = ref1[NR + r];
+                    const float m0 = s0 != 0.f ? -ref[r] : -CUDART_INF_F, m1 = s1 != 0.f ? -ref1[r] : -CUDART_INF_F;
+                    const float ol = a.other_lse ? a.other_lse[dst(r)] * 1.44269504088896340736f : -CUDART_INF_F;
+                    const float top = fmaxf(fmaxf(m0, m1), ol);
+                    float c0 = 0.f, c1 = 0.f, co = 0.f, l2 = -CUDART_INF_F;
+                    if (top != -CUDART_INF_F) {
+                        c0 = ex2(m0 - top);
+                        c1 = ex2(m1 - top);
+                        co = ex2(ol - top);
+                        const float total = s0 * c0 + s1 * c1 + co;
+                        l2 = top + log2f(total);
+                        c0 /= total;
+                        c1 /= total;
+                        co /= total;
+                    }
+                    if (s0 + s1 != s0 + s1) c0 = c1 = co = l2 = CUDART_NAN_F;   // a stream gave up
+                    coef[r] = c0;
+                    coef[NR + r] = c1;
+                    coef[2 * NR + r] = co;
+                    coef[3 * NR + r] = l2;
+                    if (a.lse != nullptr)
+                        a.lse[dst(r)] = l2 == -CUDART_INF_F ? -CUDART_INF_F : l2 * 0.69314718055994530942f;
+                }
+                both_sync();
+                if (w == 0) {
+#pragma unroll 1
+                    for (int c = 0; c < cols; c += 16) {
+                        float o[16];
+                        if (j > 0) read_o(to, c, o);
+#pragma unroll
+                        for (int k = 0; k < 16; ++k) {
+                            const int r = c + k;
+                            if (chan >= 0 && r < a.R) {
+                                float v = j > 0 ? o[k] * coef[r] : 0.f;
+                                if (coef[NR + r] != 0.f) v += part[r * D + chan] * coef[NR + r];
+                                if (coef[2 * NR + r] > 0.f) v += a.other_out[dst(r) * D + chan] * coef[2 * NR + r];
+                                if (coef[r] != coef[r]) v = coef[r];
+                                a.out[dst(r) * D + chan] = v;
+                            }
+                        }
+                    }
+                }
+                if constexpr (SCORES) {
+                    const size_t row = ((size_t)x.b * a.Hkv + x.h) * a.head_rows;
+#pragma unroll
+                    for (int q = 0; q < kDirectTiles / 2; ++q) {
+                        const int n = x.tok_first + (2 * q + w) * NT + token;
+                        if (q < j && n < x.len) {
+                            float sum = 0.f;
+#pragma unroll
+                            for (int k = 0; k < 8; ++k)
+                                if (k < a.R) sum += ex2(kept[q][k] - coef[3 * NR + k]);
+                            a.score_out[row + n] = (a.score_in ? a.score_in[row + n] : 0.f) + sum;
+                        }
+                    }
+                }
+            } else {
+                if (tid % 128 < a.R) {
+                    const int r = tid % 128;
+                    const float sum = wmax[r] + wmax[NR + r] + wmax[2 * NR + r] + wmax[3 * NR + r];
+                    // (a row whose every score is -inf has no weight)
+                    a.ws_ml[rec + r] = !all_ok             ? f2(0.f, CUDART_NAN_F)
+                                       : j > 0 && sum != 0.f ? f2(-ref[r], sum)
+                                                           : f2(-CUDART_INF_F, 0.f);
+                }
+                if (all_ok && j > 0) {
+#pragma unroll 1
+                    for (int c = 0; c < cols; c += 16) {
+                        float o[16];
+                        read_o(to, c, o);
+                        float *dst = a.ws_o + (rec + c) * D + chan;
+#pragma unroll
+                        for (int k = 0; k < 16; ++k)
+                            if (chan >= 0 && c + k < a.R) dst[k * D] = o[k];
+                    }
                 }
             }
             tc::tc_fence_before();
             stream_sync(bar);                                        // the next item writes ref again
             ok = all_ok;
-            if (!ok) {                                               // the records of the items left: NaN
+            if (!DIRECT && !ok) {                                    // the records of the items left: NaN
                 while (advance(x))
                     if (tid % 128 < a.R) a.ws_ml[x.rec + w * a.ss + tid % 128] = f2(0.f, CUDART_NAN_F);
                 break;

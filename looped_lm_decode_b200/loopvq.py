@@ -367,7 +367,8 @@ def _on_stream(stream, *tensors):
     """Memory made on the current stream and used on another is not reused before that stream is done with it."""
     if stream is not None:
         for t in tensors:
-            t.record_stream(stream)
+            if t is not None:
+                t.record_stream(stream)
 
 
 _sizes = {}
@@ -385,12 +386,15 @@ def _ws_size(fn, ref, *key):
 
 
 def _workspace(workspace, need: int, like: torch.Tensor):
+    """(tensor, address, bytes); none where the call needs none."""
     if workspace is None:
-        need = max(need, 16)
-        return torch.empty_strided((need,), (1,), dtype=torch.uint8, device=like.device), need
+        if need == 0:
+            return None, None, 0
+        workspace = torch.empty_strided((need,), (1,), dtype=torch.uint8, device=like.device)
+        return workspace, workspace.data_ptr(), need
     if workspace.device != like.device or not workspace.is_contiguous():
         raise LoopVQError(LOOPVQ_ERR_INVALID_ARG, f"workspace must be contiguous memory on {like.device}")
-    return workspace, workspace.numel() * workspace.element_size()
+    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
 def _need_current(device):
@@ -439,10 +443,10 @@ def bf16_shared_attn(cache: Bf16Cache, seq: int, q: torch.Tensor, lens: torch.Te
     if rows == 0:
         return out, lse
     L, ref = lib(), cache.ref()
-    workspace, n = _workspace(workspace, _ws_size(L.loopvq_bf16_shared_workspace_bytes, ref, "bf16", cache.B, cache.Hkv, cache.Hq,
+    workspace, ws, n = _workspace(workspace, _ws_size(L.loopvq_bf16_shared_workspace_bytes, ref, "bf16", cache.B, cache.Hkv, cache.Hq,
                                              cache.D, cache.Nmax, rows, max_len), q)
     _check(L.loopvq_bf16_shared_attn(ref, seq, q.data_ptr(), rows, _ptr(starts), lens.data_ptr(), max_len, scale,
-                                     _ptr(oo), _ptr(ol), out.data_ptr(), lse.data_ptr(), workspace.data_ptr(), n,
+                                     _ptr(oo), _ptr(ol), out.data_ptr(), lse.data_ptr(), ws, n,
                                      _stream(stream)))
     _on_stream(stream, out, lse, workspace)
     return out, lse
@@ -456,10 +460,10 @@ def shared_attn(cache: Cache, layer: int, t: int, seq: int, q: torch.Tensor, len
     if rows == 0:
         return out, lse
     L, ref = lib(), cache.ref()
-    workspace, n = _workspace(workspace, _ws_size(L.loopvq_shared_workspace_bytes, ref, "coded", cache.B, cache.Hkv, cache.Hq,
+    workspace, ws, n = _workspace(workspace, _ws_size(L.loopvq_shared_workspace_bytes, ref, "coded", cache.B, cache.Hkv, cache.Hq,
                                              cache.D, cache.Nmax, rows, max_len), q)
     _check(L.loopvq_shared_attn(ref, layer, t, seq, q.data_ptr(), rows, _ptr(starts), lens.data_ptr(), max_len, scale,
-                                _ptr(oo), _ptr(ol), out.data_ptr(), lse.data_ptr(), workspace.data_ptr(), n,
+                                _ptr(oo), _ptr(ol), out.data_ptr(), lse.data_ptr(), ws, n,
                                 _stream(stream)))
     _on_stream(stream, out, lse, workspace)
     return out, lse
@@ -491,11 +495,11 @@ def bf16_decode_attn_scored(cache: Bf16Cache, q: torch.Tensor, lens: torch.Tenso
     oo, ol = _need_other(other, B, Hq, D, dev)
     out, lse = _result(out, "out", (B, Hq, D), q), _result(lse, "lse", (B, Hq), q)
     L, ref = lib(), cache.ref()
-    workspace, n = _workspace(workspace, _ws_size(L.loopvq_bf16_scored_workspace_bytes, ref, "scored", B, cache.Hkv, Hq, D,
+    workspace, ws, n = _workspace(workspace, _ws_size(L.loopvq_bf16_scored_workspace_bytes, ref, "scored", B, cache.Hkv, Hq, D,
                                              cache.Nmax, max_len), q)
     _check(L.loopvq_bf16_decode_attn_scored(ref, q.data_ptr(), _ptr(starts), lens.data_ptr(), max_len, scale, _ptr(oo),
                                             _ptr(ol), _ptr(score), score_out.data_ptr(), out.data_ptr(),
-                                            lse.data_ptr(), workspace.data_ptr(), n, _stream(stream)))
+                                            lse.data_ptr(), ws, n, _stream(stream)))
     _on_stream(stream, out, lse, workspace)
     return out, lse, score_out
 
@@ -522,11 +526,11 @@ def bf16_evict(cache: Bf16Cache, score: torch.Tensor, pos: torch.Tensor, lens: t
     for t, name in ((lens, "lens"), (next_pos, "next_pos"), (lens_out, "lens_out")):
         _need(t, name, (B,), _I32, dev)
     L, ref = lib(), cache.ref()
-    workspace, n = _workspace(workspace, _ws_size(L.loopvq_bf16_evict_workspace_bytes, ref, "evict", B, H, cache.Hq, cache.D, N,
+    workspace, ws, n = _workspace(workspace, _ws_size(L.loopvq_bf16_evict_workspace_bytes, ref, "evict", B, H, cache.Hq, cache.D, N,
                                              max_len, budget), lens)
     _check(L.loopvq_bf16_evict(ref, score.data_ptr(), pos.data_ptr(), lens.data_ptr(), next_pos.data_ptr(), max_len,
                                budget, n_sink, n_recent, score_out.data_ptr(), pos_out.data_ptr(),
-                               lens_out.data_ptr(), workspace.data_ptr(), n, _stream(stream)))
+                               lens_out.data_ptr(), ws, n, _stream(stream)))
     _on_stream(stream, workspace)
     return score_out, pos_out, lens_out
 
