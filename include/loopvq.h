@@ -219,7 +219,8 @@ loopvq_status loopvq_merge2(const float *out_a, const float *lse_a, const float 
                             const float *lse_b, int rows, int D, float *out, float *lse,
                             void *stream);
 
-/* Workspace bytes loopvq_bf16_shared_attn / loopvq_shared_attn need for `rows` queries and up to max_len tokens. */
+/* Workspace bytes loopvq_bf16_shared_attn / loopvq_shared_attn need for `rows` queries and up to max_len tokens.
+ * Here and for the two calls below 0 is an answer: the call runs without a workspace (NULL and 0 are accepted). */
 size_t loopvq_bf16_shared_workspace_bytes(const loopvq_bf16_cache *cache, int rows, int max_len);
 size_t loopvq_shared_workspace_bytes(const loopvq_cache *cache, int rows, int max_len);
 

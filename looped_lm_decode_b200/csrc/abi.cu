@@ -88,6 +88,19 @@ cudaError_t ensure_dynamic_smem(const void *kern, size_t bytes) {
     if (e == cudaSuccess) cur = bytes;
     return e;
 }
+cudaError_t allow_large_clusters(const void *kern) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    static std::mutex mu;
+    static std::map<std::pair<const void *, int>, bool> done;
+    std::lock_guard<std::mutex> lock(mu);
+    bool &set = done[{kern, dev}];
+    if (set) return cudaSuccess;
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    set = e == cudaSuccess;
+    return e;
+}
 }  // namespace loopvq
 
 extern "C" {
@@ -432,11 +445,7 @@ loopvq_status loopvq_bf16_evict(const loopvq_bf16_cache *c, const float *score_i
     LQ_TRY(check_same_or_apart(score_in, score_out, words, "score_out"));
     LQ_TRY(check_same_or_apart(pos_in, pos_out, words, "pos_out"));
     LQ_TRY(check_same_or_apart(lens_in, lens_out, (size_t)c->B * 4, "lens_out"));
-    const size_t need = loopvq::evict_ws_bytes(c->B, c->Hkv, max_len, budget);
-    if (!workspace || ws_bytes < need)
-        return fail(LOOPVQ_ERR_WORKSPACE, "workspace of %zu bytes needed, %zu given", need,
-                    workspace ? ws_bytes : (size_t)0);
-    if (!aligned16(workspace)) return fail(LOOPVQ_ERR_INVALID_ARG, "workspace is not 16-byte aligned");
+    LQ_TRY(check_ws(workspace, ws_bytes, loopvq::evict_ws_bytes(c->B, c->Hkv, max_len, budget)));
     loopvq::EvictArgs a{};
     a.k = const_cast<uint16_t *>(c->k);
     a.v = const_cast<uint16_t *>(c->v);

@@ -492,17 +492,29 @@ int evict_cap(int max_len, int budget) {
 
 }  // namespace
 
+// One launch where a head moves at most kFusedRows rows of a short row (a step's eviction: a CTA moves them while others
+// still select) and a cluster can hold a sequence's heads: the lengths are written behind its barrier.  It needs no
+// workspace.
+constexpr int kFusedRows = 256;                                      // their lists fit into the kernel's list
+constexpr int kShortRow = 2560, kClusterHeads = 16;                  // 16: more than 8 have to be asked for
+static_assert(2 * kFusedRows <= kList, "moved rows' lists");
+static bool fused_evict(int Hkv, int max_len, int budget) {
+    return max_len <= kShortRow && evict_cap(max_len, budget) <= kFusedRows && Hkv <= kClusterHeads;
+}
+
 size_t evict_ws_bytes(int B, int Hkv, int max_len, int budget) {
+    if (fused_evict(Hkv, max_len, budget)) return 0;
     return (size_t)B * Hkv * (1 + 2 * (size_t)evict_cap(max_len, budget)) * sizeof(int32_t);
 }
 
-// One launch where a head moves at most kFusedRows rows (a step's eviction; a CTA moves them while others still select)
-// and a cluster can hold a sequence's heads, or needs not; two otherwise.
-constexpr int kFusedRows = 256;                                      // their lists fit into the kernel's list
-static_assert(2 * kFusedRows <= kList, "moved rows' lists");
-
 template <int NT, typename Keys, int FUSED_D, int CL>
 static cudaError_t launch_select(const EvictArgs &a, cudaStream_t s) {
+    auto kern = evict_select_kernel<NT, Keys, FUSED_D, CL>;
+    const bool heads = FUSED_D > 0 && a.lens_out == a.lens_in;       // a cluster of the sequence's heads
+    if (heads && a.Hkv > 8) {
+        const cudaError_t e = allow_large_clusters((const void *)kern);
+        if (e != cudaSuccess) return e;
+    }
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(a.B * a.Hkv * CL);
     cfg.blockDim = dim3(NT);
@@ -514,8 +526,8 @@ static cudaError_t launch_select(const EvictArgs &a, cudaStream_t s) {
     at[1].val.clusterDim.x = CL > 1 ? CL : a.Hkv;
     at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
     cfg.attrs = at;
-    cfg.numAttrs = CL > 1 || (FUSED_D > 0 && a.lens_out == a.lens_in) ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, evict_select_kernel<NT, Keys, FUSED_D, CL>, a);
+    cfg.numAttrs = CL > 1 || heads ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kern, a);
 }
 
 // A row is a budget and a little more, and budgets tend to be powers of two: register capacities a quarter above those.
@@ -537,9 +549,9 @@ static cudaError_t launch_long(const EvictArgs &a, cudaStream_t s) {
 cudaError_t launch_evict(const EvictArgs &args, cudaStream_t s) {
     EvictArgs a = args;
     a.cap = evict_cap(a.max_len, a.budget);
-    if (a.max_len <= 2560 && a.cap <= kFusedRows && (a.lens_out != a.lens_in || a.Hkv <= 8))
+    if (fused_evict(a.Hkv, a.max_len, a.budget))
         return a.D == 128 ? launch_short<128>(a, s) : launch_short<64>(a, s);
-    const cudaError_t e = a.max_len <= 2560 ? launch_short<0>(a, s) : launch_long(a, s);
+    const cudaError_t e = a.max_len <= kShortRow ? launch_short<0>(a, s) : launch_long(a, s);
     if (e != cudaSuccess) return e;
     const dim3 grid((unsigned)((a.cap + kMoveRows - 1) / kMoveRows > 0 ? (a.cap + kMoveRows - 1) / kMoveRows : 1),
                     (unsigned)(a.B * a.Hkv));

@@ -56,6 +56,8 @@ unsigned long long wait_limit_ns();
 // launches make no attribute call: less host time per call, and nothing but launches inside a CUDA
 // graph capture.
 cudaError_t ensure_dynamic_smem(const void *kern, size_t bytes);
+// Lets a kernel run in clusters of more than 8 CTAs on the current device (set once per kernel and device).
+cudaError_t allow_large_clusters(const void *kern);
 
 // Programmatic dependent launch: a kernel launched by launch_pdl may be set up while the kernel before it in the
 // stream still runs; grid_wait() holds it until that kernel is done and its writes are visible, so it comes before the

@@ -203,7 +203,7 @@ def test_evict_long(nmax, scores):
     run_evict(2, 1, 64, nmax, [nmax, nmax - 7], nmax // 3, 8, 64, True, scores)
 
 
-@pytest.mark.parametrize("hkv,in_place", [(1, True), (8, True), (8, False), (9, True), (16, False)])
+@pytest.mark.parametrize("hkv,in_place", [(1, True), (8, True), (8, False), (9, True), (16, True), (16, False), (17, True)])
 @pytest.mark.parametrize("budget", [1024, 1300, 1700])
 def test_evict_few_and_many_rows(hkv, in_place, budget):
     """Steps that one launch does, with clusters of a sequence's heads and without, and those that two do."""
