@@ -365,6 +365,7 @@ __global__ void __launch_bounds__(kScoreThreads) bf16_scored_merge_kernel(const 
                 ws = sum > 0.f ? ea / (sum * (ea + eb)) : 0.f;
                 wo = eb / (ea + eb);
             }
+            if (sum != sum) l2 = ws = wo = CUDART_NAN_F;   // a tensor-core CTA gave up, or a key or query was NaN
             s_mx[g] = mx;
             s_l2[g] = l2;
             s_scale[g] = ws;
@@ -385,7 +386,7 @@ __global__ void __launch_bounds__(kScoreThreads) bf16_scored_merge_kernel(const 
                 const float x = ml[sp * rec_i].x, y = o[sp * rec_i * D];
                 acc += x != -CUDART_INF_F ? y * ex2(x - s_mx[g]) : 0.f;   // a record without tokens has no output
             }
-            float r = acc * s_scale[g];
+            float r = s_scale[g] != 0.f ? acc * s_scale[g] : 0.f;
             if (s_other[g] > 0.f) r += s_other[g] * a.other_out[bh * D + d];
             out[bh * D + d] = r;
             if (lse != nullptr && d == 0)

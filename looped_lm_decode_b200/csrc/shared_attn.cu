@@ -15,7 +15,7 @@
 // they take the two halves of the rows (and share every tile).
 //
 // Precision: the library returns fp32, so P is not rounded to bf16 once but split into two bf16 parts (the
-// remainder of the first rounding in the second, 2^-18 of P at most), two products into the same accumulator; a
+// remainder of the first rounding in the second, which leaves 2^-17 of P at most), two products into the same accumulator; a
 // rebuilt, rotated key is split the same way.  bf16 queries, keys and values are exact.
 //
 // P overwrites S in place, 16 score columns becoming 8 + 8 columns of packed pairs (one product's tokens).  The running maximum moves

@@ -3,7 +3,7 @@
 Tolerances, before any run.  A score is a sum of D products in fp32 (8 per lane in pairs, then 4 exchanges, the
 query rounded once for the scale): under 24 roundings of relative size 2^-24 against sum |q k| scale, about
 sqrt(D) for normal inputs, at most 2e-5; ex2 adds 2^-22, so a weight is off by at most DELTA = 4e-5 of itself with
-the log-sum-exp's own error.  Sums over tokens run in fp32 over at most some hundred terms per lane: 2^-24 each
+the log-sum-exp's own error (a tensor-core sum of the exact products, 8 roundings of 2^-22, is within the same 2e-5).  Sums over tokens run in fp32 over at most some hundred terms per lane: 2^-24 each
 against the sum of absolute terms.  An output is held to 2 DELTA + 1e-4 / 4 < 1.1e-4 of sum p |v|."""
 import math
 
@@ -105,20 +105,78 @@ def test_scored_decode_in_place_without_scores_and_repeated():
     assert torch.allclose(s3, 2 * s1, rtol=1e-6, atol=0)
 
 
-def test_scored_decode_does_not_read_masked_values():
-    """Infinities and NaN in the slots before the start and behind the length change nothing."""
-    cache, q, _ = make(2, 2, 4, 300, 64, nmax=304)
-    starts, lens = [5, 66], [297, 131]
+@pytest.mark.parametrize("hq,n", [(2, 300), (4, 300), (2, 1500), (4, 1500)])
+def test_scored_decode_does_not_read_masked_values(hq, n):
+    """Infinities and NaN in the slots before the start and behind the length change nothing (one launch, the split
+    kernel, the tensor cores)."""
+    cache, q, _ = make(2, 2, hq, n, 64, nmax=n + 4)
+    starts, lens = [5, 66], [n - 3, 131]
     args = dict(starts=torch.tensor(starts, dtype=torch.int32, device="cuda"))
     ln = torch.tensor(lens, dtype=torch.int32, device="cuda")
-    clean = LQ.bf16_decode_attn_scored(cache, q, ln, 300, None, score_out=torch.zeros(2, 2, 304, device="cuda"), **args)
+    zeros = torch.zeros(2, 2, n + 4, device="cuda")
+    clean = LQ.bf16_decode_attn_scored(cache, q, ln, n, None, score_out=zeros.clone(), **args)
     for b in range(2):
         for x in (cache.k, cache.v):
             x[b, :, :starts[b]] = math.nan
             x[b, :, lens[b]:] = math.inf
-    dirty = LQ.bf16_decode_attn_scored(cache, q, ln, 300, None, score_out=torch.zeros(2, 2, 304, device="cuda"), **args)
+    dirty = LQ.bf16_decode_attn_scored(cache, q, ln, n, None, score_out=zeros.clone(), **args)
     for x, y in zip(clean, dirty):
         assert torch.equal(x, y)
+
+
+@pytest.mark.parametrize("b,hkv,hq,n", [(40, 4, 16, 900), (40, 4, 4, 900), (7, 2, 16, 6000), (150, 1, 2, 1100)])
+def test_scored_decode_of_ragged_batches(b, hkv, hq, n):
+    """More (sequence, KV head) pairs than SMs, pieces that end inside a sequence, sequences without tokens."""
+    cache, q, g = make(b, hkv, hq, n, 64, seed=b)
+    lens = [(i * 7919 * n // 10007) % (n + 1) if i % 5 else 0 for i in range(b)]
+    lens[1], lens[-1] = n, 1
+    starts = [0] * b
+    score = torch.rand(b, hkv, n, generator=g, device="cuda")
+    got = LQ.bf16_decode_attn_scored(cache, q, torch.tensor(lens, dtype=torch.int32, device="cuda"), n, score,
+                                     score_out=torch.zeros_like(score))
+    check(got, reference(cache, q, starts, lens, None), score, torch.zeros_like(score), starts, lens)
+    for _ in range(3):                                               # equal inputs give equal bits
+        again = LQ.bf16_decode_attn_scored(cache, q, torch.tensor(lens, dtype=torch.int32, device="cuda"), n, score,
+                                           score_out=torch.zeros_like(score))
+        assert all(torch.equal(x, y) for x, y in zip(got, again))
+
+
+def test_scored_decode_with_far_scores():
+    """Scores that leave the first tokens' reference by more than the exponent's range."""
+    for n in (600, 3000):
+        cache, q, g = make(1, 1, 2, n, 64, seed=3)
+        q[:] = 1
+        cache.k[:] = 0
+        cache.k[0, 0, :, 0] = torch.linspace(-3000, 3000, n, device="cuda").bfloat16()   # scores to +- 375
+        lens = torch.tensor([n], dtype=torch.int32, device="cuda")
+        out, lse, score = LQ.bf16_decode_attn_scored(cache, q, lens, n, None, score_out=torch.zeros(1, 1, n, device="cuda"))
+        ro, rl, w, mag = reference(cache, q, [0], [n], None)
+        # exact products (one term each): what is left is the exponent, 375 log2(e) at 2^-24 each of a few roundings
+        assert ((lse.double() - rl).abs() <= 4 * 2.0 ** -23 * 375).all()
+        assert ((out.double() - ro).abs() <= 1e-3 * mag + 1e-30).all()
+        assert ((score.double() - w).abs() <= 1e-3 * w + 1e-30).all()
+
+
+@pytest.mark.parametrize("n", [700, 1500])
+def test_scored_decode_reports_a_wait_that_runs_out(n):
+    cache, q, _ = make(2, 2, 4, n, 64)
+    lens = torch.tensor([n, n // 2], dtype=torch.int32, device="cuda")
+    call = lambda: LQ.bf16_decode_attn_scored(cache, q, lens, n, None, score_out=torch.zeros(2, 2, n, device="cuda"))  # noqa: E731
+    good = call()
+    LQ.fault_check()
+    before = LQ.wait_limit_ns()
+    LQ.set_wait_limit_ns(0)
+    try:
+        bad = call()
+        with pytest.raises(LQ.LoopVQError) as e:
+            LQ.fault_check()
+        assert e.value.status == 5
+        assert bad[0].isnan().all() and bad[1].isnan().all()
+    finally:
+        LQ.set_wait_limit_ns(before)
+    again = call()
+    LQ.fault_check()
+    assert all(torch.equal(x, y) for x, y in zip(good, again))
 
 
 def evict_reference(k, v, score, pos, lens, next_pos, budget, n_sink, n_recent):
