@@ -1,4 +1,5 @@
-"""Build libloopvq.so (the C-ABI library) in-tree for sm_100a with nvcc."""
+"""Build libloopvq.so (the C-ABI library) in-tree for sm_100a with nvcc: the sources side by side, then one link."""
+import concurrent.futures
 import glob
 import os
 import subprocess
@@ -6,28 +7,39 @@ import sys
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
+OBJ = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libloopvq.so")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
-FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-shared", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",
-         "--expt-relaxed-constexpr"]
+FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2", "--expt-relaxed-constexpr"]
 
 
 def sources():
     return sorted(glob.glob(os.path.join(CSRC, "*.cu")))
 
 
-def _stale(lib, deps):
-    if not os.path.exists(lib):
+def _stale(out, deps):
+    if not os.path.exists(out):
         return True
-    t = os.path.getmtime(lib)
+    t = os.path.getmtime(out)
     return any(os.path.getmtime(d) > t for d in deps)
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
-    deps = sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + [os.path.join(HERE, "..", "include", "loopvq.h")]
-    if force or _stale(LIB, deps):
-        cmd = ["nvcc"] + ARCH + FLAGS + (["-Xptxas", "-v"] if verbose else []) + ["-o", LIB] + sources()
-        subprocess.check_call(cmd)
+    headers = glob.glob(os.path.join(CSRC, "*.cuh")) + [os.path.join(HERE, "..", "include", "loopvq.h")]
+    if not force and not _stale(LIB, sources() + headers):
+        return LIB
+    os.makedirs(OBJ, exist_ok=True)
+
+    def compile_one(src):
+        obj = os.path.join(OBJ, os.path.basename(src)[:-3] + ".o")
+        if force or _stale(obj, [src] + headers):
+            subprocess.check_call(["nvcc"] + ARCH + FLAGS + (["-Xptxas", "-v"] if verbose else []) +
+                                  ["-c", "-o", obj, src])
+        return obj
+
+    with concurrent.futures.ThreadPoolExecutor(max(1, os.cpu_count() or 1)) as pool:
+        objs = list(pool.map(compile_one, sources()))
+    subprocess.check_call(["nvcc"] + ARCH + ["-shared", "-Xcompiler", "-fPIC", "-o", LIB] + objs)
     return LIB
 
 

@@ -112,7 +112,7 @@ struct RowsPlan {
     static constexpr int offTmem = offBar + kBars * 8;
     static constexpr int kUsed = offTmem + 16;
     static constexpr int kAlloc = kUsed + 1024;
-    static constexpr int kMma = coded ? 16 : 8, kCopy = 9, kRebuild = 8, kValues = 17, kQuery = coded ? 19 : 10;
+    [[maybe_unused]] static constexpr int kMma = coded ? 16 : 8, kCopy = 9, kRebuild = 8, kValues = 17, kQuery = coded ? 19 : 10;
     static constexpr int kThreads = (kQuery + 1) * 32;
     static constexpr int kCols = 256;                                // stream w: S at 32 w, O at 64 + 96 w
     static_assert(kAlloc <= 232448, "shared memory");
