@@ -19,8 +19,8 @@
 //
 // A CTA works through items (sequence, KV head, split) with its copies running ahead across them, so that a batch of
 // ragged sequences keeps every SM's copies in flight.  Warps: 0-3 and 4-7 softmax of the two streams that take the tiles
-// in turn; then the products' issuing warp, the copying one (bf16 cache: TMA; coded cache: eight warps that rebuild keys, two that rebuild values) and
-// one that loads the queries.
+// in turn; then two that issue the products, the copying one (bf16 cache: TMA; coded cache: eight warps that rebuild
+// keys, two that rebuild values) and one that loads the queries.
 #pragma once
 
 #include <cuda.h>
@@ -112,8 +112,9 @@ struct RowsPlan {
     static constexpr int offTmem = offBar + kBars * 8;
     static constexpr int kUsed = offTmem + 16;
     static constexpr int kAlloc = kUsed + 1024;
-    [[maybe_unused]] static constexpr int kMma = coded ? 16 : 8, kCopy = 9, kRebuild = 8, kValues = 17, kQuery = coded ? 19 : 10;
-    static constexpr int kThreads = (kQuery + 1) * 32;
+    [[maybe_unused]] static constexpr int kMma = coded ? 16 : 8, kCopy = 9, kRebuild = 8, kValues = 17, kQuery = coded ? 19 : 10,
+                         kPv = coded ? kQuery : 11;
+    static constexpr int kThreads = (kPv + 1) * 32;
     static constexpr int kCols = 256;                                // stream w: S at 32 w, O at 64 + 96 w
     static_assert(kAlloc <= 232448, "shared memory");
     static_assert(offStage % 1024 == 0 && offP % 1024 == 0 && offQ % 1024 == 0 && kP % 512 == 0, "swizzle atoms");
@@ -204,7 +205,7 @@ __global__ void __launch_bounds__(RowsPlan<D, NR, C, PG>::kThreads, 1)
                 tc::mbar_init(pfull(w), 128);
                 tc::mbar_init(odone(w), 1);
             }
-            tc::mbar_init(drain, 1);
+            tc::mbar_init(drain, 2);
             *dead = 0;
             asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         }
@@ -351,7 +352,10 @@ __global__ void __launch_bounds__(RowsPlan<D, NR, C, PG>::kThreads, 1)
             int j = 0;                                               // tiles of this stream in the item
             for (int t = 0; ok && t < x.ntiles; ++t, ++g) {
                 if ((g & 1) != w) continue;
-                ok = __all_sync(0xffffffffu, tc::mbar_wait_or_dead(sfull(w), (g >> 1) & 1, a.wait_ns, dead));
+                // S of this step; and P of the stream's step before is read, O written
+                bool came = tc::mbar_wait_or_dead(sfull(w), (g >> 1) & 1, a.wait_ns, dead);
+                if (g >= 2) came = came && tc::mbar_wait_or_dead(odone(w), ((g >> 1) - 1) & 1, a.wait_ns, dead);
+                ok = __all_sync(0xffffffffu, came);
                 tc::tc_fence_after();
                 const int n = x.tok_first + t * NT + token;
                 const bool in = token >= 0 && n >= x.st && n < x.len;
@@ -429,13 +433,6 @@ __global__ void __launch_bounds__(RowsPlan<D, NR, C, PG>::kThreads, 1)
                     for (int r2 = 0; r2 < NR; ++r2)
                         if (r2 < cols) l[r2] *= corr[r2];
                     if (j > 0) {
-                        bool done = tc::mbar_wait_or_dead(odone(w), ((g >> 1) - 1) & 1, a.wait_ns, dead);
-                        done = __all_sync(0xffffffffu, done);
-                        if (stream_any(bar, !done)) {
-                            ok = false;
-                            break;
-                        }
-                        tc::tc_fence_after();
 #pragma unroll 1
                         for (int c = 0; c < PARTS * NR; c += 16) {
                             uint32_t o[16];
@@ -637,126 +634,104 @@ __global__ void __launch_bounds__(RowsPlan<D, NR, C, PG>::kThreads, 1)
             }
         }
     } else if (warp == P::kMma) {
-        // ---- products.  QK of step g + 2 follows PV of step g: S and P of its stream are free then
-        constexpr uint32_t id_qk = tc::idesc_bf16(NT, NR);
-        constexpr uint32_t id_pv = tc::idesc_bf16(D, PARTS * NR) | (1u << 15) | (1u << 16);   // both: contraction outside
-        const long long total = item0.left;                          // what will not be used again is not freed
-        auto ready = [&](uint32_t b, uint32_t parity) { return __all_sync(0xffffffffu, tc::mbar_test(b, parity)); };
-        // two walks over the tiles: S runs up to two steps ahead
-        struct Walk {
-            Item x;
-            int it, t;                                               // the item's number, its tile
-        };
-        Walk s{item0, 0, 0}, p{item0, 0, 0};
-        auto qk = [&](long long g64) {
-            const int g = (int)g64;
-            const int sg = g % ST;
-            if (s.t == 0 && !ready(qfull(s.it % NQ), (s.it / NQ) & 1)) return false;
-            if (!ready(kfull(sg), (g / ST) & 1)) return false;
+        // ---- S^T = K Q^T.  The two kinds of products have a warp each: a product takes 46 clocks and more to issue, and
+        // one that waits for its copy must not hold up another whose tile, once read, makes room for the next
+        constexpr uint32_t id_qk = tc::idesc_bf16(NT, NR), hi = tc::desc_hi(1024, 2);
+        Item x = item0;
+        int it = 0, t = 0;                                           // the item's number, its tile
+        for (long long g64 = 0, total = item0.left; g64 < total; ++g64) {
+            const int g = (int)g64, sg = g % ST, w = g & 1;
+            bool came = t > 0 || tc::mbar_wait_or_dead(qfull(it % NQ), (it / NQ) & 1, a.wait_ns, dead);
+            came = came && tc::mbar_wait_or_dead(kfull(sg), (g / ST) & 1, a.wait_ns, dead);
+            if (g >= 2) came = came && tc::mbar_wait_or_dead(pfull(w), ((g >> 1) - 1) & 1, a.wait_ns, dead);   // S is read
+            if (!__all_sync(0xffffffffu, came)) break;
             tc::tc_fence_after();
-            const bool last = s.t + 1 == s.x.ntiles;
-            constexpr uint32_t hi = tc::desc_hi(1024, 2);
+            const bool last = t + 1 == x.ntiles;
             const uint32_t k_lo = tc::uniform(tc::desc_lo(sStage + sg * P::kStage, 16));
-            const uint32_t q_lo = tc::uniform(tc::desc_lo(base + P::offQ + (s.it % NQ) * P::kQ, 16));
-            const uint32_t sd = tc::uniform(tmem + (g & 1) * 32);
+            const uint32_t q_lo = tc::uniform(tc::desc_lo(base + P::offQ + (it % NQ) * P::kQ, 16));
+            const uint32_t sd = tc::uniform(tmem + w * 32);
             if (tc::elect_one()) {
 #pragma unroll
                 for (int part = 0; part < KP; ++part)
 #pragma unroll
                     for (int k = 0; k < D / 16; ++k)                 // 16 channels per product: 32 bytes of a row
-                        tc::mma_ss(sd,
-                                   k_lo + (part * P::kTile + (k / 4) * P::kPanel + (k % 4) * 32) / 16, hi,
+                        tc::mma_ss(sd, k_lo + (part * P::kTile + (k / 4) * P::kPanel + (k % 4) * 32) / 16, hi,
                                    q_lo + ((k / 4) * (NR * 128) + (k % 4) * 32) / 16, hi, id_qk, part + k > 0);
-                if (g + ST < total) tc::mma_commit(kempty(sg));
-                if (last && g + 1 < total) tc::mma_commit(qempty(s.it % NQ));
-                tc::mma_commit(sfull(g & 1));
+                tc::mma_commit(sfull(w));
+                if (g + ST < total) tc::mma_commit(kempty(sg));      // what will not be used again is not freed
+                if (last && g + 1 < total) tc::mma_commit(qempty(it % NQ));
             }
             __syncwarp();
-            ++s.t;
-            if (last) {
-                advance(s.x);
-                s.t = 0;
-                ++s.it;
-            }
-            return true;
-        };
-        auto pv = [&](long long g64) {
-            const int g = (int)g64;
-            const int sg = g % ST, w = g & 1;
-            const uint32_t vb = sStage + sg * P::kStage + KP * P::kTile;
-            if (!ready(pfull(w), (g >> 1) & 1) || !ready(vfull(sg), (g / ST) & 1)) return false;
-            if constexpr (!coded) {
-                // rows behind the last token may hold anything: 0 x that has to be 0
-                const int end = p.x.len - (p.x.tok_first + p.t * NT);
-                if (end < NT) {
-                    for (int it = lane; it < (NT - end) * (D / 8); it += 32) {
-                        const int n = end + it / (D / 8), ch = it % (D / 8);
-                        sts128(vb + (ch / 8) * P::kPanel + n * 128 + (ch % 8) * 16, make_uint4(0, 0, 0, 0));
-                    }
-                    tc::fence_async_smem();
-                    __syncwarp();
-                }
-            }
-            tc::tc_fence_after();
-            const uint32_t p_lo = tc::uniform(tc::desc_lo(base + P::offP + w * P::kP, P::kPart));
-            const uint32_t v_lo = tc::uniform(tc::desc_lo(vb, P::kPanel)), od = tc::uniform(tmem + 64 + w * 96);
-            const uint32_t more = tc::uniform(p.t >= 2);             // else O of this stream holds nothing of the item yet
-            if (tc::elect_one()) {
-#pragma unroll
-                for (int k = 0; k < NT / 16; ++k)                    // 16 tokens per product
-                    tc::mma_ss(od, v_lo + k * 128, tc::desc_hi(1024, 2), p_lo + k * (2 * NR),
-                               tc::desc_hi(8 * NR * 2, NR == 16 ? 6 : 4), id_pv, k > 0 ? 1u : more);
-                if (g + ST < total) tc::mma_commit(vempty(sg));
-                tc::mma_commit(odone(w));
-            }
-            __syncwarp();
-            if (++p.t == p.x.ntiles) {
-                advance(p.x);
-                p.t = 0;
-            }
-            return true;
-        };
-        // whichever product is ready goes first: one that waits for its copy must not hold up another whose tile,
-        // once read, makes room for the next copy
-        long long gs = 0, gp = 0;
-        uint64_t t0 = tc::globaltimer();
-        while (gp < total) {
-            bool went = gs < total && gs < gp + 2 && qk(gs);
-            gs += went;
-            if (gp < gs && pv(gp)) {
-                ++gp;
-                went = true;
-            }
-            if (went) {
-                t0 = tc::globaltimer();
-            } else if (*dead || tc::globaltimer() - t0 > a.wait_ns) {
-                *dead = 1;
-                break;
+            ++t;
+            if (last && advance(x)) {
+                t = 0;
+                ++it;
             }
         }
-    } else if (warp == P::kQuery) {
-        // ---- queries: NR rows (those past R zero), swizzled rows of 64 channels
-        int it = 0;
-        Item x = item0;
-        for (bool more = x.left > 0; more; more = advance(x)) {
-            if (it >= NQ &&
-                !__all_sync(0xffffffffu, tc::mbar_wait_or_dead(qempty(it % NQ), (it / NQ - 1) & 1, a.wait_ns, dead)))
-                break;
-            const uint32_t qb = base + P::offQ + (it % NQ) * P::kQ;
-            const int tokens = a.R >> a.qshift, qpk = 1 << a.qshift;
-            for (int e = lane; e < NR * (D / 8); e += 32) {
-                const int r = e / (D / 8), ch = e % (D / 8);
-                const bool real = r < a.R;
-                const uint16_t *src =
-                    a.q + (((size_t)x.b * tokens + (r >> a.qshift)) * a.Hq + x.h * qpk + (r & (qpk - 1))) * D + ch * 8;
-                cp_async16_zfill(qb + (ch / 8) * (NR * 128) + sw128(r, ch % 8), real ? src : a.q, real);
+    } else if (warp == P::kQuery || warp == P::kPv) {
+        if (warp == P::kQuery) {
+            // ---- queries: NR rows (those past R zero), swizzled rows of 64 channels
+            int it = 0;
+            Item x = item0;
+            for (bool more = x.left > 0; more; more = advance(x)) {
+                if (it >= NQ &&
+                    !__all_sync(0xffffffffu, tc::mbar_wait_or_dead(qempty(it % NQ), (it / NQ - 1) & 1, a.wait_ns, dead)))
+                    break;
+                const uint32_t qb = base + P::offQ + (it % NQ) * P::kQ;
+                const int tokens = a.R >> a.qshift, qpk = 1 << a.qshift;
+                for (int e = lane; e < NR * (D / 8); e += 32) {
+                    const int r = e / (D / 8), ch = e % (D / 8);
+                    const bool real = r < a.R;
+                    const uint16_t *src =
+                        a.q + (((size_t)x.b * tokens + (r >> a.qshift)) * a.Hq + x.h * qpk + (r & (qpk - 1))) * D + ch * 8;
+                    cp_async16_zfill(qb + (ch / 8) * (NR * 128) + sw128(r, ch % 8), real ? src : a.q, real);
+                }
+                cp_async_commit();
+                cp_async_wait<0>();
+                tc::fence_async_smem();
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive(qfull(it % NQ));
+                ++it;
             }
-            cp_async_commit();
-            cp_async_wait<0>();
-            tc::fence_async_smem();
-            __syncwarp();
-            if (lane == 0) tc::mbar_arrive(qfull(it % NQ));
-            ++it;
+        }
+        if (warp == P::kPv) {
+            // ---- O^T += V^T P^T
+            constexpr uint32_t id_pv = tc::idesc_bf16(D, PARTS * NR) | (1u << 15) | (1u << 16);   // both: contraction outside
+            Item x = item0;
+            int t = 0;
+            for (long long g64 = 0, total = item0.left; g64 < total; ++g64) {
+                const int g = (int)g64, sg = g % ST, w = g & 1;
+                const uint32_t vb = sStage + sg * P::kStage + KP * P::kTile;
+                bool came = tc::mbar_wait_or_dead(vfull(sg), (g / ST) & 1, a.wait_ns, dead);
+                if constexpr (!coded) {
+                    // rows behind the last token may hold anything: 0 x that has to be 0
+                    const int end = x.len - (x.tok_first + t * NT);
+                    if (end < NT && __all_sync(0xffffffffu, came)) {
+                        for (int it = lane; it < (NT - end) * (D / 8); it += 32) {
+                            const int n = end + it / (D / 8), ch = it % (D / 8);
+                            sts128(vb + (ch / 8) * P::kPanel + n * 128 + (ch % 8) * 16, make_uint4(0, 0, 0, 0));
+                        }
+                        tc::fence_async_smem();
+                        __syncwarp();
+                    }
+                }
+                came = came && tc::mbar_wait_or_dead(pfull(w), (g >> 1) & 1, a.wait_ns, dead);
+                if (!__all_sync(0xffffffffu, came)) break;
+                tc::tc_fence_after();
+                const uint32_t p_lo = tc::uniform(tc::desc_lo(base + P::offP + w * P::kP, P::kPart));
+                const uint32_t v_lo = tc::uniform(tc::desc_lo(vb, P::kPanel)), od = tc::uniform(tmem + 64 + w * 96);
+                const uint32_t more = tc::uniform(t >= 2);               // else O of this stream holds nothing of the item yet
+                if (tc::elect_one()) {
+#pragma unroll
+                    for (int k = 0; k < NT / 16; ++k)                    // 16 tokens per product
+                        tc::mma_ss(od, v_lo + k * 128, tc::desc_hi(1024, 2), p_lo + k * (2 * NR),
+                                   tc::desc_hi(8 * NR * 2, NR == 16 ? 6 : 4), id_pv, k > 0 ? 1u : more);
+                    tc::mma_commit(odone(w));
+                    if (g + ST < total) tc::mma_commit(vempty(sg));
+                }
+                __syncwarp();
+                if (++t == x.ntiles && advance(x)) t = 0;
+            }
         }
     } else if constexpr (!coded) {
         // ---- copies
@@ -821,7 +796,7 @@ __global__ void __launch_bounds__(RowsPlan<D, NR, C, PG>::kThreads, 1)
                 tc::mbar_wait_bounded(vfull(t % ST), (t / ST) & 1, tc::kDrainNs);
             }
         }
-        if (warp == P::kMma && lane == 0) {                          // products still in flight
+        if ((warp == P::kMma || warp == P::kPv) && lane == 0) {      // products still in flight
             tc::mma_commit(drain);
             tc::mbar_wait_bounded(drain, 0, tc::kDrainNs);
         }
