@@ -108,7 +108,9 @@ __global__ void __launch_bounds__(256) shared_merge_kernel(const MergeArgs a, co
         lse[dst] = total == 0.f ? -CUDART_INF_F : (top + log2f(total)) * 0.69314718055994530942f;
 }
 
-// Query rows of a KV head up to which tokens are the products' long side (shared_rows.cuh).
+// Query rows of a KV head up to which tokens are the products' long side (shared_rows.cuh).  On a bf16 cache the other
+// kernel takes 56 us where this one takes 48 (32768 tokens, 16 heads, 8 rows); on a coded cache, which is bound by the
+// rebuilding, 69 against 77, and this one serves calls of one launch.
 constexpr int kFewRows = 32, kFewRowsCoded = 16;
 
 // Splits: a CTA owns an SM (its tiles fill shared memory), so the splits that fill whole waves of 148 CTAs are
@@ -116,10 +118,15 @@ constexpr int kFewRows = 32, kFewRowsCoded = 16;
 SharedPlan plan_shared(int Hkv, int R, int max_len, bool coded) {
     SharedPlan p{};
     const int nt = coded ? 64 : 128;                                 // tokens per tile
-    p.few = R <= (coded ? kFewRowsCoded : kFewRows);
-    p.mb = R > 128 ? 2 : 1;
+    p.few = coded ? R <= kFewRowsCoded && max_len <= kDirectTiles * nt : R <= kFewRows;
+    const long tiles = (max_len + nt - 1) / nt;
+    // More than 128 rows: two blocks on a CTA share its tiles, or are CTAs of their own with twice the tiles.  A coded tile
+    // is rebuilt once for both; a bf16 tile's second read is L2's, and pays off while a CTA has few tiles (us with two
+    // blocks / one: 16347 tokens, 4 heads, 256 rows 24.1 / 23.9, 4096, 16 heads 30.6 / 28.7; 32768, 16 heads, 200 rows
+    // 93.2 / 111.7).
+    p.mb = R > 128 && (coded || tiles * Hkv * ((R + 255) / 256) >= 8 * 148) ? 2 : 1;
     p.nz = (R + p.mb * 128 - 1) / (p.mb * 128);
-    const long units = (long)Hkv * p.nz, tiles = (max_len + nt - 1) / nt;
+    const long units = (long)Hkv * p.nz;
     long best = -1;
     p.nsplit = 1;
     for (int w = 1; w <= 4; ++w) {

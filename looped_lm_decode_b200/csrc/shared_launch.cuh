@@ -70,10 +70,12 @@ inline cudaError_t launch_p(const SharedArgs &a, const SharedPlan &p, const CUte
                      const SharedOther &o, float *out, float *lse, cudaStream_t s) {
     if (p.few) {
         const RowsArgs r = rows_args(a, o, out, lse);
-        if (a.R <= 16)
+        if constexpr (C != 0)
+            return launch_rows_t<D, 16, C, PG, false, true>(r, km, vm, s);
+        else if (a.R <= 16)
             return p.direct ? launch_rows_t<D, 16, C, PG, false, true>(r, km, vm, s)
                             : launch_rows_t<D, 16, C, PG, false, false>(r, km, vm, s);
-        if constexpr (C == 0)
+        else
             return p.direct ? launch_rows_t<D, 32, C, PG, false, true>(r, km, vm, s)
                             : launch_rows_t<D, 32, C, PG, false, false>(r, km, vm, s);
     }

@@ -18,7 +18,8 @@ __device__ __forceinline__ void sts128(uint32_t addr, uint4 v) {
 
 // A slice in shared memory: each 8-bit code's entry fills a row of 64 bytes with copies of itself, one for every second
 // lane that a wavefront serves, so that two lanes at most meet in a bank, and they only for codes of equal parity (1.5
-// wavefronts where one copy takes 3; rows of 128 bytes take 1, but their memory is a third stage of tiles).
+// wavefronts where one copy takes 3; rows of 128 bytes take 1, but their memory is a fourth stage of tiles: 32768 x 32
+// queries, 8 channels per code, 71 us against 78).
 constexpr int kTableBytes = 256 * 64;
 
 struct RebuildArgs {
@@ -58,15 +59,15 @@ __device__ __forceinline__ void fill_tables(unsigned char *table, const uint16_t
 // The keys of tiles 0 .. ntiles-1 of 64 tokens from tok_first, through a ring of ST stages; rw: this warp's place among
 // the 8 that rebuild keys.  False: a wait ran out.
 //
-// A warp takes 8 tokens of the tile, a lane one token and one piece of 8 + 8 channels (8 RoPE pairs) at a time.  The 8
-// lanes of a 16-byte wavefront are tokens n and n ^ 4 by 4 pieces: their chunks of the swizzled rows lie in different
-// banks.  cos and sin turn from tile to tile by the fixed angle of 64 positions (4 flops a pair, where a row of the table
-// per token would be 512 bytes from L2); every 8th tile they are read from the table again, so that no more than 8
-// roundings add up.
+// A lane takes one piece of 8 + 8 channels (8 RoPE pairs) of a token, a warp 4 pieces of 8 tokens, and at D = 128 of the 8
+// tokens 32 further on.  The 8 lanes of a 16-byte wavefront are tokens n and n ^ 4 by 4 pieces: their chunks of the
+// swizzled rows lie in different banks.  cos and sin turn from tile to tile by the fixed angle of 64 positions (4 flops a
+// pair, where a row of the table per token would be 512 bytes from L2), whose own cosines and sines are the same for both
+// tokens and stay in registers; every 8th tile the table is read again, so that no more than 8 roundings add up.
 //
-// What bounds it is latency: a warp's visit to a tile is a chain of a wait, gathers, a rotation, stores, a fence and an
-// arrival, of about the same length for one unit of work as for two.  So values have warps of their own (below), and
-// index words come from a running pointer, two tiles ahead.
+// What bounds it is the shared-memory pipe (gathers, stores and the products' operands: 86% busy), and before that the
+// latency of a warp's visit to a tile: so values have warps of their own (below), and index words come from a running
+// pointer, two tiles ahead.  16 warps with one token a lane were no faster (76.8 us where 8 took 73.5, 32768 x 32).
 template <int C>
 __device__ __forceinline__ uint32_t entry_copy(int lane) {           // a lane's copy of an entry, in bytes
     const int pl = lane & 3;
@@ -113,99 +114,107 @@ template <int D, int C, bool PG, int ST>
 __device__ __forceinline__ bool rebuild_keys(const RebuildArgs &b, int rw, int tok_first, int ntiles, int st, int len) {
     constexpr int kTile = (D / 64) * 64 * 128;
     constexpr int NP = D / (2 * C);
-    constexpr int IT = D / 64;                                       // rounds of 4 pieces
+    constexpr int U = D / 64;                                        // tokens per lane, 32 apart
     constexpr int NW = Words<C>::n;
     constexpr int kAnchor = 8;
     const int lane = threadIdx.x & 31, pl = lane & 3, tl = ((lane >> 2) & 1) * 4 + (lane >> 3);
+    const int round = rw % U, piece = round * 4 + pl;                // low channels 8 piece .., high ones D/2 + 8 piece ..
     const unsigned char *tab = b.table + entry_copy<C>(lane);
-    const float4 *turn = reinterpret_cast<const float4 *>(b.turn) + pl * 2;
-    const int nl = rw * 8 + tl;
-    int n = tok_first + nl;                                          // this lane's token of the tile
-    const uint32_t *wp = b.idx + idx_word(n, Words<C>::first(pl), NP);
-    const uint32_t lo_at = b.stages + sw128(nl, pl);                 // of round 0; a round is 4 chunks further
-    const uint32_t swz = (uint32_t)(nl & 7) << 4;
-    auto load_words = [&](int ahead, uint32_t (&wd)[IT][NW]) {
-        const int m = n + ahead * 64;
+    const int nl = (rw / U) * 8 + tl;
+    int n = tok_first + nl;                                          // this lane's first token of the tile
+    const uint32_t *wp = b.idx + idx_word(n, Words<C>::first(pl), NP) + round * Words<C>::round;
+    const uint32_t lo_at = b.stages + sw128(nl, piece);
+    const uint32_t hi_at = D == 128 ? lo_at + 64 * 128 : b.stages + sw128(nl, piece + 4);
+    auto load_words = [&](int ahead, uint32_t (&wd)[U][NW]) {
 #pragma unroll
-        for (int it = 0; it < IT; ++it)
+        for (int u = 0; u < U; ++u) {
+            const int m = n + ahead * 64 + u * 32;
 #pragma unroll
             for (int k = 0; k < NW; ++k)
-                wd[it][k] = m >= st && m < len ? __ldg(wp + ahead * 64 * NP + it * Words<C>::round + k * 4) : 0u;
+                wd[u][k] = m >= st && m < len ? __ldg(wp + (ahead * 64 + u * 32) * NP + k * 4) : 0u;
+        }
     };
-    uint32_t wd[IT][NW], nx[IT][NW];
+    uint32_t wd[U][NW], nx[U][NW];
     load_words(0, wd);
     load_words(1, nx);
-    float2 cs[IT][4], sn[IT][4];                                     // of this lane's token and channels
+    float2 cs[U][4] = {}, sn[U][4] = {};                             // of this lane's tokens and channels
+    float2 tc64[4], ts64[4];                                         // of the turn by 64 positions
+    {
+        const float4 *turn = reinterpret_cast<const float4 *>(b.turn) + piece * 2;
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const float4 c = turn[k], x = turn[D / 8 + k];
+            tc64[2 * k] = f2(c.x, c.y);
+            tc64[2 * k + 1] = f2(c.z, c.w);
+            ts64[2 * k] = f2(x.x, x.y);
+            ts64[2 * k + 1] = f2(x.z, x.w);
+        }
+    }
     int s = 0;
     uint32_t par = 1;                                                // an empty ring counts as read
     for (int t = 0; t < ntiles; ++t) {
-        const bool in = n >= st && n < len;
-        uint32_t n2[IT][NW];
+        uint32_t n2[U][NW];
         load_words(2, n2);                                           // two tiles ahead: a tile is shorter than a load
         if (t % kAnchor == 0) {
-            const float4 *row = reinterpret_cast<const float4 *>(b.rope + (size_t)(n < len ? n : st) * D) + pl * 2;
 #pragma unroll
-            for (int it = 0; it < IT; ++it)
+            for (int u = 0; u < U; ++u) {
+                const int m = n + u * 32;
+                const float4 *row = reinterpret_cast<const float4 *>(b.rope + (size_t)(m < len ? m : st) * D) + piece * 2;
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
-                    const float4 c = __ldg(row + it * 8 + k), x = __ldg(row + D / 8 + it * 8 + k);
-                    cs[it][2 * k] = f2(c.x, c.y);
-                    cs[it][2 * k + 1] = f2(c.z, c.w);
-                    sn[it][2 * k] = f2(x.x, x.y);
-                    sn[it][2 * k + 1] = f2(x.z, x.w);
+                    const float4 c = __ldg(row + k), x = __ldg(row + D / 8 + k);
+                    cs[u][2 * k] = f2(c.x, c.y);
+                    cs[u][2 * k + 1] = f2(c.z, c.w);
+                    sn[u][2 * k] = f2(x.x, x.y);
+                    sn[u][2 * k + 1] = f2(x.z, x.w);
                 }
+            }
         }
-        uint4 k0[IT], k1[IT];
+        uint4 k0[U], k1[U];
 #pragma unroll
-        for (int it = 0; it < IT; ++it) {
-            const uint4 z = make_uint4(0, 0, 0, 0);
-            const int piece = it * 4 + pl;
-            k0[it] = in ? gather_piece<D, C, PG>(b, tab, b.slk, 0, 0, piece, wd[it][0], wd[it][NW - 1]) : z;
-            k1[it] = in ? gather_piece<D, C, PG>(b, tab, b.slk, 8, 1, piece, wd[it][0], wd[it][NW - 1]) : z;
+        for (int u = 0; u < U; ++u) {
+            const int m = n + u * 32;
+            k0[u] = k1[u] = make_uint4(0, 0, 0, 0);
+            if (m >= st && m < len) {
+                k0[u] = gather_piece<D, C, PG>(b, tab, b.slk, 0, 0, piece, wd[u][0], wd[u][NW - 1]);
+                k1[u] = gather_piece<D, C, PG>(b, tab, b.slk, 8, 1, piece, wd[u][0], wd[u][NW - 1]);
+            }
         }
         if (!__all_sync(0xffffffffu, tc::mbar_wait_or_dead(b.kempty + 8u * s, par, b.wait_ns, b.dead))) return false;
         const uint32_t off = (uint32_t)s * (3 * kTile);
 #pragma unroll
-        for (int it = 0; it < IT; ++it) {
-            const uint32_t kl[4] = {k0[it].x, k0[it].y, k0[it].z, k0[it].w};
-            const uint32_t kh[4] = {k1[it].x, k1[it].y, k1[it].z, k1[it].w};
+        for (int u = 0; u < U; ++u) {
+            const uint32_t kl[4] = {k0[u].x, k0[u].y, k0[u].z, k0[u].w};
+            const uint32_t kh[4] = {k1[u].x, k1[u].y, k1[u].z, k1[u].w};
             uint32_t ah[4], al[4], bh[4], bl[4];                     // rotated: bf16 parts of the low and high channels
             const float2 minus = f2(-1.f, -1.f);
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
                 const float2 x = unpack2(kl[k]), y = unpack2(kh[k]), ny = unpack2(kh[k] ^ 0x80008000u);
-                const float2 ra = __ffma2_rn(x, cs[it][k], __fmul2_rn(ny, sn[it][k]));
-                const float2 rb = __ffma2_rn(y, cs[it][k], __fmul2_rn(x, sn[it][k]));
+                const float2 ra = __ffma2_rn(x, cs[u][k], __fmul2_rn(ny, sn[u][k]));
+                const float2 rb = __ffma2_rn(y, cs[u][k], __fmul2_rn(x, sn[u][k]));
                 ah[k] = cvt_bf16x2(ra.y, ra.x);
                 bh[k] = cvt_bf16x2(rb.y, rb.x);
                 const float2 da = __ffma2_rn(unpack2(ah[k]), minus, ra), db = __ffma2_rn(unpack2(bh[k]), minus, rb);
                 al[k] = cvt_bf16x2(da.y, da.x);
                 bl[k] = cvt_bf16x2(db.y, db.x);
             }
-            // low channels 8 piece .., high channels D/2 + 8 piece ..
-            const uint32_t lo = off + (it == 0 ? lo_at : b.stages + (uint32_t)nl * 128u + (((pl + 4u) << 4) ^ swz));
-            const uint32_t hi = D == 128 ? lo + 64 * 128 : off + b.stages + (uint32_t)nl * 128u + (((pl + 4u) << 4) ^ swz);
-            sts128(lo, make_uint4(ah[0], ah[1], ah[2], ah[3]));
-            sts128(hi, make_uint4(bh[0], bh[1], bh[2], bh[3]));
-            sts128(lo + kTile, make_uint4(al[0], al[1], al[2], al[3]));
-            sts128(hi + kTile, make_uint4(bl[0], bl[1], bl[2], bl[3]));
+            const uint32_t at = off + u * (32 * 128);                // 32 rows further: the same swizzle
+            sts128(lo_at + at, make_uint4(ah[0], ah[1], ah[2], ah[3]));
+            sts128(hi_at + at, make_uint4(bh[0], bh[1], bh[2], bh[3]));
+            sts128(lo_at + at + kTile, make_uint4(al[0], al[1], al[2], al[3]));
+            sts128(hi_at + at + kTile, make_uint4(bl[0], bl[1], bl[2], bl[3]));
         }
         tc::fence_async_smem();
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(b.kfull + 8u * s);
 #pragma unroll
-        for (int it = 0; it < IT; ++it)
+        for (int u = 0; u < U; ++u)
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                const float4 c64 = turn[it * 8 + k], s64 = turn[D / 8 + it * 8 + k];
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    const float2 c = cs[it][2 * k + j], x = sn[it][2 * k + j];
-                    const float2 tc2 = j ? f2(c64.z, c64.w) : f2(c64.x, c64.y);
-                    const float2 ts2 = j ? f2(s64.z, s64.w) : f2(s64.x, s64.y);
-                    cs[it][2 * k + j] = __ffma2_rn(c, tc2, __fmul2_rn(neg2(x), ts2));
-                    sn[it][2 * k + j] = __ffma2_rn(x, tc2, __fmul2_rn(c, ts2));
-                }
+            for (int k = 0; k < 4; ++k) {
+                const float2 c = cs[u][k], x = sn[u][k];
+                cs[u][k] = __ffma2_rn(c, tc64[k], __fmul2_rn(neg2(x), ts64[k]));
+                sn[u][k] = __ffma2_rn(x, tc64[k], __fmul2_rn(c, ts64[k]));
             }
         n += 64;
         wp += 64 * NP;
@@ -214,11 +223,11 @@ __device__ __forceinline__ bool rebuild_keys(const RebuildArgs &b, int rw, int t
             par ^= 1;
         }
 #pragma unroll
-        for (int it = 0; it < IT; ++it)
+        for (int u = 0; u < U; ++u)
 #pragma unroll
             for (int k = 0; k < NW; ++k) {
-                wd[it][k] = nx[it][k];
-                nx[it][k] = n2[it][k];
+                wd[u][k] = nx[u][k];
+                nx[u][k] = n2[u][k];
             }
     }
     return true;
