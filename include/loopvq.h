@@ -245,8 +245,9 @@ size_t loopvq_shared_workspace_bytes(const loopvq_cache *cache, int rows, int ma
  * max_len    host upper bound of len, 0 <= max_len <= Nmax.
  * scale      <= 0 selects 1/sqrt(D).
  * other_out  fp32 [rows][Hq][D] and other_lse fp32 [rows][Hq]: the other part,
- *            or both NULL; a row with other_lse = -inf has no other tokens.  out
- *            may be other_out; lse may not overlap other_lse.
+ *            or both NULL; a row with other_lse = -inf has no other tokens, and one
+ *            with NaN (of a call that gave up waiting) becomes NaN.  out may be
+ *            other_out; lse may not overlap other_lse.
  * out        fp32 [rows][Hq][D]; lse fp32 [rows][Hq], may be NULL.  No tokens at
  *            all: zeros and -inf.
  * workspace  of at least loopvq_bf16_shared_workspace_bytes(cache, rows, max_len)
@@ -298,6 +299,9 @@ size_t loopvq_bf16_scored_workspace_bytes(const loopvq_bf16_cache *cache, int ma
  * The other arguments are those of loopvq_bf16_decode_attn; workspace of at
  * least loopvq_bf16_scored_workspace_bytes(cache, max_len) bytes, ordered like
  * any workspace.  Sums run in a fixed order: equal inputs give equal bits.
+ * Grouped heads and short calls run on the tensor cores: waits, faults and the
+ * first call on a device as in loopvq_bf16_shared_attn (scores of a KV head whose
+ * wait ran out are undefined).
  */
 loopvq_status loopvq_bf16_decode_attn_scored(const loopvq_bf16_cache *cache, const uint16_t *q,
                                              const int32_t *starts, const int32_t *lens, int max_len, float scale,
@@ -540,8 +544,9 @@ const char *loopvq_last_error(void);
  *     releases its tensor memory, writes 0xFF code bytes for the tokens it
  *     had not finished and sets the fault;
  *   - the shared-prefix attention (loopvq_bf16_shared_attn, loopvq_shared_attn)
- *     bounds each wait for its own copies and products in the same way; a
- *     thread block whose wait runs out makes the rows it worked on NaN;
+ *     and loopvq_bf16_decode_attn_scored bound each wait for their own copies
+ *     and products in the same way; a thread block whose wait runs out makes
+ *     the rows it worked on NaN;
  *   - loopvq_window_advance does not roll a sequence whose coded cache has no
  *     room for the page (coded_end + 8 > Nmax) and sets the fault; that
  *     sequence's window stays full, so its next append overwrites the newest

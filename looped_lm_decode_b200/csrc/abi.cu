@@ -288,6 +288,9 @@ static loopvq_status check_other(const float *other_out, const float *other_lse)
     return check_word_ptr(other_lse, "other_lse");
 }
 
+// Query rows of a KV head that a grid can hold, in blocks of 128.
+static bool rows_fit(int rows, int qpk) { return (int64_t)rows * qpk <= 65535LL * 128; }
+
 // Arguments that the two shared-prefix calls have in common; sets the default scale.
 static loopvq_status check_shared(int B, int Hkv, int Hq, int D, int Nmax, int seq, const uint16_t *q, int rows,
                                   const int32_t *starts, const int32_t *lens, int max_len, float *scale,
@@ -305,7 +308,7 @@ static loopvq_status check_shared(int B, int Hkv, int Hq, int D, int Nmax, int s
         return fail(LOOPVQ_ERR_INVALID_ARG, "max_len=%d out of [0, Nmax=%d]", max_len, Nmax);
     if (!std::isfinite(*scale)) return fail(LOOPVQ_ERR_INVALID_ARG, "scale is not finite");
     if (*scale <= 0.f) *scale = 1.0f / std::sqrt((float)D);
-    if (Hkv > 65535 || (int64_t)rows * (Hq / Hkv) > 65535LL * 128)
+    if (Hkv > 65535 || !rows_fit(rows, Hq / Hkv))
         return fail(LOOPVQ_ERR_UNSUPPORTED, "Hkv=%d or rows * Hq / Hkv = %lld too large", Hkv,
                     (long long)rows * (Hq / Hkv));
     const size_t n = (size_t)rows * Hq;
@@ -326,12 +329,14 @@ static loopvq_status check_ws(const void *workspace, size_t given, size_t need) 
 }
 
 size_t loopvq_bf16_shared_workspace_bytes(const loopvq_bf16_cache *c, int rows, int max_len) {
-    if (check_bf16(c) != LOOPVQ_OK || rows < 0 || max_len < 0 || max_len > c->Nmax) return 0;
+    if (check_bf16(c) != LOOPVQ_OK || rows < 0 || max_len < 0 || max_len > c->Nmax || !rows_fit(rows, c->Hq / c->Hkv))
+        return 0;
     return loopvq::shared_ws_bytes(c->Hkv, c->Hq, c->D, rows, max_len, false);
 }
 
 size_t loopvq_shared_workspace_bytes(const loopvq_cache *cc, int rows, int max_len) {
-    if (check_shape(cc) != LOOPVQ_OK || rows < 0 || max_len < 0 || max_len > cc->Nmax) return 0;
+    if (check_shape(cc) != LOOPVQ_OK || rows < 0 || max_len < 0 || max_len > cc->Nmax || !rows_fit(rows, cc->Hq / cc->Hkv))
+        return 0;
     return loopvq::shared_ws_bytes(cc->Hkv, cc->Hq, cc->D, rows, max_len, true);
 }
 

@@ -1,6 +1,6 @@
 // Device-side fault reporting: a word per GPU that kernels set when they cannot do their job (a bounded
-// wait of the tensor-core encoder or of the shared-prefix attention ran out, or a window roll found the coded
-// cache full), and the entry
+// wait of the tensor-core encoder or of the shared-prefix or scored attention ran out, or a window roll found
+// the coded cache full), and the entry
 // points that bound those waits and read the word back.  Calls stay asynchronous; only
 // loopvq_fault_check synchronises.
 #include <atomic>
@@ -69,7 +69,7 @@ loopvq_status loopvq_fault_check(void *stream) {
                  "a tensor-core encode gave up waiting for its own contraction (wait limit %llu ns); the codes that "
                  "encode call wrote are undefined%s%s",
                  (unsigned long long)loopvq::wait_limit_ns(),
-                 (bits & loopvq::kFaultAttnWait) ? "; also a shared-prefix attention gave up waiting (NaN rows)" : "",
+                 (bits & loopvq::kFaultAttnWait) ? "; also an attention on the tensor cores gave up waiting (NaN rows)" : "",
                  (bits & loopvq::kFaultWindowFull) ? "; also a window roll found the coded cache full" : "");
         loopvq::set_last_error(msg);
         return LOOPVQ_ERR_TIMEOUT;
@@ -77,7 +77,7 @@ loopvq_status loopvq_fault_check(void *stream) {
     if (bits & loopvq::kFaultAttnWait) {
         char msg[256];
         snprintf(msg, sizeof(msg),
-                 "a shared-prefix attention gave up waiting for its own copies or products (wait limit %llu ns); rows of "
+                 "a shared-prefix or scored attention gave up waiting for its own copies or products (wait limit %llu ns); rows of "
                  "its out and lse are NaN%s",
                  (unsigned long long)loopvq::wait_limit_ns(),
                  (bits & loopvq::kFaultWindowFull) ? "; also a window roll found the coded cache full" : "");

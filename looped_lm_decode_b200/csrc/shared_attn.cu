@@ -93,7 +93,7 @@ __global__ void __launch_bounds__(256) shared_merge_kernel(const MergeArgs a, co
             acc.w += w * y.w;
         }
         const float wo = ex2(ol - top);
-        if (wo > 0.f) {
+        if (wo != 0.f) {
             const float4 y = *reinterpret_cast<const float4 *>(other_out + dst * D + c4 * 4);
             total += wo;
             acc.x += wo * y.x;
@@ -102,6 +102,7 @@ __global__ void __launch_bounds__(256) shared_merge_kernel(const MergeArgs a, co
             acc.w += wo * y.w;
         }
     }
+    if (ol != ol) total = ol;                                        // passed over by fmaxf above
     const float inv = total != 0.f ? 1.f / total : 0.f;              // no tokens at all: zeros
     *reinterpret_cast<float4 *>(out + dst * D + c4 * 4) = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
     if (lse != nullptr && c4 == 0)

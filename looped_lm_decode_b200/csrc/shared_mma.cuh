@@ -385,7 +385,8 @@ __global__ void __launch_bounds__(Plan<D, MB, C, PG>::kThreads, 1)
             asm volatile("bar.sync 1, 256;" ::: "memory");
         }
         if (any && (MB == 2 || w == 0)) {
-            if (rq < a.R) a.ws_ml[rec + rq] = ok ? f2(sm.m, sm.l) : f2(0.f, CUDART_NAN_F);
+            // (a maximum passes NaN over: a row of nothing but NaN must not look like one without tokens)
+            if (rq < a.R) a.ws_ml[rec + rq] = ok && sm.l == sm.l ? f2(sm.m, sm.l) : f2(0.f, CUDART_NAN_F);
 #pragma unroll 1
             for (int c = 0; c < D; c += 32) {
                 uint32_t o[32];
@@ -532,7 +533,7 @@ __global__ void __launch_bounds__(Plan<D, MB, C, PG>::kThreads, 1)
                 tc::mbar_wait_bounded(kfull(t % ST), (t / ST) & 1, tc::kDrainNs);
                 tc::mbar_wait_bounded(vfull(t % ST), (t / ST) & 1, tc::kDrainNs);
             }
-        if (warp == P::kMma && lane == 0) {                          // products still in flight
+        if (warp == P::kMma && tc::elect_one()) {                    // products still in flight, of the thread that issued them
             tc::mma_commit(drain);
             tc::mbar_wait_bounded(drain, 0, tc::kDrainNs);
         }

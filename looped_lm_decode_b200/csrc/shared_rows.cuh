@@ -210,11 +210,14 @@ __global__ void __launch_bounds__(RowsPlan<D, NR, C, PG>::kThreads, 1)
             asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         }
         __syncwarp();
+    }
+    grid_wait();
+    if (warp == P::kMma) {                                           // behind the wait: a CTA that waits holds no tensor
+                                                                     // memory that the kernel before could want
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(tc::smem_u32(tmem_slot)),
                      "r"(P::kCols));
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
     }
-    grid_wait();
     if constexpr (coded) {                                           // an item's KV head is this CTA's: one item per CTA
         if constexpr (!PG) {
             const int h = DIRECT ? blockIdx.x % a.Hkv : blockIdx.x / a.nsplit;
@@ -562,7 +565,7 @@ __global__ void __launch_bounds__(RowsPlan<D, NR, C, PG>::kThreads, 1)
                         c1 /= total;
                         co /= total;
                     }
-                    if (s0 + s1 != s0 + s1) c0 = c1 = co = l2 = CUDART_NAN_F;   // a stream gave up
+                    if (s0 + s1 != s0 + s1 || ol != ol) c0 = c1 = co = l2 = CUDART_NAN_F;   // a stream gave up, or NaN inputs
                     coef[r] = c0;
                     coef[NR + r] = c1;
                     coef[2 * NR + r] = co;
@@ -796,7 +799,7 @@ __global__ void __launch_bounds__(RowsPlan<D, NR, C, PG>::kThreads, 1)
                 tc::mbar_wait_bounded(vfull(t % ST), (t / ST) & 1, tc::kDrainNs);
             }
         }
-        if ((warp == P::kMma || warp == P::kPv) && lane == 0) {      // products still in flight
+        if ((warp == P::kMma || warp == P::kPv) && tc::elect_one()) {   // products still in flight, of the threads that issued them
             tc::mma_commit(drain);
             tc::mbar_wait_bounded(drain, 0, tc::kDrainNs);
         }

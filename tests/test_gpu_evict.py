@@ -141,6 +141,28 @@ def test_scored_decode_of_ragged_batches(b, hkv, hq, n):
         assert all(torch.equal(x, y) for x, y in zip(got, again))
 
 
+@pytest.mark.parametrize("hq,n", [(2, 300), (8, 300), (2, 1500), (8, 1500)])
+def test_scored_decode_does_not_lose_nan(hq, n):
+    """A query or another part of NaN makes its row and its KV head's scores NaN and changes nothing else."""
+    cache, q, g = make(3, 2, hq, n, 64, seed=12)
+    lens = torch.tensor([n, n - 7, 0], dtype=torch.int32, device="cuda")
+    other = torch.randn(3, hq, 64, generator=g, device="cuda"), torch.randn(3, hq, generator=g, device="cuda")
+    bad_q, bad_o = q.clone(), (other[0], other[1].clone())
+    bad_q[1, 0, 7] = math.nan
+    bad_o[1][0, hq - 1], bad_o[1][2, 0] = math.nan, math.nan
+    call = lambda x, o: LQ.bf16_decode_attn_scored(cache, x, lens, n, None, other=o,  # noqa: E731
+                                                   score_out=torch.zeros(3, 2, n, device="cuda"))
+    for x, o, rows, heads in ((bad_q, None, [(1, 0)], [(1, 0)]), (q, bad_o, [(0, hq - 1), (2, 0)], [(0, 1)])):
+        good, bad = call(q, None if o is None else other), call(x, o)
+        row, head = torch.zeros(3, hq, dtype=torch.bool, device="cuda"), torch.zeros(3, 2, n, dtype=torch.bool, device="cuda")
+        for at in rows:
+            row[at] = True
+        for b, h in heads:
+            head[b, h, :int(lens[b])] = True
+        assert bad[0][row].isnan().all() and bad[1][row].isnan().all() and bad[2][head].isnan().all()
+        assert all(torch.equal(u[~m], w[~m]) for u, w, m in zip(good, bad, (row, row, head)))
+
+
 def test_scored_decode_with_far_scores():
     """Scores that leave the first tokens' reference by more than the exponent's range."""
     for n in (600, 3000):
@@ -351,3 +373,47 @@ def test_captured_and_on_another_stream():
                                        workspace=w1, out=torch.empty_like(out), lse=torch.empty_like(lse))
     side.synchronize()
     assert again[0].isfinite().all()
+
+
+@pytest.mark.parametrize("hq,n,budget", [(2, 500, 490), (8, 2100, 300)])
+def test_two_sequences_of_calls_at_once(hq, n, budget):
+    """Decode and eviction of two caches on two streams, each with workspaces of its own, give what they give alone."""
+    sets, alone = [], []
+    for seed in (20, 21):
+        cache, q, g = make(2, 2, hq, n, 128, seed=seed)
+        lens = torch.tensor([n, n - 30], dtype=torch.int32, device="cuda")
+        pos = torch.arange(n, device="cuda", dtype=torch.int32).expand(2, 2, n).contiguous()
+        score = torch.rand(2, 2, n, generator=g, device="cuda")
+        sets.append((cache, q, lens, score, pos))
+
+    def steps(cache, q, lens, score, pos, stream):
+        out = torch.empty(2, hq, 128, device="cuda"), torch.empty(2, hq, device="cuda")
+        ws = [torch.empty(s, dtype=torch.uint8, device="cuda") for s in
+              (LQ.bf16_scored_workspace_bytes(cache, n), LQ.bf16_evict_workspace_bytes(cache, n, budget))]
+        nxt = torch.full((2,), n, dtype=torch.int32, device="cuda")
+        yield
+        for _ in range(6):
+            LQ.bf16_decode_attn_scored(cache, q, lens, n, score, score_out=score, out=out[0], lse=out[1], workspace=ws[0],
+                                       stream=stream)
+            LQ.bf16_evict(cache, score, pos, lens, nxt, n, budget, n_sink=4, n_recent=16, score_out=score, pos_out=pos,
+                          lens_out=lens, workspace=ws[1], stream=stream)
+            yield
+        yield out + (lens, score[..., :budget], pos[..., :budget], cache.k[:, :, :budget], cache.v[:, :, :budget])
+
+    def copy(cache, *rest):
+        return (LQ.Bf16Cache(cache.k.clone(), cache.v.clone(), hq),) + tuple(x.clone() for x in rest)
+
+    for x in sets:
+        alone.append(list(steps(*copy(*x), None))[-1])
+    streams = [torch.cuda.Stream() for _ in sets]
+    runs = [steps(*copy(*x), s) for x, s in zip(sets, streams)]
+    for r in runs:
+        next(r)
+    torch.cuda.synchronize()
+    for _ in range(6):
+        for r in runs:
+            next(r)
+    torch.cuda.synchronize()
+    for r, want in zip(runs, alone):
+        assert all(torch.equal(x, y) for x, y in zip(next(r), want))
+    LQ.fault_check()

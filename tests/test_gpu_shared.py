@@ -156,6 +156,29 @@ def test_bf16_masked_values_are_not_seen(rows):
     assert torch.equal(clean[0], dirty[0]) and torch.equal(clean[1], dirty[1])
 
 
+@pytest.mark.parametrize("rows", [5, 25, 100, 300])
+@pytest.mark.parametrize("n", [300, 3000])
+def test_nan_stays_in_its_row_and_is_not_lost(rows, n):
+    """A query or another part of NaN makes its row NaN, with tokens or without, and no other row differs."""
+    g = gen(11)
+    cache = LQ.Bf16Cache(bf16(g, 2, 2, n, 128), bf16(g, 2, 2, n, 128), 2)
+    coded = make_coded(g, 2, 2, 128, 4, 4, 1, 256, 2, n)
+    q, lens = bf16(g, rows, 2, 128), i32([n, 0])
+    other = make_other(g, rows, 2, 128)
+    bad_q, bad_o = q.clone(), (other[0], other[1].clone())
+    bad_q[3, 1, 5] = math.nan
+    bad_o[1][2, 0] = math.nan
+    hit = torch.zeros(rows, 2, dtype=torch.bool, device="cuda")
+    for call in (lambda x, o, s: LQ.bf16_shared_attn(cache, s, x, lens, n, other=o),
+                 lambda x, o, s: LQ.shared_attn(coded, 0, 1, s, x, lens, n, other=o)):
+        for x, o, s, at in ((bad_q, None, 0, (3, 1)), (q, bad_o, 0, (2, 0)), (q, bad_o, 1, (2, 0))):
+            good, bad = call(q, None if o is None else other, s), call(x, o, s)
+            hit[:] = False
+            hit[at] = True
+            assert bad[0][hit].isnan().all() and bad[1][hit].isnan().all()
+            assert torch.equal(good[0][~hit], bad[0][~hit]) and torch.equal(good[1][~hit], bad[1][~hit])
+
+
 # ------------------------------------------------------------------ coded
 
 def make_coded(g, hkv, hq, d, c, tc, ncb, entries, seqs, nmax, loops=4):

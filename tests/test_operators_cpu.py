@@ -139,6 +139,8 @@ def test_workspace_sizes():
     # more rows and longer prefixes never need less
     sizes = [L.loopvq_bf16_shared_workspace_bytes(C.byref(big), r, 32768) for r in (1, 4, 16, 33, 64, 65, 300)]
     assert all(s > 0 for s in sizes)
+    assert L.loopvq_bf16_shared_workspace_bytes(C.byref(big), 2 ** 31 - 1, 32768) == 0   # more rows than a call takes
+    assert shared(big, rows=2 ** 31 - 1, max_len=32768) == UNSUPPORTED
     # a batch's scores alone: 4 bytes a token and query head
     assert L.loopvq_bf16_scored_workspace_bytes(C.byref(desc(B=64, Hkv=4, Hq=16)), 4096) >= 64 * 16 * 4096 * 4
 
