@@ -12,11 +12,16 @@
 //
 // Selection: scores map to unsigned keys in their own order (radix order of the fp32 bits, NaN lowest, protected
 // tokens highest), a key and its slot to one 64-bit rank (ties: the lower slot first), and one CTA per (sequence, KV
-// head), or a cluster, finds the budget-th largest rank: a histogram of the keys' top 11 bits names the bin that holds it, and the
-// few keys of that bin are ranked against one another; only if they are many (equal scores) do further digits follow,
-// and then the slots' order.  Histograms are integer counts in shared memory and ranks are distinct, so the atomics'
-// order does not matter.  Keys are read once and stay in registers; a
-// long row is shared out over a cluster of up to 8 CTAs, which read one another's counts and lists.
+// head), or a cluster, finds the budget-th largest rank: a histogram of the keys' top 11 bits names the bin that holds
+// it, and the few keys of that bin are ranked against one another; only if they are many (equal scores) do further
+// digits follow, and then the slots' order.  Histograms are integer counts in shared memory and ranks are distinct, so
+// the atomics' order does not matter.  Keys are read once and stay in registers; a long row is shared out over a cluster
+// of up to 8 CTAs, which send one another their counts and lists.
+//
+// What bounds it: a step's eviction (32 sequences x 16 heads, 2049 slots to 2048: 8.9 us, 17 MB read and written) is a
+// chain of latencies, 12000 clocks: loads 3500, histogram 1000, digit 1000, list 2500, marks 2800 (clocks that
+// several CTAs of an SM share).  A long one (2 x 16 heads, 32768 slots to 4096: 41 us) selects in 20 us, of which the
+// cluster's slowest loads are half (its CTAs wait for one another), and reads and writes 117 MB of rows of 256 bytes in 20.
 #include "loopvq_internal.cuh"
 
 namespace loopvq {
@@ -179,6 +184,7 @@ __global__ void __launch_bounds__(NT, NT == 256 ? 4 : 2) evict_select_kernel(con
     constexpr int NW = NT / 32;
     constexpr bool FUSED = FUSED_D > 0;
     static_assert(CL == 1 || !FUSED, "clusters of a row, or of a sequence's heads");
+    static_assert(1024 % NT == 0, "runs of bins");
     __shared__ __align__(16) int hist[kBins];
     __shared__ int slots[NW];
     __shared__ int s_digit, s_above, s_count;
@@ -240,12 +246,18 @@ __global__ void __launch_bounds__(NT, NT == 256 ? 4 : 2) evict_select_kernel(con
             cluster_sync();
         }
         // the digit whose suffix count reaches `need`: every thread sums a run of bins, from the highest down
-        const int per = bins / NT > 0 ? bins / NT : 1;
+        const int per = bins / NT;
         int mine = 0;
         const int hi = bins - 1 - tid * per;                         // this thread's highest bin
-#pragma unroll 8
-        for (int i = 0; i < per; ++i)
-            if (hi - i >= 0) mine += bins_all[hi - i];
+        if (per % 4 == 0) {                                          // wide: single words of runs meet in few banks
+            const int4 *run = reinterpret_cast<const int4 *>(bins_all + hi + 1 - per);
+            for (int i = 0; i < per / 4; ++i) {
+                const int4 c = run[i];
+                mine += c.x + c.y + c.z + c.w;
+            }
+        } else {
+            for (int i = 0; i < per; ++i) mine += bins_all[hi - i];
+        }
         int inc = mine;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -329,7 +341,8 @@ __global__ void __launch_bounds__(NT, NT == 256 ? 4 : 2) evict_select_kernel(con
             } else {
                 // a key's place: larger ones and, before it, equal ones.  `parts` neighbouring threads share its comparisons
                 const int own2 = last - first;
-                const int parts = own2 * 4 <= NT ? 4 : own2 * 2 <= NT ? 2 : 1;
+                int parts = 1;
+                while (parts < 32 && own2 * parts * 2 <= NT) parts *= 2;
                 const int quads = (count + 3) / 4;
                 for (int i0 = first; i0 < last; i0 += NT / parts) {
                     const int i = i0 + tid / parts, share = tid % parts;
@@ -456,9 +469,11 @@ __global__ void __launch_bounds__(NT, NT == 256 ? 4 : 2) evict_select_kernel(con
 }
 
 // Rows of the moved tokens, their scores and positions; and the new lengths (the selection reads the old ones,
-// which may be the same memory).  D / 8 lanes move a 16-byte piece each of a key row and a value row.
+// which may be the same memory).  D / 8 lanes move a 16-byte piece each of a key row and a value row; everything that a
+// thread moves is loaded before its first store (one row after the other, its score behind its key: 44 us where this
+// takes 41, 32768 slots to 4096).
 constexpr int kMoveThreads = 256;
-constexpr int kMoveRows = 64;                                        // per CTA
+constexpr int kMoveRows = 32;                                        // per CTA
 
 template <int D>
 __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictArgs a) {
@@ -472,16 +487,31 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictArg
     const int32_t *holes = a.ws + (size_t)a.B * a.Hkv + (size_t)bh * 2 * a.cap, *sources = holes + a.cap;
     const size_t row = (size_t)bh * a.Nmax;
     const int lane = threadIdx.x % NL;
-    const int end = min(moved, (int)(blockIdx.x + 1) * kMoveRows);
-#pragma unroll 2
-    for (int i = blockIdx.x * kMoveRows + threadIdx.x / NL; i < end; i += PER) {
-        const size_t to = row + holes[i], from = row + sources[i];
-        const uint4 kw = *reinterpret_cast<const uint4 *>(a.k + from * D + lane * 8);
-        const uint4 vw = *reinterpret_cast<const uint4 *>(a.v + from * D + lane * 8);
-        *reinterpret_cast<uint4 *>(a.k + to * D + lane * 8) = kw;
-        *reinterpret_cast<uint4 *>(a.v + to * D + lane * 8) = vw;
-        if (lane == 0) a.score_out[to] = a.score_in[from];
-        if (lane == 1) a.pos_out[to] = a.pos_in[from];
+    constexpr int IT = kMoveRows / PER;
+    const int i0 = blockIdx.x * kMoveRows + threadIdx.x / NL;
+    if (i0 >= moved) return;
+    size_t to[IT], from[IT];
+    uint4 kw[IT], vw[IT];
+    int x[IT];
+#pragma unroll
+    for (int j = 0; j < IT; ++j) {                                   // rows past the last: the first again, not written
+        const int i = i0 + j * PER < moved ? i0 + j * PER : i0;
+        to[j] = row + holes[i];
+        from[j] = row + sources[i];
+    }
+#pragma unroll
+    for (int j = 0; j < IT; ++j) {
+        kw[j] = *reinterpret_cast<const uint4 *>(a.k + from[j] * D + lane * 8);
+        vw[j] = *reinterpret_cast<const uint4 *>(a.v + from[j] * D + lane * 8);
+        x[j] = lane == 0 ? __float_as_int(a.score_in[from[j]]) : lane == 1 ? a.pos_in[from[j]] : 0;
+    }
+#pragma unroll
+    for (int j = 0; j < IT; ++j) {
+        if (i0 + j * PER >= moved) break;
+        *reinterpret_cast<uint4 *>(a.k + to[j] * D + lane * 8) = kw[j];
+        *reinterpret_cast<uint4 *>(a.v + to[j] * D + lane * 8) = vw[j];
+        if (lane == 0) a.score_out[to[j]] = __int_as_float(x[j]);
+        if (lane == 1) a.pos_out[to[j]] = x[j];
     }
 }
 
