@@ -518,9 +518,9 @@ __global__ void __launch_bounds__(Plan<D, MB, C, PG>::kThreads, 1)
         b.dead = dead;
         if (warp < P::kRebuild + 8) {
             asm volatile("setmaxnreg.inc.sync.aligned.u32 112;");
-            rebuild_keys<D, C, PG, ST>(b, warp - P::kRebuild, tok_first, ntiles, st, len);
+            rebuild_keys<D, C, PG, ST, KP>(b, warp - P::kRebuild, tok_first, ntiles, st, len);
         } else if (warp < P::kValues + 2) {
-            rebuild_values<D, C, PG, ST>(b, warp - P::kValues, tok_first, ntiles, st, len);
+            rebuild_values<D, C, PG, ST, KP>(b, warp - P::kValues, tok_first, ntiles, st, len);
         }
     }
 

@@ -28,7 +28,7 @@ struct RebuildArgs {
     const float *rope;
     const unsigned char *table;      // both slices in shared memory (not with one codebook per channel group)
     const unsigned char *turn;       // rope row 64 in shared memory
-    uint32_t stages;                 // shared address of the stages: K upper part, K lower part, V
+    uint32_t stages;                 // shared address of the stages: KP bf16 parts of K from the upper one on, V
     uint32_t kfull, vfull, kempty, vempty;   // first barriers of the stages
     int K;
     uint64_t wait_ns;
@@ -57,7 +57,7 @@ __device__ __forceinline__ void fill_tables(unsigned char *table, const uint16_t
 }
 
 // The keys of tiles 0 .. ntiles-1 of 64 tokens from tok_first, through a ring of ST stages; rw: this warp's place among
-// the 8 that rebuild keys.  False: a wait ran out.
+// the 8 that rebuild keys; KP: bf16 parts of a key (2 leave 2^-17 of it, 3 all of an fp32 value).  False: a wait ran out.
 //
 // A lane takes one piece of 8 + 8 channels (8 RoPE pairs) of a token, a warp 4 pieces of 8 tokens, and at D = 128 of the 8
 // tokens 32 further on.  The 8 lanes of a 16-byte wavefront are tokens n and n ^ 4 by 4 pieces: their chunks of the
@@ -110,7 +110,7 @@ struct Words {                                                       // index wo
     static __device__ __forceinline__ int first(int pl) { return C == 4 ? pl * 2 : pl / (C / 8); }
 };
 
-template <int D, int C, bool PG, int ST>
+template <int D, int C, bool PG, int ST, int KP>
 __device__ __forceinline__ bool rebuild_keys(const RebuildArgs &b, int rw, int tok_first, int ntiles, int st, int len) {
     constexpr int kTile = (D / 64) * 64 * 128;
     constexpr int NP = D / (2 * C);
@@ -181,12 +181,13 @@ __device__ __forceinline__ bool rebuild_keys(const RebuildArgs &b, int rw, int t
             }
         }
         if (!__all_sync(0xffffffffu, tc::mbar_wait_or_dead(b.kempty + 8u * s, par, b.wait_ns, b.dead))) return false;
-        const uint32_t off = (uint32_t)s * (3 * kTile);
+        const uint32_t off = (uint32_t)s * ((KP + 1) * kTile);
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const uint32_t kl[4] = {k0[u].x, k0[u].y, k0[u].z, k0[u].w};
             const uint32_t kh[4] = {k1[u].x, k1[u].y, k1[u].z, k1[u].w};
             uint32_t ah[4], al[4], bh[4], bl[4];                     // rotated: bf16 parts of the low and high channels
+            [[maybe_unused]] uint32_t az[4], bz[4];                  // third ones
             const float2 minus = f2(-1.f, -1.f);
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
@@ -198,12 +199,21 @@ __device__ __forceinline__ bool rebuild_keys(const RebuildArgs &b, int rw, int t
                 const float2 da = __ffma2_rn(unpack2(ah[k]), minus, ra), db = __ffma2_rn(unpack2(bh[k]), minus, rb);
                 al[k] = cvt_bf16x2(da.y, da.x);
                 bl[k] = cvt_bf16x2(db.y, db.x);
+                if constexpr (KP == 3) {
+                    const float2 ea = __ffma2_rn(unpack2(al[k]), minus, da), eb = __ffma2_rn(unpack2(bl[k]), minus, db);
+                    az[k] = cvt_bf16x2(ea.y, ea.x);
+                    bz[k] = cvt_bf16x2(eb.y, eb.x);
+                }
             }
             const uint32_t at = off + u * (32 * 128);                // 32 rows further: the same swizzle
             sts128(lo_at + at, make_uint4(ah[0], ah[1], ah[2], ah[3]));
             sts128(hi_at + at, make_uint4(bh[0], bh[1], bh[2], bh[3]));
             sts128(lo_at + at + kTile, make_uint4(al[0], al[1], al[2], al[3]));
             sts128(hi_at + at + kTile, make_uint4(bl[0], bl[1], bl[2], bl[3]));
+            if constexpr (KP == 3) {
+                sts128(lo_at + at + 2 * kTile, make_uint4(az[0], az[1], az[2], az[3]));
+                sts128(hi_at + at + 2 * kTile, make_uint4(bz[0], bz[1], bz[2], bz[3]));
+            }
         }
         tc::fence_async_smem();
         __syncwarp();
@@ -234,7 +244,7 @@ __device__ __forceinline__ bool rebuild_keys(const RebuildArgs &b, int rw, int t
 }
 
 // The values of the same tiles, by 2 warps of 32 tokens each: gathers and stores, nothing between them.
-template <int D, int C, bool PG, int ST>
+template <int D, int C, bool PG, int ST, int KP>
 __device__ __forceinline__ bool rebuild_values(const RebuildArgs &b, int vw, int tok_first, int ntiles, int st, int len) {
     constexpr int kTile = (D / 64) * 64 * 128;
     constexpr int NP = D / (2 * C);
@@ -261,7 +271,7 @@ __device__ __forceinline__ bool rebuild_values(const RebuildArgs &b, int vw, int
     uint32_t par = 1;
     for (int t = 0; t < ntiles; ++t) {
         if (!__all_sync(0xffffffffu, tc::mbar_wait_or_dead(b.vempty + 8u * s, par, b.wait_ns, b.dead))) return false;
-        const uint32_t vb = b.stages + (uint32_t)s * (3 * kTile) + 2 * kTile;
+        const uint32_t vb = b.stages + (uint32_t)s * ((KP + 1) * kTile) + KP * kTile;
 #pragma unroll
         for (int g0 = 0; g0 < 4; g0 += 2) {                          // loads of two groups before their stores
             uint4 v[2][IT][2];

@@ -83,12 +83,13 @@ __device__ __forceinline__ RowTiles row_space(const int32_t *starts, const int32
     return r;
 }
 
-// NT tokens per tile; KP bf16 parts per key; NR columns; three parts of P.
+// NT tokens per tile; KP bf16 parts per key (three hold a rebuilt, rotated key's fp32 values whole: calls of one launch are
+// bound by latency, and what a third part costs does not show); NR columns; three parts of P.
 template <int D, int NR, int C, bool PG>
 struct RowsPlan {
     static constexpr bool coded = C != 0;
     static constexpr int NT = coded ? 64 : 128;
-    static constexpr int KP = coded ? 2 : 1;
+    static constexpr int KP = coded ? 3 : 1;
     static constexpr int PARTS = 3;
     static constexpr int kPanel = NT * 128;
     static constexpr int kTile = (D / 64) * kPanel;
@@ -97,7 +98,7 @@ struct RowsPlan {
     static constexpr int kP = PARTS * kPart;                         // of one stream
     static constexpr int kQ = (D / 64) * NR * 128;
     static constexpr int NQ = coded ? 1 : 2;                         // buffers of queries
-    static constexpr int ST = D == 64 ? 4 : coded || NR == 16 ? 3 : 2;
+    static constexpr int ST = D == 64 ? 4 : !coded && NR == 16 ? 3 : 2;
     static constexpr int kTable = coded && !PG ? kTableBytes : 0;
     static constexpr int offStage = 0;
     static constexpr int offP = ST * kStage;
@@ -152,6 +153,12 @@ __device__ __forceinline__ float unordered(int i) { return __int_as_float(i ^ ((
 
 // Tiles up to which a CTA takes all tokens of its rows.
 constexpr int kDirectTiles = 8;
+
+// Tiles of a stream after which O moves from tensor memory into registers: the tensor cores cut what they add to 24 bits
+// instead of rounding it, always toward zero, so a long run of additions drifts (32768 tokens, 16 heads: off by 2e-6
+// without the moves and 6e-7 with them, in the same time).
+constexpr int kFlush = 4;
+static_assert(kDirectTiles / 2 <= kFlush, "direct calls keep O in tensor memory");
 
 // SCORES: every attended token's scores are kept (NR = 16 only).
 // DIRECT: grid = sequences x KV heads; a CTA has all tokens of its rows, merges its two streams and the other part, writes
@@ -351,6 +358,7 @@ __global__ void __launch_bounds__(RowsPlan<D, NR, C, PG>::kThreads, 1)
             float l[NR];
 #pragma unroll
             for (int r = 0; r < NR; ++r) l[r] = 0.f;
+            float osum[DIRECT ? 1 : NR] = {};                        // this channel's O of the tiles before the last move
             float kept[SCORES && DIRECT ? kDirectTiles / 2 : 1][8] = {};   // this token's scores in the stream's tiles
             int j = 0;                                               // tiles of this stream in the item
             for (int t = 0; ok && t < x.ntiles; ++t, ++g) {
@@ -362,6 +370,19 @@ __global__ void __launch_bounds__(RowsPlan<D, NR, C, PG>::kThreads, 1)
                 tc::tc_fence_after();
                 const int n = x.tok_first + t * NT + token;
                 const bool in = token >= 0 && n >= x.st && n < x.len;
+                if constexpr (!DIRECT) {
+                    if (ok && j > 0 && j % kFlush == 0) {            // the next product starts O afresh
+#pragma unroll
+                        for (int c = 0; c < NR; c += 16) {
+                            if (c < cols) {
+                                float o[16];
+                                read_o(to, c, o);
+#pragma unroll
+                                for (int k = 0; k < 16; ++k) osum[c + k] += o[k];
+                            }
+                        }
+                    }
+                }
                 // 16 columns in the exponent's units relative to the reference
                 auto load = [&](int c, float (&v)[16]) {
                     uint32_t s[16];
@@ -434,7 +455,10 @@ __global__ void __launch_bounds__(RowsPlan<D, NR, C, PG>::kThreads, 1)
                     stream_sync(bar);
 #pragma unroll
                     for (int r2 = 0; r2 < NR; ++r2)
-                        if (r2 < cols) l[r2] *= corr[r2];
+                        if (r2 < cols) {
+                            l[r2] *= corr[r2];
+                            if constexpr (!DIRECT) osum[r2] *= corr[r2];
+                        }
                     if (j > 0) {
 #pragma unroll 1
                         for (int c = 0; c < PARTS * NR; c += 16) {
@@ -616,14 +640,16 @@ __global__ void __launch_bounds__(RowsPlan<D, NR, C, PG>::kThreads, 1)
                                                            : f2(-CUDART_INF_F, 0.f);
                 }
                 if (all_ok && j > 0) {
-#pragma unroll 1
-                    for (int c = 0; c < cols; c += 16) {
-                        float o[16];
-                        read_o(to, c, o);
-                        float *dst = a.ws_o + (rec + c) * D + chan;
 #pragma unroll
-                        for (int k = 0; k < 16; ++k)
-                            if (chan >= 0 && c + k < a.R) dst[k * D] = o[k];
+                    for (int c = 0; c < NR; c += 16) {
+                        if (c < cols) {
+                            float o[16];
+                            read_o(to, c, o);
+                            float *dst = a.ws_o + (rec + c) * D + chan;
+#pragma unroll
+                            for (int k = 0; k < 16; ++k)
+                                if (chan >= 0 && c + k < a.R) dst[k * D] = o[k] + osum[c + k];
+                        }
                     }
                 }
             }
@@ -723,7 +749,7 @@ __global__ void __launch_bounds__(RowsPlan<D, NR, C, PG>::kThreads, 1)
                 tc::tc_fence_after();
                 const uint32_t p_lo = tc::uniform(tc::desc_lo(base + P::offP + w * P::kP, P::kPart));
                 const uint32_t v_lo = tc::uniform(tc::desc_lo(vb, P::kPanel)), od = tc::uniform(tmem + 64 + w * 96);
-                const uint32_t more = tc::uniform(t >= 2);               // else O of this stream holds nothing of the item yet
+                const uint32_t more = tc::uniform((t >> 1) % kFlush != 0);   // else O of this stream holds nothing to keep
                 if (tc::elect_one()) {
 #pragma unroll
                     for (int k = 0; k < NT / 16; ++k)                    // 16 tokens per product
@@ -782,9 +808,9 @@ __global__ void __launch_bounds__(RowsPlan<D, NR, C, PG>::kThreads, 1)
         b.dead = dead;
         if (warp < P::kRebuild + 8) {
             asm volatile("setmaxnreg.inc.sync.aligned.u32 112;");
-            rebuild_keys<D, C, PG, ST>(b, warp - P::kRebuild, item0.tok_first, item0.ntiles, item0.st, item0.len);
+            rebuild_keys<D, C, PG, ST, KP>(b, warp - P::kRebuild, item0.tok_first, item0.ntiles, item0.st, item0.len);
         } else {
-            rebuild_values<D, C, PG, ST>(b, warp - P::kValues, item0.tok_first, item0.ntiles, item0.st, item0.len);
+            rebuild_values<D, C, PG, ST, KP>(b, warp - P::kValues, item0.tok_first, item0.ntiles, item0.st, item0.len);
         }
     }
 
