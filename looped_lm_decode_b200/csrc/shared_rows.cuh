@@ -21,6 +21,10 @@
 // ragged sequences keeps every SM's copies in flight.  Warps: 0-3 and 4-7 softmax of the two streams that take the tiles
 // in turn; then two that issue the products, the copying one (bf16 cache: TMA; coded cache: eight warps that rebuild
 // keys, two that rebuild values) and one that loads the queries.
+//
+// What bounds it: long bf16 prefixes the HBM (32768 tokens, 8 queries, 16 heads: 268 MB in 47 us with the merge, 5.7 TB/s,
+// 87% of a copy; 16 ragged sequences of up to 16384 tokens with scores: 305 MB in 56 us and 8 us of merge), short ones the
+// chain of a tile through copy, product, softmax and product (1000 tokens, 3 queries, 16 heads, one launch: 10.1 us).
 #pragma once
 
 #include <cuda.h>
