@@ -114,6 +114,13 @@ __global__ void __launch_bounds__(256) shared_merge_kernel(const MergeArgs a, co
 // rebuilding, 77 where the other takes 69, so there it only serves calls of one launch.
 constexpr int kFewRows = 32, kFewRowsCoded = 16;
 
+// Tiles up to which a CTA of the kernel with rows as M takes all tokens of its rows and writes the result itself: one launch
+// and no records, but tile after tile (bf16 1.1 us each, coded 1.0).  Calls in a graph / made one by one, us, one launch
+// against two, 64 queries, 16 heads: bf16 3 tiles 10.8 / 11.6 against 11.0 / 16.1, 6 tiles 14.1 / 14.4 against 11.4 / 16.4;
+// coded 4 tiles 13.1 / 13.1 against 13.7 / 16.7, 8 tiles 17.1 / 17.2 against 14.3 / 16.7.  Records of many rows cost more
+// than the tiles: 200 queries, 16 heads, 8 tiles: bf16 18.0 against 18.8, coded 19.4 against 22.5.
+constexpr int kDirectTilesM = 3, kDirectTilesCoded = 4, kManyRows = 2048;
+
 // Splits: a CTA owns an SM (its tiles fill shared memory), so the splits that fill whole waves of 148 CTAs are
 // compared by waves x (tiles per split + set-up), the set-up and drain of a CTA counted as two tiles.
 SharedPlan plan_shared(int Hkv, int R, int max_len, bool coded) {
@@ -121,11 +128,16 @@ SharedPlan plan_shared(int Hkv, int R, int max_len, bool coded) {
     const int nt = coded ? 64 : 128;                                 // tokens per tile
     p.few = coded ? R <= kFewRowsCoded && max_len <= kDirectTiles * nt : R <= kFewRows;
     const long tiles = (max_len + nt - 1) / nt;
+    // Few tiles: a head on one CTA, in one launch without a workspace, instead of its tiles on several and a merge: 1000
+    // tokens, 3 queries, 16 heads 14 us against 19 where calls are made one by one (10 against 8 in a graph).
+    p.direct = tiles <= (p.few || (long)Hkv * R >= kManyRows ? kDirectTiles : coded ? kDirectTilesCoded : kDirectTilesM);
     // More than 128 rows: two blocks on a CTA share its tiles, or are CTAs of their own with twice the tiles.  A coded tile
-    // is rebuilt once for both; a bf16 tile's second read is L2's, and pays off while a CTA has few tiles (us with two
+    // is rebuilt once for both (direct calls with SMs to spare rebuild it twice: 4 tiles, 200 queries, 16 heads 15.1 us
+    // against 19.7); a bf16 tile's second read is L2's, and pays off while a CTA has few tiles (us with two
     // blocks / one: 16347 tokens, 4 heads, 256 rows 24.1 / 23.9, 4096, 16 heads 30.6 / 28.7; 32768, 16 heads, 200 rows
     // 93.2 / 111.7).
-    p.mb = R > 128 && (coded || tiles * Hkv * ((R + 255) / 256) >= 8 * 148) ? 2 : 1;
+    const bool share = coded ? !(p.direct && (long)Hkv * ((R + 127) / 128) <= 148) : tiles * Hkv * ((R + 255) / 256) >= 8 * 148;
+    p.mb = R > 128 && share ? 2 : 1;
     p.nz = (R + p.mb * 128 - 1) / (p.mb * 128);
     const long units = (long)Hkv * p.nz;
     long best = -1;
@@ -140,9 +152,8 @@ SharedPlan plan_shared(int Hkv, int R, int max_len, bool coded) {
             p.nsplit = (int)ns;
         }
     }
-    // few tiles: a head on one CTA, in one launch without a workspace, instead of its tiles on several and a merge: 1000
-    // tokens, 3 queries, 16 heads 14 us against 19 where calls are made one by one (10 against 8 in a graph)
-    p.direct = p.few && tiles <= kDirectTiles;
+    if (p.direct) p.nsplit = 1;
+    if (!p.few && p.nsplit == 1) p.direct = true;                    // enough rows to fill the SMs: nothing to merge
     p.nrec = p.direct ? 0 : p.few ? 2 * p.nsplit : p.nsplit;         // a CTA's two streams write a record each
     return p;
 }

@@ -8,7 +8,7 @@ namespace loopvq {
 
 struct SharedPlan {
     bool few;                // shared_rows_kernel; else shared_attn_kernel with mb blocks of 128 rows
-    bool direct;             // one CTA per KV head, which writes the result itself
+    bool direct;             // one CTA per KV head (and block of rows), which writes the result itself
     int mb, nsplit, nz, nrec;
 };
 
@@ -79,7 +79,14 @@ inline cudaError_t launch_p(const SharedArgs &a, const SharedPlan &p, const CUte
             return p.direct ? launch_rows_t<D, 32, C, PG, false, true>(r, km, vm, s)
                             : launch_rows_t<D, 32, C, PG, false, false>(r, km, vm, s);
     }
-    return p.mb == 2 ? launch_t<D, 2, C, PG>(a, p, km, vm, s) : launch_t<D, 1, C, PG>(a, p, km, vm, s);
+    SharedArgs x = a;
+    if (p.direct) {
+        x.other_out = o.out;
+        x.other_lse = o.lse;
+        x.out = out;
+        x.lse = lse;
+    }
+    return p.mb == 2 ? launch_t<D, 2, C, PG>(x, p, km, vm, s) : launch_t<D, 1, C, PG>(x, p, km, vm, s);
 }
 
 template <int C, bool PG>

@@ -50,6 +50,9 @@ struct SharedArgs {
     const uint16_t *slk, *slv;
     const float *rope;
     int K;
+    // one split: the kernel writes the result itself, merged with the other part (null where there is none)
+    const float *other_out, *other_lse;
+    float *out, *lse;        // out null: records for the merge; lse may be null
 };
 
 // Shared-memory and tensor-memory plan.  NT tokens per tile, KP bf16 parts per key.
@@ -214,6 +217,23 @@ __global__ void __launch_bounds__(Plan<D, MB, C, PG>::kThreads, 1)
     const int nsteps = ntiles * MB;                                  // step i: stream i & 1
     const size_t rec = ((size_t)split * a.Hkv + h) * a.R;            // this split's records of the head
 
+    const bool whole = a.out != nullptr;                             // no other split, no merge
+    auto result_row = [&](int r) {
+        return (size_t)(r >> a.qshift) * a.Hq + h * a.qpk + (r & (a.qpk - 1));
+    };
+    if (ntiles == 0 && whole) {                                      // no tokens: the other part, or zeros
+        const int rows = min(MB * 128, a.R - r0);
+        for (int it = tid; it < rows * (D / 4); it += P::kThreads) {
+            const size_t row = result_row(r0 + it / (D / 4));
+            const float ol = a.other_lse ? a.other_lse[row] : -CUDART_INF_F;
+            float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (ol != -CUDART_INF_F) x = *reinterpret_cast<const float4 *>(a.other_out + row * D + it % (D / 4) * 4);
+            if (!(fabsf(ol) < CUDART_INF_F) && ol != -CUDART_INF_F) x = make_float4(ol - ol, ol - ol, ol - ol, ol - ol);
+            *reinterpret_cast<float4 *>(a.out + row * D + it % (D / 4) * 4) = x;
+            if (a.lse != nullptr && it % (D / 4) == 0) a.lse[row] = ol == CUDART_INF_F ? ol - ol : ol;
+        }
+        return;
+    }
     if (ntiles == 0) {                                               // nothing in this split
         for (int r = r0 + tid; r < min(r0 + MB * 128, a.R); r += P::kThreads) a.ws_ml[rec + r] = f2(-CUDART_INF_F, 0.f);
         return;
@@ -389,16 +409,33 @@ __global__ void __launch_bounds__(Plan<D, MB, C, PG>::kThreads, 1)
             }
             asm volatile("bar.sync 1, 256;" ::: "memory");
         }
+        // the factors of this thread's O and of the other part in the result, where the kernel writes it
+        const size_t dst = rq < a.R ? result_row(rq) : 0;
+        float f_own = 1.f, f_other = 0.f;
+        if (whole && rq < a.R && (MB == 2 || w == 0)) {
+            const float ol = a.other_lse ? a.other_lse[dst] * 1.44269504088896340736f : -CUDART_INF_F;
+            const float top = fmaxf(sm.m, ol);
+            float l2 = -CUDART_INF_F;
+            f_own = 0.f;
+            if (top != -CUDART_INF_F) {
+                const float eo = ex2(sm.m - top), ex = ex2(ol - top), total = sm.l * eo + ex;
+                l2 = top + log2f(total);
+                f_own = eo / total;
+                f_other = ex / total;
+            }
+            if (!ok || sm.l != sm.l || ol != ol) f_own = f_other = l2 = CUDART_NAN_F;
+            if (a.lse != nullptr) a.lse[dst] = l2 == -CUDART_INF_F ? l2 : l2 * 0.69314718055994530942f;
+        }
         if (any && (MB == 2 || w == 0)) {
             // (a maximum passes NaN over: a row of nothing but NaN must not look like one without tokens)
-            if (rq < a.R) a.ws_ml[rec + rq] = ok && sm.l == sm.l ? f2(sm.m, sm.l) : f2(0.f, CUDART_NAN_F);
+            if (!whole && rq < a.R) a.ws_ml[rec + rq] = ok && sm.l == sm.l ? f2(sm.m, sm.l) : f2(0.f, CUDART_NAN_F);
 #pragma unroll 1
             for (int c = 0; c < D; c += 32) {
                 uint32_t o[32];
                 tc::tmem_ld32(to + c, o);
                 tc::tmem_wait_ld(o);
                 if (rq < a.R) {
-                    float4 *dst = reinterpret_cast<float4 *>(a.ws_o) + (rec / a.R * (D / 4) + c / 4) * a.R + rq;
+                    float4 *rec_o = reinterpret_cast<float4 *>(a.ws_o) + (rec / a.R * (D / 4) + c / 4) * a.R + rq;
 #pragma unroll
                     for (int k = 0; k < 8; ++k) {
                         float4 x = make_float4(__uint_as_float(o[4 * k]), __uint_as_float(o[4 * k + 1]),
@@ -410,7 +447,18 @@ __global__ void __launch_bounds__(Plan<D, MB, C, PG>::kThreads, 1)
                             x.z = x.z * c0 + y.z * c1;
                             x.w = x.w * c0 + y.w * c1;
                         }
-                        dst[(size_t)k * a.R] = x;
+                        if (whole) {
+                            const size_t at = dst * D + c + 4 * k;
+                            float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+                            if (a.other_lse && f_other != 0.f) y = *reinterpret_cast<const float4 *>(a.other_out + at);
+                            x = f_own != 0.f ? make_float4(x.x * f_own, x.y * f_own, x.z * f_own, x.w * f_own)
+                                             : make_float4(0.f, 0.f, 0.f, 0.f);
+                            if (f_other != 0.f)
+                                x = make_float4(x.x + y.x * f_other, x.y + y.y * f_other, x.z + y.z * f_other, x.w + y.w * f_other);
+                            *reinterpret_cast<float4 *>(a.out + at) = x;
+                        } else {
+                            rec_o[(size_t)k * a.R] = x;
+                        }
                     }
                 }
             }

@@ -102,6 +102,25 @@ def test_bf16_many_rows(rows):
     run_bf16(2111, rows, 1, 2, 128)
 
 
+@pytest.mark.parametrize("n", [0, 1, 100, 257, 385, 513, 1024, 1025])
+@pytest.mark.parametrize("rows,hkv,hq", [(33, 1, 1), (140, 2, 2), (70, 16, 32), (600, 40, 40)])
+def test_results_with_and_without_records(rows, hkv, hq, n):
+    """One launch that writes the result, or records and a merge: every side of the rules that choose, into the other part's
+    own memory, with empty parts."""
+    g = gen(13 + n)
+    cache = LQ.Bf16Cache(bf16(g, 1, hkv, max(n, 8), 64), bf16(g, 1, hkv, max(n, 8), 64), hq)
+    q, lens = bf16(g, rows, hq, 64), i32([n])
+    other = make_other(g, rows, hq, 64)
+    other[1][:, -1] = -math.inf
+    want = reference(q, cache.k[0, :, :n].double(), cache.v[0, :, :n].double(), (torch.where(
+        other[1][..., None] == -math.inf, 0.0, other[0]), other[1]))
+    out = other[0].clone()
+    got = LQ.bf16_shared_attn(cache, 0, q, lens, n, other=(out, other[1]), out=out)
+    LQ.fault_check()
+    assert got[0].data_ptr() == out.data_ptr()
+    check(got, want)
+
+
 def test_bf16_long_and_scaled():
     run_bf16(40001, 4, 1, 1, 128)
     run_bf16(3001, 20, 2, 2, 128, scale=0.01)
@@ -350,11 +369,10 @@ def test_repeated_captured_and_on_other_streams(rows):
         assert torch.equal(outs[2 + i], eager[i][0]) and torch.equal(lses[2 + i], eager[i][1])
 
 
-@pytest.mark.parametrize("rows", [4, 200])
-def test_a_wait_that_runs_out_is_reported(rows):
+@pytest.mark.parametrize("rows,n", [(4, 700), (200, 700), (200, 252), (90, 252)])
+def test_a_wait_that_runs_out_is_reported(rows, n):
     """With a limit of 0 every wait tests once and gives up: NaN rows, a fault, and the next call works."""
     g = gen(9)
-    n = 700
     cache = LQ.Bf16Cache(bf16(g, 1, 1, n, 128), bf16(g, 1, 1, n, 128), 1)
     coded = make_coded(g, 1, 1, 128, 4, 4, 1, 256, 1, n)
     q, lens = bf16(g, rows, 1, 128), i32([n])
