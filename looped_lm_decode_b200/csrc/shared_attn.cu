@@ -115,11 +115,16 @@ __global__ void __launch_bounds__(256) shared_merge_kernel(const MergeArgs a, co
 constexpr int kFewRows = 32, kFewRowsCoded = 16;
 
 // Tiles up to which a CTA of the kernel with rows as M takes all tokens of its rows and writes the result itself: one launch
-// and no records, but tile after tile (bf16 1.1 us each, coded 1.0).  Calls in a graph / made one by one, us, one launch
-// against two, 64 queries, 16 heads: bf16 3 tiles 10.8 / 11.6 against 11.0 / 16.1, 6 tiles 14.1 / 14.4 against 11.4 / 16.4;
-// coded 4 tiles 13.1 / 13.1 against 13.7 / 16.7, 8 tiles 17.1 / 17.2 against 14.3 / 16.7.  Records of many rows cost more
-// than the tiles: 200 queries, 16 heads, 8 tiles: bf16 18.0 against 18.8, coded 19.4 against 22.5.
+// and no records, but tile after tile.  Calls in a graph / made one by one, us, one launch against two, 64 queries, 16
+// heads: bf16 3 tiles 12.3 / 12.5 against 11.0 / 16.1, 6 tiles 14.1 / 14.4 (P in two parts) against 11.4 / 16.4; coded 4
+// tiles 14.9 / 15.0 against 13.7 / 16.7, 8 tiles 17.1 / 17.2 (two parts) against 14.3 / 16.7.  Records of many rows cost
+// more than the tiles: 200 queries, 16 heads: bf16 4 tiles 15.4 against 17.0, 8 tiles 18.0 against 18.8; coded 8 tiles 22.1
+// against 22.5.
 constexpr int kDirectTilesM = 3, kDirectTilesCoded = 4, kManyRows = 2048;
+
+// Tokens up to which such calls hold P and rebuilt keys in three bf16 parts.  Few tokens average little out: 52 coded
+// tokens are off by 2.9e-6 with two parts, 5.8e-7 with three (3 bf16 tiles 12.3 us against 10.8, 4 coded ones 14.9 / 13.1).
+constexpr int kFineTokens = 512;
 
 // Splits: a CTA owns an SM (its tiles fill shared memory), so the splits that fill whole waves of 148 CTAs are
 // compared by waves x (tiles per split + set-up), the set-up and drain of a CTA counted as two tiles.
@@ -133,7 +138,7 @@ SharedPlan plan_shared(int Hkv, int R, int max_len, bool coded) {
     p.direct = tiles <= (p.few || (long)Hkv * R >= kManyRows ? kDirectTiles : coded ? kDirectTilesCoded : kDirectTilesM);
     // More than 128 rows: two blocks on a CTA share its tiles, or are CTAs of their own with twice the tiles.  A coded tile
     // is rebuilt once for both (direct calls with SMs to spare rebuild it twice: 4 tiles, 200 queries, 16 heads 15.1 us
-    // against 19.7); a bf16 tile's second read is L2's, and pays off while a CTA has few tiles (us with two
+    // against 19.7, keys in two parts); a bf16 tile's second read is L2's, and pays off while a CTA has few tiles (us with two
     // blocks / one: 16347 tokens, 4 heads, 256 rows 24.1 / 23.9, 4096, 16 heads 30.6 / 28.7; 32768, 16 heads, 200 rows
     // 93.2 / 111.7).
     const bool share = coded ? !(p.direct && (long)Hkv * ((R + 127) / 128) <= 148) : tiles * Hkv * ((R + 255) / 256) >= 8 * 148;
@@ -154,6 +159,7 @@ SharedPlan plan_shared(int Hkv, int R, int max_len, bool coded) {
     }
     if (p.direct) p.nsplit = 1;
     if (!p.few && p.nsplit == 1) p.direct = true;                    // enough rows to fill the SMs: nothing to merge
+    p.fine = !p.few && p.direct && p.mb == 1 && tiles * nt <= kFineTokens;
     p.nrec = p.direct ? 0 : p.few ? 2 * p.nsplit : p.nsplit;         // a CTA's two streams write a record each
     return p;
 }
@@ -183,7 +189,7 @@ cudaError_t encode_tiled_fn(EncodeTiled *out) {
     return cudaSuccess;
 }
 
-// Map of one sequence's rows [rows][D]: boxes of 128 tokens x 64 channels, rows of 128 bytes swizzled.
+// Map of one sequence's rows [rows][D]: boxes of nt tokens x 64 channels, rows of 128 bytes swizzled.
 cudaError_t make_map(CUtensorMap *m, const uint16_t *p, size_t rows, int D, int nt) {
     EncodeTiled enc;
     cudaError_t e = encode_tiled_fn(&enc);
@@ -290,8 +296,9 @@ cudaError_t launch_bf16_shared(const loopvq_bf16_cache &c, int seq, const uint16
     a.head_rows = c.Nmax;
     const size_t at = (size_t)seq * c.Hkv * c.Nmax * c.D, map_rows = (size_t)c.Hkv * c.Nmax;
     CUtensorMap km, vm;
-    e = make_map(&km, c.k + at, map_rows, c.D, 128);
-    if (e == cudaSuccess) e = make_map(&vm, c.v + at, map_rows, c.D, 128);
+    const int nt = p.fine ? 64 : 128;                                // rows of a copy
+    e = make_map(&km, c.k + at, map_rows, c.D, nt);
+    if (e == cudaSuccess) e = make_map(&vm, c.v + at, map_rows, c.D, nt);
     if (e == cudaSuccess) e = launch_d<0, false>(c.D, a, p, km, vm, other, out, lse, s);
     if (e != cudaSuccess || p.direct) return e;
     return finish(a, p, c.D, other, out, lse, s);

@@ -9,14 +9,15 @@ namespace loopvq {
 struct SharedPlan {
     bool few;                // shared_rows_kernel; else shared_attn_kernel with mb blocks of 128 rows
     bool direct;             // one CTA per KV head (and block of rows), which writes the result itself
+    bool fine;               // shared_attn_kernel with P and rebuilt keys in three bf16 parts, tiles of 64 tokens
     int mb, nsplit, nz, nrec;
 };
 
-template <int D, int MB, int C, bool PG>
+template <int D, int MB, int C, bool PG, bool FINE>
 inline cudaError_t launch_t(const SharedArgs &a, const SharedPlan &p, const CUtensorMap &km, const CUtensorMap &vm,
                      cudaStream_t s) {
-    using PL = Plan<D, MB, C, PG>;
-    auto kern = shared_attn_kernel<D, MB, C, PG>;
+    using PL = Plan<D, MB, C, PG, FINE>;
+    auto kern = shared_attn_kernel<D, MB, C, PG, FINE>;
     cudaError_t e = ensure_dynamic_smem((const void *)kern, PL::kAlloc);
     if (e != cudaSuccess) return e;
     return launch_pdl(kern, dim3(p.nsplit, a.Hkv, p.nz), PL::kThreads, PL::kAlloc, s, a, km, vm);
@@ -86,7 +87,8 @@ inline cudaError_t launch_p(const SharedArgs &a, const SharedPlan &p, const CUte
         x.out = out;
         x.lse = lse;
     }
-    return p.mb == 2 ? launch_t<D, 2, C, PG>(x, p, km, vm, s) : launch_t<D, 1, C, PG>(x, p, km, vm, s);
+    if (p.fine) return launch_t<D, 1, C, PG, true>(x, p, km, vm, s);
+    return p.mb == 2 ? launch_t<D, 2, C, PG, false>(x, p, km, vm, s) : launch_t<D, 1, C, PG, false>(x, p, km, vm, s);
 }
 
 template <int C, bool PG>

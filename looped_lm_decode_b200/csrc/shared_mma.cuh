@@ -15,11 +15,12 @@
 // they take the two halves of the rows (and share every tile).
 //
 // Precision: the library returns fp32, so P is not rounded to bf16 once but split into two bf16 parts (the
-// remainder of the first rounding in the second, which leaves 2^-17 of P at most), two products into the same accumulator; a
-// rebuilt, rotated key is split the same way.  bf16 queries, keys and values are exact.
+// remainder of the first rounding in the second, which leaves 2^-17 of P at most), two products into the same
+// accumulator, or three where tokens are few (FINE); a rebuilt, rotated key is split the same way.  bf16 queries, keys
+// and values are exact.
 //
-// P overwrites S in place, 16 score columns becoming 8 + 8 columns of packed pairs (one product's tokens).  The running maximum moves
-// only when a tile passes it by 2^8 (any reference is exact; it bounds P), so O is rarely rescaled.
+// P overwrites S in place, 16 score columns becoming 8 + 8 columns of packed pairs (one product's tokens; a third part
+// has columns of its own).  The running maximum moves only when a tile passes it by 2^8 (any reference is exact; it bounds P), so O is rarely rescaled.
 //
 // What bounds it: over a bf16 prefix the products and, with few tiles a CTA, its set-up and exchange (16347 tokens, 64
 // queries, 4 KV / 16 query heads: 26 us with the merge, tensor pipe busy 35% of 23); over a coded one the shared-memory
@@ -55,20 +56,22 @@ struct SharedArgs {
     float *out, *lse;        // out null: records for the merge; lse may be null
 };
 
-// Shared-memory and tensor-memory plan.  NT tokens per tile, KP bf16 parts per key.
+// Shared-memory and tensor-memory plan.  NT tokens per tile, KP bf16 parts per key, PARTS of P.
+// FINE: P and rebuilt keys in three parts, all of an fp32 value, where one CTA writes the result of few tokens.
 // bf16 cache: the queries lie in shared memory (S and O fill the tensor memory at 128-token tiles).
 // Coded cache: 64-token tiles leave tensor memory for the queries, so the products read only the tiles from shared
 // memory, whose bandwidth they share with the rebuilding.
-template <int D, int MB, int C, bool PG>
+template <int D, int MB, int C, bool PG, bool FINE>
 struct Plan {
     static constexpr bool coded = C != 0;
-    static constexpr int NT = coded ? 64 : 128;
-    static constexpr int KP = coded ? 2 : 1;
+    static constexpr int NT = coded || FINE ? 64 : 128;
+    static constexpr int KP = coded ? (FINE ? 3 : 2) : 1;
+    static constexpr int PARTS = FINE ? 3 : 2;
     static constexpr int kPanel = NT * 128;                          // 64 channels of a tile
     static constexpr int kTile = (D / 64) * kPanel;
     static constexpr int kStage = (KP + 1) * kTile;                  // K parts, then V
     static constexpr int kQ = coded ? 0 : (D / 64) * 128 * 128;      // one row block
-    static constexpr int ST = D == 64 || coded ? 4 : MB == 1 ? 3 : 2;
+    static constexpr int ST = D == 64 ? 4 : coded ? (FINE ? 2 : 4) : FINE ? 4 : MB == 1 ? 3 : 2;
     static constexpr int kTable = coded && !PG ? kTableBytes : 0;    // K slice, then V slice
     static constexpr int offQ = 0;
     static constexpr int offStage = MB * kQ;
@@ -83,7 +86,9 @@ struct Plan {
     static constexpr int kMma = coded ? 16 : 8;                      // warps: products;
     static constexpr int kCopy = coded ? 16 : 9;                     // copies (and the barriers' set-up);
     [[maybe_unused]] static constexpr int kRebuild = 8, kValues = 17;                 // the first of those that rebuild keys, values
-    static constexpr int colS = coded ? 64 : 128;                    // S of stream w at w * colS
+    static constexpr int colS = NT;                                  // S of stream w at w * colS
+    [[maybe_unused]] static constexpr int colP3 = 192;                // FINE: third part of P of stream w at 192 + 32 w
+    static_assert(!FINE || MB == 1, "Q of a second row block lies there");
     [[maybe_unused]] static constexpr int colQ = coded ? 128 : 0;                     // coded: Q of row block w at 128 + 64 w
     static_assert(kAlloc <= 232448, "shared memory");
     static_assert(ST * kStage >= 128 * D * 4, "the streams' exchange reuses the tiles");
@@ -92,13 +97,14 @@ struct Plan {
 constexpr int kTmemCols = 512;                                       // O of stream w at 256 + 128 w
 
 // The running softmax of one query row of one stream, and what its thread does with a tile's scores.
-template <int D, int NT>
+template <int D, int NT, int PARTS>
 struct RowSoftmax {
     float m, l;                                                      // maximum reference (log2 units), sum
 
-    // S columns at ts; tokens [lo, hi) of the tile count; O columns at to.  first: O holds nothing yet.
+    // S columns at ts (a third part of P goes to tp); tokens [lo, hi) of the tile count; O columns at to.  first: O holds
+    // nothing yet.
     // odone: barrier (parity) of the stream's previous O += P V.
-    __device__ __forceinline__ bool tile(uint32_t ts, uint32_t to, int lo, int hi, float qs, bool first, uint32_t odone,
+    __device__ __forceinline__ bool tile(uint32_t ts, uint32_t tp, uint32_t to, int lo, int hi, float qs, bool first, uint32_t odone,
                                          uint32_t odone_parity, uint64_t limit, volatile int *dead) {
         // 32 scores at a time, read from tensor memory once for the maximum and once for the exponentials: a tile's
         // scores in registers spill, and loops keep the code small enough for the instruction cache (a call of few
@@ -153,6 +159,7 @@ struct RowSoftmax {
         for (int c = 0; c < NT; c += 32) {
             uint32_t x[32];
             load(x, c);
+            [[maybe_unused]] uint32_t w3[16];
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
                 uint32_t w[16];
@@ -164,10 +171,13 @@ struct RowSoftmax {
                     s1 += p1;
                     const uint32_t hi2 = cvt_bf16x2(p1, p0);
                     w[k] = hi2;
-                    w[8 + k] = cvt_bf16x2(p1 - bf16hi(hi2), p0 - bf16lo(hi2));
+                    const float d0 = p0 - bf16lo(hi2), d1 = p1 - bf16hi(hi2);
+                    w[8 + k] = cvt_bf16x2(d1, d0);
+                    if constexpr (PARTS == 3) w3[half * 8 + k] = cvt_bf16x2(d1 - bf16hi(w[8 + k]), d0 - bf16lo(w[8 + k]));
                 }
                 tc::tmem_st16(ts + c + half * 16, w);
             }
+            if constexpr (PARTS == 3) tc::tmem_st16(tp + c / 2, w3);
         }
         l += s0 + s1;
         tc::tmem_wait_st();
@@ -178,11 +188,11 @@ struct RowSoftmax {
 // D channels (64 or 128), MB blocks of 128 query rows per CTA, C = 0 for a bf16 cache or the channels per code of
 // a coded one; PG: one codebook per channel group, whose slices (128 bytes per entry and more) do not fit beside
 // the tiles and are gathered from L2.
-template <int D, int MB, int C, bool PG>
-__global__ void __launch_bounds__(Plan<D, MB, C, PG>::kThreads, 1)
+template <int D, int MB, int C, bool PG, bool FINE>
+__global__ void __launch_bounds__(Plan<D, MB, C, PG, FINE>::kThreads, 1)
     shared_attn_kernel(const SharedArgs a, const __grid_constant__ CUtensorMap kmap,
                        const __grid_constant__ CUtensorMap vmap) {
-    using P = Plan<D, MB, C, PG>;
+    using P = Plan<D, MB, C, PG, FINE>;
     constexpr bool coded = C != 0;
     constexpr int NT = P::NT, KP = P::KP, ST = P::ST, NPAN = D / 64;
 
@@ -347,7 +357,7 @@ __global__ void __launch_bounds__(Plan<D, MB, C, PG>::kThreads, 1)
         const uint32_t ts = tmem + lane_base + w * P::colS, to = tmem + lane_base + 256 + w * 128;
         const int rq = r0 + (MB == 2 ? w * 128 : 0) + row;           // query row of this thread
         const bool any = __any_sync(0xffffffffu, rq < a.R);          // warps of padding only keep step
-        RowSoftmax<D, NT> sm{-CUDART_INF_F, 0.f};
+        RowSoftmax<D, NT, P::PARTS> sm{-CUDART_INF_F, 0.f};
         bool ok = true;
         int j = 0;
         for (int i = w; i < nsteps; i += 2, ++j) {
@@ -357,7 +367,7 @@ __global__ void __launch_bounds__(Plan<D, MB, C, PG>::kThreads, 1)
             tc::tc_fence_after();
             if (any) {
                 const int n0 = tok_first + t * NT;
-                ok = sm.tile(ts, to, st - n0, len - n0, a.qscale, j == 0, odone(w), (j - 1) & 1, a.wait_ns, dead);
+                ok = sm.tile(ts, tmem + lane_base + P::colP3 + w * 32, to, st - n0, len - n0, a.qscale, j == 0, odone(w), (j - 1) & 1, a.wait_ns, dead);
                 if (!ok) break;
             }
             tc::tc_fence_before();
@@ -519,13 +529,14 @@ __global__ void __launch_bounds__(Plan<D, MB, C, PG>::kThreads, 1)
             if (!wait(pfull(w), (i >> 1) & 1)) break;
             tc::tc_fence_after();
             const uint32_t od = tc::uniform(tmem + 256 + w * 128), pa = tc::uniform(tmem + w * P::colS);
+            [[maybe_unused]] const uint32_t pz = tc::uniform(tmem + P::colP3 + w * 32);
             const uint32_t v_lo = tc::uniform(tc::desc_lo(vb, P::kPanel)), more = tc::uniform(i > 1);
             if (tc::elect_one()) {
 #pragma unroll
-                for (int part = 0; part < 2; ++part)
+                for (int part = 0; part < P::PARTS; ++part)
 #pragma unroll
                     for (int k = 0; k < NT / 16; ++k)                // 16 tokens per product: 8 packed columns
-                        tc::mma_ts(od, pa + k * 16 + part * 8, v_lo + k * 128, tc::desc_hi(1024, 2), id_pv,
+                        tc::mma_ts(od, part < 2 ? pa + k * 16 + part * 8 : pz + k * 8, v_lo + k * 128, tc::desc_hi(1024, 2), id_pv,
                                    part + k > 0 ? 1u : more);
                 if ((MB == 1 || w == 1) && t + ST < ntiles) tc::mma_commit(vempty(s));
                 tc::mma_commit(odone(w));
