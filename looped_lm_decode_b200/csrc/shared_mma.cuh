@@ -20,7 +20,8 @@
 // and values are exact.
 //
 // P overwrites S in place, 16 score columns becoming 8 + 8 columns of packed pairs (one product's tokens; a third part
-// has columns of its own).  The running maximum moves only when a tile passes it by 2^8 (any reference is exact; it bounds P), so O is rarely rescaled.
+// has columns of its own).  The running maximum moves only when a tile passes it by 2^8 (any reference is exact; it
+// bounds P), so O is rarely rescaled.
 //
 // What bounds it: over a bf16 prefix the products and, with few tiles a CTA, its set-up and exchange (16347 tokens, 64
 // queries, 4 KV / 16 query heads: 26 us with the merge, tensor pipe busy 35% of 23); over a coded one the shared-memory
@@ -367,7 +368,8 @@ __global__ void __launch_bounds__(Plan<D, MB, C, PG, FINE>::kThreads, 1)
             tc::tc_fence_after();
             if (any) {
                 const int n0 = tok_first + t * NT;
-                ok = sm.tile(ts, tmem + lane_base + P::colP3 + w * 32, to, st - n0, len - n0, a.qscale, j == 0, odone(w), (j - 1) & 1, a.wait_ns, dead);
+                ok = sm.tile(ts, tmem + lane_base + P::colP3 + w * 32, to, st - n0, len - n0, a.qscale, j == 0, odone(w),
+                             (j - 1) & 1, a.wait_ns, dead);
                 if (!ok) break;
             }
             tc::tc_fence_before();
@@ -459,7 +461,7 @@ __global__ void __launch_bounds__(Plan<D, MB, C, PG, FINE>::kThreads, 1)
                         }
                         if (whole) {
                             const size_t at = dst * D + c + 4 * k;
-                            float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+                            float4 y = make_float4(0.f, 0.f, 0.f, 0.f);   // (factors of NaN make the row NaN)
                             if (a.other_lse && f_other != 0.f) y = *reinterpret_cast<const float4 *>(a.other_out + at);
                             x = f_own != 0.f ? make_float4(x.x * f_own, x.y * f_own, x.z * f_own, x.w * f_own)
                                              : make_float4(0.f, 0.f, 0.f, 0.f);

@@ -64,8 +64,8 @@ struct RowsArgs {
 
 // The tile space of a batch of ragged sequences: segment s = h * B + b holds the 128-token tiles of sequence b from its
 // start; all segments lie end to end and CTA c of G = min(CTAs, T) takes tiles [c T / G, (c + 1) T / G), so that every
-// CTA has the same work whatever the lengths, and the others none.  The part of segment s in CTA c is piece s + c (both only rise along the space, so no two
-// pieces share a number), and the pieces of a segment are consecutive.
+// CTA has the same work whatever the lengths, and the others none.  The part of segment s in CTA c is piece s + c (both
+// only rise along the space, so no two pieces share a number), and the pieces of a segment are consecutive.
 struct RowTiles {
     long long per_head, before;      // tiles of a KV head; those of the sequences before b
 };
