@@ -345,9 +345,9 @@ __global__ void __launch_bounds__(NT, NT == 256 ? 4 : 2) evict_select_kernel(con
                 while (parts < 32 && own2 * parts * 2 <= NT) parts *= 2;
                 const int quads = (count + 3) / 4;
                 for (int i0 = first; i0 < last; i0 += NT / parts) {
-                    const int i = i0 + tid / parts, share = tid % parts;
-                    const bool live = i < last;
-                    const uint32_t mine = list[live ? i : 0];
+                    const bool live = i0 + tid / parts < last;
+                    const int i = live ? i0 + tid / parts : first, share = tid % parts;   // (behind the list: not read)
+                    const uint32_t mine = list[i];
                     int higher = 0, j = share;
 #pragma unroll 4
                     for (; j < i / 4 && j < quads; j += parts) {     // earlier slots

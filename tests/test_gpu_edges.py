@@ -1,0 +1,52 @@
+"""Edges of the shared-prefix, scored and evicting calls that a user's program can reach: full lists, scores of -inf, long
+runs of accumulation, default workspaces on other streams, calls in a row without a kernel of another library between."""
+import math
+
+import pytest
+import torch
+
+import looped_lm_decode_b200 as LQ
+from tests.test_gpu_evict import evict_reference
+
+pytestmark = pytest.mark.gpu
+
+
+def gen(seed):
+    return torch.Generator(device="cuda").manual_seed(seed)
+
+
+def bf16(g, *shape):
+    return torch.randn(*shape, generator=g, device="cuda", dtype=torch.bfloat16)
+
+
+def i32(x):
+    return torch.tensor(x, dtype=torch.int32, device="cuda")
+
+
+# ------------------------------------------------------------------ eviction
+
+@pytest.mark.parametrize("count", [509, 510, 511, 512])
+@pytest.mark.parametrize("own", [0, 1, 2, 100, 300])
+@pytest.mark.parametrize("need", [1, 300, 508])
+def test_evict_with_a_full_list(count, own, need):
+    """The bin of the threshold holds as many keys as are ranked directly, all but `own` of them in the first of the row's
+    two CTAs: places at the end of the list."""
+    n, split, budget = 5000, 2560, 700
+    g = gen(count * 7 + own)
+    at = torch.cat([torch.randperm(split, generator=g, device="cuda")[:count - own],
+                    split + torch.randperm(n - split, generator=g, device="cuda")[:own]])
+    score = torch.full((n,), 0.125, device="cuda")
+    free = torch.ones(n, dtype=torch.bool, device="cuda")
+    free[at] = False
+    rest = torch.nonzero(free).view(-1)
+    score[rest[torch.randperm(len(rest), generator=g, device="cuda")[:budget - need]]] = 8.0
+    score[at] = 1 + torch.randint(0, 1000, (count,), generator=g, device="cuda") / 4096     # one bin, some of them equal
+    score = score.view(1, 1, n)
+    cache = LQ.Bf16Cache(bf16(g, 1, 1, n, 64), bf16(g, 1, 1, n, 64), 1)
+    pos = torch.arange(n, device="cuda", dtype=torch.int32).view(1, 1, n)
+    want = evict_reference(cache.k.cpu(), cache.v.cpu(), score.cpu(), pos.cpu(), [n], torch.tensor([n]), budget, 0, 0)
+    so, po, lo = LQ.bf16_evict(cache, score, pos, i32([n]), i32([n]), n, budget, n_sink=0, n_recent=0)
+    assert lo.tolist() == [budget]
+    assert torch.equal(so[..., :budget].cpu(), want[2][..., :budget]) and torch.equal(po[..., :budget].cpu(), want[3][..., :budget])
+    assert torch.equal(cache.k.cpu().view(torch.int16), want[0].view(torch.int16))
+    assert torch.equal(cache.v.cpu().view(torch.int16), want[1].view(torch.int16))
