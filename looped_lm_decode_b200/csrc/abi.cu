@@ -329,13 +329,13 @@ static loopvq_status check_ws(const void *workspace, size_t given, size_t need) 
 }
 
 size_t loopvq_bf16_shared_workspace_bytes(const loopvq_bf16_cache *c, int rows, int max_len) {
-    if (check_bf16(c) != LOOPVQ_OK || rows < 0 || max_len < 0 || max_len > c->Nmax || !rows_fit(rows, c->Hq / c->Hkv))
+    if (check_bf16(c) != LOOPVQ_OK || rows <= 0 || max_len < 0 || max_len > c->Nmax || !rows_fit(rows, c->Hq / c->Hkv))
         return 0;
     return loopvq::shared_ws_bytes(c->Hkv, c->Hq, c->D, rows, max_len, false);
 }
 
 size_t loopvq_shared_workspace_bytes(const loopvq_cache *cc, int rows, int max_len) {
-    if (check_shape(cc) != LOOPVQ_OK || rows < 0 || max_len < 0 || max_len > cc->Nmax || !rows_fit(rows, cc->Hq / cc->Hkv))
+    if (check_shape(cc) != LOOPVQ_OK || rows <= 0 || max_len < 0 || max_len > cc->Nmax || !rows_fit(rows, cc->Hq / cc->Hkv))
         return 0;
     return loopvq::shared_ws_bytes(cc->Hkv, cc->Hq, cc->D, rows, max_len, true);
 }

@@ -440,8 +440,6 @@ def bf16_shared_attn(cache: Bf16Cache, seq: int, q: torch.Tensor, lens: torch.Te
     own, merged in, or None.  lens, starts int32 [B].  Returns (out fp32 [rows][Hq][D], lse fp32 [rows][Hq])."""
     dev = _need_current(cache.k.device)
     rows, oo, ol, out, lse = _shared_args(cache, q, starts, lens, other, out, lse, dev)
-    if rows == 0:
-        return out, lse
     L, ref = lib(), cache.ref()
     workspace, ws, n = _workspace(workspace, _ws_size(L.loopvq_bf16_shared_workspace_bytes, ref, "bf16", cache.B, cache.Hkv, cache.Hq,
                                              cache.D, cache.Nmax, rows, max_len), q)
@@ -457,8 +455,6 @@ def shared_attn(cache: Cache, layer: int, t: int, seq: int, q: torch.Tensor, len
     """bf16_shared_attn over loop step t of one sequence of a coded cache."""
     dev = _need_current(cache.idx.device)
     rows, oo, ol, out, lse = _shared_args(cache, q, starts, lens, other, out, lse, dev)
-    if rows == 0:
-        return out, lse
     L, ref = lib(), cache.ref()
     workspace, ws, n = _workspace(workspace, _ws_size(L.loopvq_shared_workspace_bytes, ref, "coded", cache.B, cache.Hkv, cache.Hq,
                                              cache.D, cache.Nmax, rows, max_len), q)
