@@ -247,7 +247,8 @@ size_t loopvq_shared_workspace_bytes(const loopvq_cache *cache, int rows, int ma
  * other_out  fp32 [rows][Hq][D] and other_lse fp32 [rows][Hq]: the other part,
  *            or both NULL; a row with other_lse = -inf has no other tokens, and one
  *            with NaN (of a call that gave up waiting) becomes NaN.  out may be
- *            other_out; lse may not overlap other_lse.
+ *            other_out itself; otherwise out, lse and the workspace overlap neither
+ *            an input nor one another (refused).
  * out        fp32 [rows][Hq][D]; lse fp32 [rows][Hq], may be NULL.  No tokens at
  *            all: zeros and -inf.
  * workspace  of at least loopvq_bf16_shared_workspace_bytes(cache, rows, max_len)
@@ -292,7 +293,8 @@ size_t loopvq_bf16_scored_workspace_bytes(const loopvq_bf16_cache *cache, int ma
  *
  * other_out  fp32 [B][Hq][D] and other_lse fp32 [B][Hq]: the other part, or
  *            both NULL; a row with other_lse = -inf has no other tokens.  out may
- *            be other_out; lse may not overlap other_lse.
+ *            be other_out itself; otherwise outputs and workspace overlap neither an
+ *            input nor one another (refused).
  * score_in   fp32 [B][Hkv][Nmax], or NULL for zeros.
  * score_out  fp32 [B][Hkv][Nmax]: score_in itself, or memory apart from it;
  *            elements of other tokens stay as they are.
@@ -330,9 +332,10 @@ size_t loopvq_bf16_evict_workspace_bytes(const loopvq_bf16_cache *cache, int max
  *           each slot's token; lens_in int32 [B], clamped to [0, max_len];
  *           next_pos int32 [B], the position of the sequence's next token.
  * budget    >= 1, n_sink + n_recent <= budget (both >= 0).
- * score_out, pos_out, lens_out: the arrays after the eviction: the inputs
- *           themselves, or memory apart from them.  Written for slots
- *           n < min(len_b, budget) = lens_out_b only.
+ * score_out, pos_out, lens_out: the arrays after the eviction, each its own
+ *           input (score_in, pos_in, lens_in) or memory apart from every array of
+ *           the call (anything else is refused, lens_out = next_pos too).  Written
+ *           for slots n < min(len_b, budget) = lens_out_b only.
  * workspace of at least loopvq_bf16_evict_workspace_bytes bytes, 16-byte aligned.
  */
 loopvq_status loopvq_bf16_evict(const loopvq_bf16_cache *cache, const float *score_in, const int32_t *pos_in,

@@ -69,6 +69,34 @@ loopvq_status check_ptr(const void *p, const char *name) {
         if (_s != LOOPVQ_OK) return _s;        \
     } while (0)
 
+// Whether [a, a + na) and [b, b + nb) bytes share memory.
+bool overlaps(const void *a, size_t na, const void *b, size_t nb) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return x < y + nb && y < x + na;
+}
+
+// What a call writes: apart from its inputs (but for an output that may be the input `self` itself) and from the rest of
+// what it writes.  The kernels' CTAs read inputs while others write.
+struct Span {
+    const void *p;               // null: not given
+    size_t bytes;
+    const char *name;
+    const void *self = nullptr;
+};
+template <size_t O, size_t I>
+loopvq_status check_apart(const Span (&outs)[O], const Span (&ins)[I]) {
+    for (size_t i = 0; i < O; ++i) {
+        if (!outs[i].p) continue;
+        for (const Span &in : ins)
+            if (in.p && !(in.p == outs[i].p && in.p == outs[i].self) && overlaps(outs[i].p, outs[i].bytes, in.p, in.bytes))
+                return fail(LOOPVQ_ERR_INVALID_ARG, "%s overlaps %s", outs[i].name, in.name);
+        for (size_t j = 0; j < i; ++j)
+            if (outs[j].p && overlaps(outs[i].p, outs[i].bytes, outs[j].p, outs[j].bytes))
+                return fail(LOOPVQ_ERR_INVALID_ARG, "%s overlaps %s", outs[i].name, outs[j].name);
+    }
+    return LOOPVQ_OK;
+}
+
 }  // namespace
 
 namespace loopvq {
@@ -261,19 +289,6 @@ loopvq_status loopvq_bf16_decode_attn(const loopvq_bf16_cache *c, const uint16_t
     return LOOPVQ_OK;
 }
 
-// Whether [a, a + na) and [b, b + nb) bytes share memory.
-static bool overlaps(const void *a, size_t na, const void *b, size_t nb) {
-    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-    return x < y + nb && y < x + na;
-}
-
-// An output that is the input itself or memory apart from it.
-static loopvq_status check_same_or_apart(const void *in, const void *out, size_t bytes, const char *name) {
-    if (in != out && overlaps(in, bytes, out, bytes))
-        return fail(LOOPVQ_ERR_INVALID_ARG, "%s overlaps its input without being it", name);
-    return LOOPVQ_OK;
-}
-
 static loopvq_status check_word_ptr(const void *p, const char *name) {
     if (!p) return fail(LOOPVQ_ERR_INVALID_ARG, "%s is NULL", name);
     if (reinterpret_cast<uintptr_t>(p) & 3u) return fail(LOOPVQ_ERR_INVALID_ARG, "%s not 4-byte aligned", name);
@@ -311,13 +326,17 @@ static loopvq_status check_shared(int B, int Hkv, int Hq, int D, int Nmax, int s
     if (Hkv > 65535 || !rows_fit(rows, Hq / Hkv))
         return fail(LOOPVQ_ERR_UNSUPPORTED, "Hkv=%d or rows * Hq / Hkv = %lld too large", Hkv,
                     (long long)rows * (Hq / Hkv));
-    const size_t n = (size_t)rows * Hq;
-    if (other_out) {
-        LQ_TRY(check_same_or_apart(other_out, out, n * D * sizeof(float), "out"));
-        if (lse && overlaps(lse, n * sizeof(float), other_lse, n * sizeof(float)))
-            return fail(LOOPVQ_ERR_INVALID_ARG, "lse overlaps other_lse");
-    }
     return LOOPVQ_OK;
+}
+
+static loopvq_status check_shared_memory(int B, int Hq, int D, const uint16_t *q, int rows, const int32_t *starts,
+                                         const int32_t *lens, const float *other_out, const float *other_lse, float *out,
+                                         float *lse, const void *workspace, size_t need) {
+    const size_t n = (size_t)rows * Hq * 4, b = (size_t)B * 4;
+    const Span outs[] = {{out, n * D, "out", other_out}, {lse, n, "lse"}, {need ? workspace : nullptr, need, "workspace"}};
+    const Span ins[] = {{q, n * D / 2, "q"}, {other_out, n * D, "other_out"}, {other_lse, n, "other_lse"}, {starts, b, "starts"},
+                        {lens, b, "lens"}};
+    return check_apart(outs, ins);
 }
 
 static loopvq_status check_ws(const void *workspace, size_t given, size_t need) {
@@ -351,7 +370,9 @@ loopvq_status loopvq_bf16_shared_attn(const loopvq_bf16_cache *c, int seq, const
     if ((int64_t)c->Hkv * c->Nmax + 128 > INT32_MAX)
         return fail(LOOPVQ_ERR_UNSUPPORTED, "Hkv * Nmax = %lld exceeds 2^31", (long long)c->Hkv * c->Nmax);
     if (rows == 0) return LOOPVQ_OK;
-    LQ_TRY(check_ws(workspace, ws_bytes, loopvq::shared_ws_bytes(c->Hkv, c->Hq, c->D, rows, max_len, false)));
+    const size_t need = loopvq::shared_ws_bytes(c->Hkv, c->Hq, c->D, rows, max_len, false);
+    LQ_TRY(check_ws(workspace, ws_bytes, need));
+    LQ_TRY(check_shared_memory(c->B, c->Hq, c->D, q, rows, starts, lens, other_out, other_lse, out, lse, workspace, need));
     cudaError_t e = loopvq::launch_bf16_shared(*c, seq, q, rows, starts, lens, max_len, scale, {other_out, other_lse},
                                                out, lse, workspace, (cudaStream_t)stream);
     if (e != cudaSuccess) return cuda_fail(e, "loopvq_bf16_shared_attn");
@@ -372,7 +393,9 @@ loopvq_status loopvq_shared_attn(const loopvq_cache *cc, int layer, int t, int s
     LQ_TRY(check_shared(cc->B, cc->Hkv, cc->Hq, cc->D, cc->Nmax, seq, q, rows, starts, lens, max_len, &scale,
                         other_out, other_lse, out, lse));
     if (rows == 0) return LOOPVQ_OK;
-    LQ_TRY(check_ws(workspace, ws_bytes, loopvq::shared_ws_bytes(cc->Hkv, cc->Hq, cc->D, rows, max_len, true)));
+    const size_t need = loopvq::shared_ws_bytes(cc->Hkv, cc->Hq, cc->D, rows, max_len, true);
+    LQ_TRY(check_ws(workspace, ws_bytes, need));
+    LQ_TRY(check_shared_memory(cc->B, cc->Hq, cc->D, q, rows, starts, lens, other_out, other_lse, out, lse, workspace, need));
     cudaError_t e = loopvq::launch_shared(*cc, layer, t, seq, q, rows, starts, lens, max_len, scale,
                                           {other_out, other_lse}, out, lse, workspace, (cudaStream_t)stream);
     if (e != cudaSuccess) return cuda_fail(e, "loopvq_shared_attn");
@@ -403,16 +426,16 @@ loopvq_status loopvq_bf16_decode_attn_scored(const loopvq_bf16_cache *c, const u
     if (!std::isfinite(scale)) return fail(LOOPVQ_ERR_INVALID_ARG, "scale is not finite");
     if (scale <= 0.f) scale = 1.0f / std::sqrt((float)c->D);
     if (c->B > 65535 || c->Hkv > 65535) return fail(LOOPVQ_ERR_UNSUPPORTED, "B or Hkv exceeds 65535");
-    const size_t rows = (size_t)c->B * c->Hq;
-    if (other_out)
-        LQ_TRY(check_same_or_apart(other_out, out, rows * c->D * sizeof(float), "out"));
-    if (lse && other_lse && overlaps(lse, rows * sizeof(float), other_lse, rows * sizeof(float)))
-        return fail(LOOPVQ_ERR_INVALID_ARG, "lse overlaps other_lse");
-    if (score_in)
-        LQ_TRY(check_same_or_apart(score_in, score_out, (size_t)c->B * c->Hkv * c->Nmax * sizeof(float), "score_out"));
     const loopvq::DecodePlan plan = loopvq::plan_bf16(*c, max_len);
     if (plan.nsplit > 65535) return fail(LOOPVQ_ERR_UNSUPPORTED, "too many splits");
-    LQ_TRY(check_ws(workspace, ws_bytes, loopvq::plan_scored(*c, max_len).ws_bytes));
+    const size_t need = loopvq::plan_scored(*c, max_len).ws_bytes;
+    LQ_TRY(check_ws(workspace, ws_bytes, need));
+    const size_t n = (size_t)c->B * c->Hq * 4, words = (size_t)c->B * c->Hkv * c->Nmax * 4, b = (size_t)c->B * 4;
+    const Span outs[] = {{out, n * c->D, "out", other_out}, {lse, n, "lse"}, {score_out, words, "score_out", score_in},
+                         {need ? workspace : nullptr, need, "workspace"}};
+    const Span ins[] = {{q, n * c->D / 2, "q"}, {other_out, n * c->D, "other_out"}, {other_lse, n, "other_lse"},
+                        {score_in, words, "score_in"}, {starts, b, "starts"}, {lens, b, "lens"}};
+    LQ_TRY(check_apart(outs, ins));
     const loopvq::Bf16Scored sc{other_out, other_lse, score_in, score_out};
     cudaError_t e = loopvq::launch_bf16_decode(*c, plan, q, starts, lens, max_len, scale, out, lse, workspace,
                                                (cudaStream_t)stream, &sc);
@@ -447,10 +470,15 @@ loopvq_status loopvq_bf16_evict(const loopvq_bf16_cache *c, const float *score_i
     if ((int64_t)c->B * c->Hkv > 65535)
         return fail(LOOPVQ_ERR_UNSUPPORTED, "B * Hkv = %lld exceeds 65535", (long long)c->B * c->Hkv);
     const size_t words = (size_t)c->B * c->Hkv * c->Nmax * 4;
-    LQ_TRY(check_same_or_apart(score_in, score_out, words, "score_out"));
-    LQ_TRY(check_same_or_apart(pos_in, pos_out, words, "pos_out"));
-    LQ_TRY(check_same_or_apart(lens_in, lens_out, (size_t)c->B * 4, "lens_out"));
-    LQ_TRY(check_ws(workspace, ws_bytes, loopvq::evict_ws_bytes(c->B, c->Hkv, max_len, budget)));
+    const size_t need = loopvq::evict_ws_bytes(c->B, c->Hkv, max_len, budget), b = (size_t)c->B * 4;
+    LQ_TRY(check_ws(workspace, ws_bytes, need));
+    const Span outs[] = {{score_out, words, "score_out", score_in}, {pos_out, words, "pos_out", pos_in},
+                         {lens_out, b, "lens_out", lens_in}, {need ? workspace : nullptr, need, "workspace"}};
+    // (one array as lens_in, next_pos and lens_out: every head has read it before it is written in place)
+    const bool one = next_pos == lens_in && lens_out == lens_in;
+    const Span ins[] = {{score_in, words, "score_in"}, {pos_in, words, "pos_in"}, {lens_in, b, "lens_in"},
+                        {one ? nullptr : next_pos, b, "next_pos"}};
+    LQ_TRY(check_apart(outs, ins));
     loopvq::EvictArgs a{};
     a.k = const_cast<uint16_t *>(c->k);
     a.v = const_cast<uint16_t *>(c->v);

@@ -50,3 +50,18 @@ def test_evict_with_a_full_list(count, own, need):
     assert torch.equal(so[..., :budget].cpu(), want[2][..., :budget]) and torch.equal(po[..., :budget].cpu(), want[3][..., :budget])
     assert torch.equal(cache.k.cpu().view(torch.int16), want[0].view(torch.int16))
     assert torch.equal(cache.v.cpu().view(torch.int16), want[1].view(torch.int16))
+
+
+@pytest.mark.parametrize("hkv", [3, 16, 17])
+def test_evict_with_one_array_of_lengths_and_positions(hkv):
+    """The next position is the length, in one array that the call shortens."""
+    n, budget, b = 900, 800, 6
+    g = gen(hkv)
+    cache = LQ.Bf16Cache(bf16(g, b, hkv, n, 64), bf16(g, b, hkv, n, 64), hkv)
+    score = torch.rand(b, hkv, n, generator=g, device="cuda")
+    pos = torch.arange(n, device="cuda", dtype=torch.int32).expand(b, hkv, n).contiguous()
+    lens = i32([900, 850, 801, 800, 12, 0])
+    want = evict_reference(cache.k.cpu(), cache.v.cpu(), score.cpu(), pos.cpu(), lens.tolist(), lens.cpu(), budget, 8, 64)
+    LQ.bf16_evict(cache, score, pos, lens, lens, n, budget)
+    assert lens.tolist() == want[4] and torch.equal(cache.k.cpu().view(torch.int16), want[0].view(torch.int16))
+    assert torch.equal(pos.cpu()[..., :12], want[3][..., :12])
