@@ -374,15 +374,19 @@ def _on_stream(stream, *tensors):
 _sizes = {}
 
 
-def _ws_size(fn, ref, *key):
+def _ws_size(fn, ref, key):
     """A workspace size, which goes by the shapes alone, from the library the first time (a call of its own costs as much
-    as a kernel launch's host side)."""
+    as a kernel launch's host side).  The library also answers 0 for what it refuses, and the key holds shapes, not all that
+    it looks at: a size is kept by _keep_size, after a call that it took."""
     n = _sizes.get(key)
-    if n is None:
+    return fn(ref, *key[6:]) if n is None else n
+
+
+def _keep_size(key, need: int):
+    if key not in _sizes:
         if len(_sizes) >= 4096:
             _sizes.clear()
-        n = _sizes[key] = fn(ref, *key[6:])
-    return n
+        _sizes[key] = need
 
 
 def _workspace(workspace, need: int, like: torch.Tensor):
@@ -441,11 +445,13 @@ def bf16_shared_attn(cache: Bf16Cache, seq: int, q: torch.Tensor, lens: torch.Te
     dev = _need_current(cache.k.device)
     rows, oo, ol, out, lse = _shared_args(cache, q, starts, lens, other, out, lse, dev)
     L, ref = lib(), cache.ref()
-    workspace, ws, n = _workspace(workspace, _ws_size(L.loopvq_bf16_shared_workspace_bytes, ref, "bf16", cache.B, cache.Hkv, cache.Hq,
-                                             cache.D, cache.Nmax, rows, max_len), q)
+    key = ("bf16", cache.B, cache.Hkv, cache.Hq, cache.D, cache.Nmax, rows, max_len)
+    need = _ws_size(L.loopvq_bf16_shared_workspace_bytes, ref, key)
+    workspace, ws, n = _workspace(workspace, need, q)
     _check(L.loopvq_bf16_shared_attn(ref, seq, q.data_ptr(), rows, _ptr(starts), lens.data_ptr(), max_len, scale,
                                      _ptr(oo), _ptr(ol), out.data_ptr(), lse.data_ptr(), ws, n,
                                      _stream(stream)))
+    _keep_size(key, need)
     _on_stream(stream, out, lse, workspace)
     return out, lse
 
@@ -456,11 +462,13 @@ def shared_attn(cache: Cache, layer: int, t: int, seq: int, q: torch.Tensor, len
     dev = _need_current(cache.idx.device)
     rows, oo, ol, out, lse = _shared_args(cache, q, starts, lens, other, out, lse, dev)
     L, ref = lib(), cache.ref()
-    workspace, ws, n = _workspace(workspace, _ws_size(L.loopvq_shared_workspace_bytes, ref, "coded", cache.B, cache.Hkv, cache.Hq,
-                                             cache.D, cache.Nmax, rows, max_len), q)
+    key = ("coded", cache.B, cache.Hkv, cache.Hq, cache.D, cache.Nmax, rows, max_len)
+    need = _ws_size(L.loopvq_shared_workspace_bytes, ref, key)
+    workspace, ws, n = _workspace(workspace, need, q)
     _check(L.loopvq_shared_attn(ref, layer, t, seq, q.data_ptr(), rows, _ptr(starts), lens.data_ptr(), max_len, scale,
                                 _ptr(oo), _ptr(ol), out.data_ptr(), lse.data_ptr(), ws, n,
                                 _stream(stream)))
+    _keep_size(key, need)
     _on_stream(stream, out, lse, workspace)
     return out, lse
 
@@ -491,11 +499,13 @@ def bf16_decode_attn_scored(cache: Bf16Cache, q: torch.Tensor, lens: torch.Tenso
     oo, ol = _need_other(other, B, Hq, D, dev)
     out, lse = _result(out, "out", (B, Hq, D), q), _result(lse, "lse", (B, Hq), q)
     L, ref = lib(), cache.ref()
-    workspace, ws, n = _workspace(workspace, _ws_size(L.loopvq_bf16_scored_workspace_bytes, ref, "scored", B, cache.Hkv, Hq, D,
-                                             cache.Nmax, max_len), q)
+    key = ("scored", B, cache.Hkv, Hq, D, cache.Nmax, max_len)
+    need = _ws_size(L.loopvq_bf16_scored_workspace_bytes, ref, key)
+    workspace, ws, n = _workspace(workspace, need, q)
     _check(L.loopvq_bf16_decode_attn_scored(ref, q.data_ptr(), _ptr(starts), lens.data_ptr(), max_len, scale, _ptr(oo),
                                             _ptr(ol), _ptr(score), score_out.data_ptr(), out.data_ptr(),
                                             lse.data_ptr(), ws, n, _stream(stream)))
+    _keep_size(key, need)
     _on_stream(stream, out, lse, workspace)
     return out, lse, score_out
 
@@ -522,11 +532,13 @@ def bf16_evict(cache: Bf16Cache, score: torch.Tensor, pos: torch.Tensor, lens: t
     for t, name in ((lens, "lens"), (next_pos, "next_pos"), (lens_out, "lens_out")):
         _need(t, name, (B,), _I32, dev)
     L, ref = lib(), cache.ref()
-    workspace, ws, n = _workspace(workspace, _ws_size(L.loopvq_bf16_evict_workspace_bytes, ref, "evict", B, H, cache.Hq, cache.D, N,
-                                             max_len, budget), lens)
+    key = ("evict", B, H, cache.Hq, cache.D, N, max_len, budget)
+    need = _ws_size(L.loopvq_bf16_evict_workspace_bytes, ref, key)
+    workspace, ws, n = _workspace(workspace, need, lens)
     _check(L.loopvq_bf16_evict(ref, score.data_ptr(), pos.data_ptr(), lens.data_ptr(), next_pos.data_ptr(), max_len,
                                budget, n_sink, n_recent, score_out.data_ptr(), pos_out.data_ptr(),
                                lens_out.data_ptr(), ws, n, _stream(stream)))
+    _keep_size(key, need)
     _on_stream(stream, workspace)
     return score_out, pos_out, lens_out
 

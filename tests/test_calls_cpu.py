@@ -5,7 +5,10 @@ import subprocess
 import sys
 
 import pytest
+import torch
 
+import looped_lm_decode_b200 as LQ
+import looped_lm_decode_b200.loopvq as binding
 from tests.test_operators_cpu import A, B_, Cc, D_, INVALID, P, WORKSPACE, coded, evict, message, scored, shared
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
@@ -65,3 +68,76 @@ def test_evict_takes_one_array_of_lengths_and_positions():
     assert evict(li=one, nx=one, lo=one, ws=None) == WORKSPACE
     assert evict(li=one, nx=one, lo=P(0x70000004), ws=None) == WORKSPACE
     assert evict(li=one, nx=one, lo=P(0x70000004)) == INVALID
+
+
+# ------------------------------------------------------------------ the binding's own memory
+
+class OnHost:
+    """The binding's calls with host tensors: the GPU check passes and the launch is a stub that takes what the library's
+    checks would take (a cache at an odd address, or of a code width that is not built, is refused)."""
+
+    def __init__(self, monkeypatch):
+        self.sizes = []
+        real = LQ.lib()
+
+        class Lib:
+            def __getattr__(_, name):
+                fn = getattr(real, name)
+                if name in ("loopvq_bf16_shared_attn", "loopvq_shared_attn", "loopvq_bf16_decode_attn_scored", "loopvq_bf16_evict"):
+                    def call(desc, *args):
+                        self.sizes.append(args[-2])
+                        x = desc._obj
+                        return 1 if (getattr(x, "k", 0) or 0) % 16 or getattr(x, "c", 4) not in (4, 8, 16, 32) else 0
+                    return call
+                return fn
+
+        monkeypatch.setattr(binding, "lib", lambda: Lib())
+        monkeypatch.setattr(binding, "_need_current", lambda device: device)
+        monkeypatch.setattr(binding, "_stream", lambda stream: None)
+        monkeypatch.setattr(binding, "_sizes", {})
+
+
+def aligned(n, off=0):
+    """n bf16 elements at an address that is a multiple of 16, or two bytes behind one."""
+    x = torch.zeros(n + 16, dtype=torch.bfloat16)
+    at = (-x.data_ptr() // 2) % 8 + off
+    return x[at:at + n]
+
+
+def odd_and_right(hkv, n, d, hq):
+    make = lambda off: LQ.Bf16Cache(aligned(hkv * n * d, off).view(1, hkv, n, d), aligned(hkv * n * d).view(1, hkv, n, d), hq)  # noqa: E731
+    return make(1), make(0)
+
+
+@pytest.mark.parametrize("op", ["shared", "scored", "evict"])
+def test_a_refused_cache_leaves_no_size_behind(monkeypatch, op):
+    """The library answers a size of 0 for a cache that it refuses; a right call of the same shape gets its own."""
+    host = OnHost(monkeypatch)
+    odd, right = odd_and_right(2, 32768, 64, 2)
+    q, lens, score = torch.zeros(1, 2, 64, dtype=torch.bfloat16), torch.zeros(1, dtype=torch.int32), torch.zeros(1, 2, 32768)
+    call = dict(shared=lambda c: LQ.bf16_shared_attn(c, 0, q, lens, 32768),
+                scored=lambda c: LQ.bf16_decode_attn_scored(c, q, lens, 32768, score),
+                evict=lambda c: LQ.bf16_evict(c, score, score.int(), lens, lens, 32768, 100, 4, 8))[op]
+    with pytest.raises(LQ.LoopVQError):
+        call(odd)
+    call(right)
+    call(right)                                                      # from what was kept
+    want = dict(shared=LQ.bf16_shared_workspace_bytes(right, 1, 32768), scored=LQ.bf16_scored_workspace_bytes(right, 32768),
+                evict=LQ.bf16_evict_workspace_bytes(right, 32768, 100))[op]
+    assert want > 0 and host.sizes == [0, want, want]
+
+
+def test_a_refused_coded_cache_leaves_no_size_behind(monkeypatch):
+    host = OnHost(monkeypatch)
+    q, lens = torch.zeros(3, 2, 64, dtype=torch.bfloat16), torch.zeros(1, dtype=torch.int32)
+
+    def cache(c):
+        x = LQ.Cache(1, 4, 4, 2, 2, 64, c, 256, 1, 32768, alloc=False)
+        x.idx = x.codebook = x.slices = x.rope = torch.zeros(16)
+        return x
+
+    with pytest.raises(LQ.LoopVQError):
+        LQ.shared_attn(cache(6), 0, 0, 0, q, lens, 32768)
+    LQ.shared_attn(cache(4), 0, 0, 0, q, lens, 32768)
+    want = LQ.shared_workspace_bytes(cache(4), 3, 32768)
+    assert want > 0 and host.sizes == [0, want]
