@@ -354,21 +354,35 @@ def _need(t: torch.Tensor, name: str, shape: tuple, dtypes: tuple, device):
                           f"{list(t.shape)} {t.dtype} on {t.device}")
 
 
-def _result(t, name: str, shape: tuple, like: torch.Tensor):
-    """An fp32 output: the caller's, or a new one (torch.empty_strided takes half the time of torch.empty)."""
+def _empty(shape: tuple, strides: tuple, dtype, device, stream):
+    """Memory of a call's own, made on the stream that uses it (the current one or `stream`): what the current stream gave
+    back may still be in use there while another stream's call already writes it.  (torch.empty_strided takes half the time
+    of torch.empty.)"""
+    if stream is None:
+        return torch.empty_strided(shape, strides, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty_strided(shape, strides, dtype=dtype, device=device)
+
+
+def _result(t, name: str, shape: tuple, like: torch.Tensor, stream):
+    """An fp32 output: the caller's, or a new one."""
     if t is None:
         strides = (shape[1] * shape[2], shape[2], 1) if len(shape) == 3 else (shape[1], 1)
-        return torch.empty_strided(shape, strides, dtype=torch.float32, device=like.device)
+        return _empty(shape, strides, torch.float32, like.device, stream)
     _need(t, name, shape, _F32, like.device)
     return t
 
 
-def _on_stream(stream, *tensors):
-    """Memory made on the current stream and used on another is not reused before that stream is done with it."""
+def _on_stream(stream, workspace, *results):
+    """What a call on `stream` uses is not reused before that stream is done with it, and results not before the current
+    stream, where the caller reads them (behind a wait of the caller's), is done either."""
     if stream is not None:
-        for t in tensors:
-            if t is not None:
-                t.record_stream(stream)
+        here = torch.cuda.current_stream()
+        if workspace is not None:
+            workspace.record_stream(stream)
+        for t in results:
+            t.record_stream(stream)
+            t.record_stream(here)
 
 
 _sizes = {}
@@ -389,22 +403,24 @@ def _keep_size(key, need: int):
         _sizes[key] = need
 
 
-def _workspace(workspace, need: int, like: torch.Tensor):
+def _workspace(workspace, need: int, like: torch.Tensor, stream):
     """(tensor, address, bytes); none where the call needs none."""
     if workspace is None:
         if need == 0:
             return None, None, 0
-        workspace = torch.empty_strided((need,), (1,), dtype=torch.uint8, device=like.device)
+        workspace = _empty((need,), (1,), torch.uint8, like.device, stream)
         return workspace, workspace.data_ptr(), need
     if workspace.device != like.device or not workspace.is_contiguous():
         raise LoopVQError(LOOPVQ_ERR_INVALID_ARG, f"workspace must be contiguous memory on {like.device}")
     return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
-def _need_current(device):
-    """The launch goes to the current GPU: memory of another one, or of the host, is refused."""
+def _need_current(device, stream):
+    """The launch goes to the current GPU: memory of another one, or of the host, is refused, and another one's stream."""
     if device.type != "cuda" or device.index != torch._C._cuda_getDevice():
         raise LoopVQError(LOOPVQ_ERR_INVALID_ARG, f"the cache is on {device}, which is not the current GPU")
+    if stream is not None and stream.device != device:
+        raise LoopVQError(LOOPVQ_ERR_INVALID_ARG, f"the stream is of {stream.device}, the cache on {device}")
     return device
 
 
@@ -427,14 +443,14 @@ def shared_workspace_bytes(cache: Cache, rows: int, max_len: int) -> int:
     return lib().loopvq_shared_workspace_bytes(cache.ref(), rows, max_len)
 
 
-def _shared_args(cache, q, starts, lens, other, out, lse, dev):
+def _shared_args(cache, q, starts, lens, other, out, lse, dev, stream):
     rows, Hq, D = q.shape[0], cache.Hq, cache.D
     _need(q, "q", (rows, Hq, D), _Q, dev)
     _need(lens, "lens", (cache.B,), _I32, dev)
     if starts is not None:
         _need(starts, "starts", (cache.B,), _I32, dev)
     oo, ol = _need_other(other, rows, Hq, D, dev)
-    return rows, oo, ol, _result(out, "out", (rows, Hq, D), q), _result(lse, "lse", (rows, Hq), q)
+    return rows, oo, ol, _result(out, "out", (rows, Hq, D), q, stream), _result(lse, "lse", (rows, Hq), q, stream)
 
 
 def bf16_shared_attn(cache: Bf16Cache, seq: int, q: torch.Tensor, lens: torch.Tensor, max_len: int, starts=None,
@@ -442,34 +458,34 @@ def bf16_shared_attn(cache: Bf16Cache, seq: int, q: torch.Tensor, lens: torch.Te
     """Attention of every query token q[r], bf16 [rows][Hq][D], over the tokens starts[seq] <= n < lens[seq] of one
     sequence of the cache (the prefix that a batch shares); other: (out, lse) of the same queries over tokens of their
     own, merged in, or None.  lens, starts int32 [B].  Returns (out fp32 [rows][Hq][D], lse fp32 [rows][Hq])."""
-    dev = _need_current(cache.k.device)
-    rows, oo, ol, out, lse = _shared_args(cache, q, starts, lens, other, out, lse, dev)
+    dev = _need_current(cache.k.device, stream)
+    rows, oo, ol, out, lse = _shared_args(cache, q, starts, lens, other, out, lse, dev, stream)
     L, ref = lib(), cache.ref()
     key = ("bf16", cache.B, cache.Hkv, cache.Hq, cache.D, cache.Nmax, rows, max_len)
     need = _ws_size(L.loopvq_bf16_shared_workspace_bytes, ref, key)
-    workspace, ws, n = _workspace(workspace, need, q)
+    workspace, ws, n = _workspace(workspace, need, q, stream)
     _check(L.loopvq_bf16_shared_attn(ref, seq, q.data_ptr(), rows, _ptr(starts), lens.data_ptr(), max_len, scale,
                                      _ptr(oo), _ptr(ol), out.data_ptr(), lse.data_ptr(), ws, n,
                                      _stream(stream)))
     _keep_size(key, need)
-    _on_stream(stream, out, lse, workspace)
+    _on_stream(stream, workspace, out, lse)
     return out, lse
 
 
 def shared_attn(cache: Cache, layer: int, t: int, seq: int, q: torch.Tensor, lens: torch.Tensor, max_len: int,
                 starts=None, scale: float = 0.0, other=None, out=None, lse=None, workspace=None, stream=None):
     """bf16_shared_attn over loop step t of one sequence of a coded cache."""
-    dev = _need_current(cache.idx.device)
-    rows, oo, ol, out, lse = _shared_args(cache, q, starts, lens, other, out, lse, dev)
+    dev = _need_current(cache.idx.device, stream)
+    rows, oo, ol, out, lse = _shared_args(cache, q, starts, lens, other, out, lse, dev, stream)
     L, ref = lib(), cache.ref()
     key = ("coded", cache.B, cache.Hkv, cache.Hq, cache.D, cache.Nmax, rows, max_len)
     need = _ws_size(L.loopvq_shared_workspace_bytes, ref, key)
-    workspace, ws, n = _workspace(workspace, need, q)
+    workspace, ws, n = _workspace(workspace, need, q, stream)
     _check(L.loopvq_shared_attn(ref, layer, t, seq, q.data_ptr(), rows, _ptr(starts), lens.data_ptr(), max_len, scale,
                                 _ptr(oo), _ptr(ol), out.data_ptr(), lse.data_ptr(), ws, n,
                                 _stream(stream)))
     _keep_size(key, need)
-    _on_stream(stream, out, lse, workspace)
+    _on_stream(stream, workspace, out, lse)
     return out, lse
 
 
@@ -484,7 +500,7 @@ def bf16_decode_attn_scored(cache: Bf16Cache, q: torch.Tensor, lens: torch.Tenso
     score + weights (score_out None: score itself, in place; score None: zeros).  other: (out, lse) of the same
     queries over tokens that are not in this cache, or None; the result and the weights are then those of the
     joint softmax.  Returns (out, lse, score_out)."""
-    B, Hq, D, dev = cache.B, cache.Hq, cache.D, _need_current(cache.k.device)
+    B, Hq, D, dev = cache.B, cache.Hq, cache.D, _need_current(cache.k.device, stream)
     if score_out is None:
         score_out = score
     if score_out is None:
@@ -497,16 +513,16 @@ def bf16_decode_attn_scored(cache: Bf16Cache, q: torch.Tensor, lens: torch.Tenso
         if t is not None:
             _need(t, name, (B, cache.Hkv, cache.Nmax), _F32, dev)
     oo, ol = _need_other(other, B, Hq, D, dev)
-    out, lse = _result(out, "out", (B, Hq, D), q), _result(lse, "lse", (B, Hq), q)
+    out, lse = _result(out, "out", (B, Hq, D), q, stream), _result(lse, "lse", (B, Hq), q, stream)
     L, ref = lib(), cache.ref()
     key = ("scored", B, cache.Hkv, Hq, D, cache.Nmax, max_len)
     need = _ws_size(L.loopvq_bf16_scored_workspace_bytes, ref, key)
-    workspace, ws, n = _workspace(workspace, need, q)
+    workspace, ws, n = _workspace(workspace, need, q, stream)
     _check(L.loopvq_bf16_decode_attn_scored(ref, q.data_ptr(), _ptr(starts), lens.data_ptr(), max_len, scale, _ptr(oo),
                                             _ptr(ol), _ptr(score), score_out.data_ptr(), out.data_ptr(),
                                             lse.data_ptr(), ws, n, _stream(stream)))
     _keep_size(key, need)
-    _on_stream(stream, out, lse, workspace)
+    _on_stream(stream, workspace, out, lse)
     return out, lse, score_out
 
 
@@ -521,7 +537,7 @@ def bf16_evict(cache: Bf16Cache, score: torch.Tensor, pos: torch.Tensor, lens: t
     before next_pos, and the highest scores; kept rows behind the budget move into emptied slots of cache.k and
     cache.v.  score fp32 and pos int32 [B][Hkv][Nmax], lens and next_pos int32 [B]; the outputs default to the
     inputs (in place).  Returns (score_out, pos_out, lens_out)."""
-    B, H, N, dev = cache.B, cache.Hkv, cache.Nmax, _need_current(cache.k.device)
+    B, H, N, dev = cache.B, cache.Hkv, cache.Nmax, _need_current(cache.k.device, stream)
     score_out = score if score_out is None else score_out
     pos_out = pos if pos_out is None else pos_out
     lens_out = lens if lens_out is None else lens_out
@@ -534,7 +550,7 @@ def bf16_evict(cache: Bf16Cache, score: torch.Tensor, pos: torch.Tensor, lens: t
     L, ref = lib(), cache.ref()
     key = ("evict", B, H, cache.Hq, cache.D, N, max_len, budget)
     need = _ws_size(L.loopvq_bf16_evict_workspace_bytes, ref, key)
-    workspace, ws, n = _workspace(workspace, need, lens)
+    workspace, ws, n = _workspace(workspace, need, lens, stream)
     _check(L.loopvq_bf16_evict(ref, score.data_ptr(), pos.data_ptr(), lens.data_ptr(), next_pos.data_ptr(), max_len,
                                budget, n_sink, n_recent, score_out.data_ptr(), pos_out.data_ptr(),
                                lens_out.data_ptr(), ws, n, _stream(stream)))

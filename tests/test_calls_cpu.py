@@ -92,8 +92,9 @@ class OnHost:
                 return fn
 
         monkeypatch.setattr(binding, "lib", lambda: Lib())
-        monkeypatch.setattr(binding, "_need_current", lambda device: device)
+        monkeypatch.setattr(binding, "_need_current", lambda device, stream: device)
         monkeypatch.setattr(binding, "_stream", lambda stream: None)
+        monkeypatch.setattr(binding, "_on_stream", lambda *_: None)
         monkeypatch.setattr(binding, "_sizes", {})
 
 
@@ -141,3 +142,33 @@ def test_a_refused_coded_cache_leaves_no_size_behind(monkeypatch):
     LQ.shared_attn(cache(4), 0, 0, 0, q, lens, 32768)
     want = LQ.shared_workspace_bytes(cache(4), 3, 32768)
     assert want > 0 and host.sizes == [0, want]
+
+
+@pytest.mark.parametrize("stream", [None, "side"])
+def test_own_memory_is_made_on_the_stream_that_uses_it(monkeypatch, stream):
+    """Results and workspaces that the caller leaves to the binding."""
+    OnHost(monkeypatch)
+    current, made = [None], []
+
+    class Use:
+        def __init__(self, s):
+            self.s = s
+
+        def __enter__(self):
+            current.append(self.s)
+
+        def __exit__(self, *_):
+            current.pop()
+
+    real = torch.empty_strided
+    monkeypatch.setattr(torch.cuda, "stream", Use)
+    monkeypatch.setattr(torch, "empty_strided", lambda *a, **k: (made.append(current[-1]), real(*a, **k))[1])
+    _, cache = odd_and_right(2, 32768, 64, 2)
+    q, lens, score = torch.zeros(1, 2, 64, dtype=torch.bfloat16), torch.zeros(1, dtype=torch.int32), torch.zeros(1, 2, 32768)
+    coded = LQ.Cache(1, 4, 4, 2, 2, 64, 4, 256, 1, 32768, alloc=False)
+    coded.idx = coded.codebook = coded.slices = coded.rope = torch.zeros(16)
+    LQ.bf16_shared_attn(cache, 0, q, lens, 32768, stream=stream)
+    LQ.shared_attn(coded, 0, 0, 0, q, lens, 32768, stream=stream)
+    LQ.bf16_decode_attn_scored(cache, q, lens, 32768, score, stream=stream)
+    LQ.bf16_evict(cache, score, score.int(), lens, lens, 32768, 100, 4, 8, stream=stream)
+    assert made == [stream] * 10                                     # three results and workspaces, and evict's workspace

@@ -65,3 +65,63 @@ def test_evict_with_one_array_of_lengths_and_positions(hkv):
     LQ.bf16_evict(cache, score, pos, lens, lens, n, budget)
     assert lens.tolist() == want[4] and torch.equal(cache.k.cpu().view(torch.int16), want[0].view(torch.int16))
     assert torch.equal(pos.cpu()[..., :12], want[3][..., :12])
+
+
+# ------------------------------------------------------------------ streams
+
+def coded_cache(g, hkv, hq, d, c, tc, entries, nmax, layers=1, loops=4, seqs=1):
+    cache = LQ.Cache(layers, loops, tc, hkv, hq, d, c, entries, seqs, nmax)
+    cache.codebook.copy_(bf16(g, cache.codebook.numel()).view(torch.int16))
+    LQ.prepare(cache)
+    cache.idx.copy_(torch.randint(-2 ** 31, 2 ** 31, cache.idx.shape, generator=g, device="cuda", dtype=torch.int64).int())
+    return cache
+
+
+def test_default_memory_on_two_streams():
+    """Calls that bring no memory of their own, in turn on the current stream and another without a wait between: each
+    gives what it gives alone."""
+    g = gen(30)
+    n, hkv, hq, rows = 20000, 4, 16, 48
+    cache = LQ.Bf16Cache(bf16(g, 2, hkv, n, 128), bf16(g, 2, hkv, n, 128), hq)
+    coded = coded_cache(g, hkv, hq, 128, 8, 4, 256, n)
+    q, qb, lens = bf16(g, rows, hq, 128), bf16(g, 2, hq, 128), i32([n, n - 7])
+    score = torch.rand(2, hkv, n, generator=g, device="cuda")
+    outs = [torch.zeros_like(score) for _ in range(16)]
+    calls = (lambda s, i: LQ.bf16_shared_attn(cache, 0, q, lens, n, stream=s),
+             lambda s, i: LQ.shared_attn(coded, 0, 1, 0, q, lens[:1], n, stream=s),
+             lambda s, i: LQ.bf16_decode_attn_scored(cache, qb, lens, n, score, score_out=outs[i], stream=s)[:2])
+    side = torch.cuda.Stream()
+    for call in calls:
+        want = [x.clone() for x in call(None, 0)]
+        torch.cuda.synchronize()
+        got = [call(side if i % 2 else None, i) for i in range(16)]
+        torch.cuda.synchronize()
+        LQ.fault_check()
+        assert all(torch.equal(x, y) for r in got for x, y in zip(r, want))
+        del got
+    k, v, pos = cache.k.clone(), cache.v.clone(), torch.arange(n, device="cuda", dtype=torch.int32).expand(2, hkv, n).contiguous()
+    both = [LQ.Bf16Cache(k.clone(), v.clone(), hq) for _ in range(2)]
+    res = [[torch.zeros_like(score), torch.zeros_like(pos), torch.zeros_like(lens)] for _ in range(2)]
+    torch.cuda.synchronize()
+    for i in range(8):                                               # workspaces of 2 x 4 x 12001 words
+        x = res[i % 2]
+        LQ.bf16_evict(both[i % 2], score, pos, lens, lens, n, 6000, score_out=x[0], pos_out=x[1], lens_out=x[2],
+                      stream=side if i % 2 else None)
+        if i < 2:                                                    # (kept rows move on from call to call)
+            torch.cuda.synchronize()
+            first = [y.clone() for y in res[i]] + [both[i].k.clone()]
+            keep = first if i == 0 else keep
+            assert all(torch.equal(y, z) for y, z in zip(first, keep))
+    torch.cuda.synchronize()
+    assert all(torch.equal(y, z) for y, z in zip(res[0], res[1])) and torch.equal(both[0].k, both[1].k)
+
+
+def test_a_stream_of_another_gpu_is_refused():
+    class Stream:
+        device, cuda_stream = torch.device("cuda", torch.cuda.current_device() + 1), 0
+
+    g = gen(31)
+    cache = LQ.Bf16Cache(bf16(g, 1, 1, 64, 64), bf16(g, 1, 1, 64, 64), 1)
+    with pytest.raises(LQ.LoopVQError) as e:
+        LQ.bf16_shared_attn(cache, 0, bf16(g, 1, 1, 64), i32([64]), 64, stream=Stream())
+    assert e.value.status == 1
