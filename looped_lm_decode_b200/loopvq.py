@@ -187,6 +187,35 @@ def _stream(stream):
     return stream.cuda_stream
 
 
+def _empty(shape: tuple, strides: tuple, dtype, device, stream):
+    """Memory of a call's own, made on the stream that uses it (the current one or `stream`): what the current stream gave
+    back may still be in use there while another stream's call already writes it.  (torch.empty_strided takes half the time
+    of torch.empty.)"""
+    if stream is None:
+        return torch.empty_strided(shape, strides, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty_strided(shape, strides, dtype=dtype, device=device)
+
+
+def _empty_like(t: torch.Tensor, stream):
+    if stream is None:
+        return torch.empty_like(t)
+    with torch.cuda.stream(stream):
+        return torch.empty_like(t)
+
+
+def _on_stream(stream, workspace, *results):
+    """What a call on `stream` uses is not reused before that stream is done with it, and results not before the current
+    stream, where the caller reads them (behind a wait of the caller's), is done either."""
+    if stream is not None:
+        here = torch.cuda.current_stream()
+        if workspace is not None:
+            workspace.record_stream(stream)
+        for t in results:
+            t.record_stream(stream)
+            t.record_stream(here)
+
+
 class Cache:
     """Shape plus the four device buffers of a coded cache (see include/loopvq.h)."""
 
@@ -252,15 +281,16 @@ def decode_attn(cache: Cache, layer: int, t: int, q: torch.Tensor, lens: torch.T
     B, Hq, D = cache.B, cache.Hq, cache.D
     dev = q.device
     if out is None:
-        out = torch.empty((B, Hq, D), dtype=torch.float32, device=dev)
+        out = _empty((B, Hq, D), (Hq * D, D, 1), torch.float32, dev, stream)
     if lse is None:
-        lse = torch.empty((B, Hq), dtype=torch.float32, device=dev)
+        lse = _empty((B, Hq), (Hq, 1), torch.float32, dev, stream)
     need = decode_workspace_bytes(cache, max_len)
     if workspace is None:
-        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
+        workspace = _empty((max(need, 16),), (1,), torch.uint8, dev, stream)
     _check(lib().loopvq_decode_attn(cache.ref(), layer, t, _ptr(q), _ptr(lens), max_len, scale, _ptr(out),
                                     _ptr(lse), _ptr(workspace), workspace.numel() * workspace.element_size(),
                                     _stream(stream)))
+    _on_stream(stream, workspace, out, lse)
     return out, lse
 
 
@@ -269,11 +299,12 @@ def decode_attn_noalloc(cache: Cache, layer: int, t: int, q: torch.Tensor, lens:
     """decode_attn with the library's built-in scratch array instead of a caller workspace."""
     B, Hq, D = cache.B, cache.Hq, cache.D
     if out is None:
-        out = torch.empty((B, Hq, D), dtype=torch.float32, device=q.device)
+        out = _empty((B, Hq, D), (Hq * D, D, 1), torch.float32, q.device, stream)
     if lse is None:
-        lse = torch.empty((B, Hq), dtype=torch.float32, device=q.device)
+        lse = _empty((B, Hq), (Hq, 1), torch.float32, q.device, stream)
     _check(lib().loopvq_decode_attn_noalloc(cache.ref(), layer, t, _ptr(q), _ptr(lens), max_len, scale, _ptr(out),
                                             _ptr(lse), _stream(stream)))
+    _on_stream(stream, None, out, lse)
     return out, lse
 
 
@@ -283,15 +314,16 @@ def decode_attn_range(cache: Cache, layer: int, t: int, q: torch.Tensor, starts,
     B, Hq, D = cache.B, cache.Hq, cache.D
     dev = q.device
     if out is None:
-        out = torch.empty((B, Hq, D), dtype=torch.float32, device=dev)
+        out = _empty((B, Hq, D), (Hq * D, D, 1), torch.float32, dev, stream)
     if lse is None:
-        lse = torch.empty((B, Hq), dtype=torch.float32, device=dev)
+        lse = _empty((B, Hq), (Hq, 1), torch.float32, dev, stream)
     need = decode_workspace_bytes(cache, max_len)
     if workspace is None:
-        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
+        workspace = _empty((max(need, 16),), (1,), torch.uint8, dev, stream)
     _check(lib().loopvq_decode_attn_range(cache.ref(), layer, t, _ptr(q), _ptr(starts), _ptr(lens), max_len, scale,
                                           _ptr(out), _ptr(lse), _ptr(workspace),
                                           workspace.numel() * workspace.element_size(), _stream(stream)))
+    _on_stream(stream, workspace, out, lse)
     return out, lse
 
 
@@ -321,15 +353,16 @@ def bf16_decode_attn(cache: Bf16Cache, q: torch.Tensor, lens: torch.Tensor, max_
     B, Hq, D = cache.B, cache.Hq, cache.D
     dev = q.device
     if out is None:
-        out = torch.empty((B, Hq, D), dtype=torch.float32, device=dev)
+        out = _empty((B, Hq, D), (Hq * D, D, 1), torch.float32, dev, stream)
     if lse is None:
-        lse = torch.empty((B, Hq), dtype=torch.float32, device=dev)
+        lse = _empty((B, Hq), (Hq, 1), torch.float32, dev, stream)
     need = bf16_decode_workspace_bytes(cache, max_len)
     if workspace is None:
-        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
+        workspace = _empty((max(need, 16),), (1,), torch.uint8, dev, stream)
     _check(lib().loopvq_bf16_decode_attn(cache.ref(), _ptr(q), _ptr(starts), _ptr(lens), max_len, scale, _ptr(out),
                                          _ptr(lse), _ptr(workspace), workspace.numel() * workspace.element_size(),
                                          _stream(stream)))
+    _on_stream(stream, workspace, out, lse)
     return out, lse
 
 
@@ -338,11 +371,12 @@ def merge2(out_a, lse_a, out_b, lse_b, out=None, lse=None, stream=None):
     D = out_a.shape[-1]
     rows = out_a.numel() // D
     if out is None:
-        out = torch.empty_like(out_a)
+        out = _empty_like(out_a, stream)
     if lse is None:
-        lse = torch.empty_like(lse_a)
+        lse = _empty_like(lse_a, stream)
     _check(lib().loopvq_merge2(_ptr(out_a), _ptr(lse_a), _ptr(out_b), _ptr(lse_b), rows, D, _ptr(out), _ptr(lse),
                                _stream(stream)))
+    _on_stream(stream, None, out, lse)
     return out, lse
 
 
@@ -354,16 +388,6 @@ def _need(t: torch.Tensor, name: str, shape: tuple, dtypes: tuple, device):
                           f"{list(t.shape)} {t.dtype} on {t.device}")
 
 
-def _empty(shape: tuple, strides: tuple, dtype, device, stream):
-    """Memory of a call's own, made on the stream that uses it (the current one or `stream`): what the current stream gave
-    back may still be in use there while another stream's call already writes it.  (torch.empty_strided takes half the time
-    of torch.empty.)"""
-    if stream is None:
-        return torch.empty_strided(shape, strides, dtype=dtype, device=device)
-    with torch.cuda.stream(stream):
-        return torch.empty_strided(shape, strides, dtype=dtype, device=device)
-
-
 def _result(t, name: str, shape: tuple, like: torch.Tensor, stream):
     """An fp32 output: the caller's, or a new one."""
     if t is None:
@@ -371,18 +395,6 @@ def _result(t, name: str, shape: tuple, like: torch.Tensor, stream):
         return _empty(shape, strides, torch.float32, like.device, stream)
     _need(t, name, shape, _F32, like.device)
     return t
-
-
-def _on_stream(stream, workspace, *results):
-    """What a call on `stream` uses is not reused before that stream is done with it, and results not before the current
-    stream, where the caller reads them (behind a wait of the caller's), is done either."""
-    if stream is not None:
-        here = torch.cuda.current_stream()
-        if workspace is not None:
-            workspace.record_stream(stream)
-        for t in results:
-            t.record_stream(stream)
-            t.record_stream(here)
 
 
 _sizes = {}
@@ -596,15 +608,16 @@ def tasq_decode_attn(cache: Cache, tasq: Tasq, layer: int, t: int, q, lens, max_
     B, Hq, D = cache.B, cache.Hq, cache.D
     dev = q.device
     if out is None:
-        out = torch.empty((B, Hq, D), dtype=torch.float32, device=dev)
+        out = _empty((B, Hq, D), (Hq * D, D, 1), torch.float32, dev, stream)
     if lse is None:
-        lse = torch.empty((B, Hq), dtype=torch.float32, device=dev)
+        lse = _empty((B, Hq), (Hq, 1), torch.float32, dev, stream)
     need = decode_workspace_bytes(cache, max_len)
     if workspace is None:
-        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
+        workspace = _empty((max(need, 16),), (1,), torch.uint8, dev, stream)
     _check(lib().loopvq_tasq_decode_attn(cache.ref(), tasq.ref(), layer, t, _ptr(q), _ptr(lens), max_len, scale,
                                          _ptr(out), _ptr(lse), _ptr(workspace),
                                          workspace.numel() * workspace.element_size(), _stream(stream)))
+    _on_stream(stream, workspace, out, lse)
     return out, lse
 
 
@@ -649,15 +662,15 @@ def window_decode_attn(win: Window, cache: Cache, layer: int, t: int, q, max_cod
     B, Hq, D = cache.B, cache.Hq, cache.D
     dev = q.device
     if out is None:
-        out = torch.empty((B, Hq, D), dtype=torch.float32, device=dev)
+        out = _empty((B, Hq, D), (Hq * D, D, 1), torch.float32, dev, stream)
     if lse is None:
-        lse = torch.empty((B, Hq), dtype=torch.float32, device=dev)
+        lse = _empty((B, Hq), (Hq, 1), torch.float32, dev, stream)
     if workspace is None:
-        workspace = torch.empty(max(window_workspace_bytes(win, cache, max_coded), 16), dtype=torch.uint8,
-                                device=dev)
+        workspace = _empty((max(window_workspace_bytes(win, cache, max_coded), 16),), (1,), torch.uint8, dev, stream)
     _check(lib().loopvq_window_decode_attn(win.ref(), cache.ref(), layer, t, _ptr(q), max_coded, scale, _ptr(out),
                                            _ptr(lse), _ptr(workspace), workspace.numel() * workspace.element_size(),
                                            _stream(stream)))
+    _on_stream(stream, workspace, out, lse)
     return out, lse
 
 
@@ -668,24 +681,25 @@ def window_append_decode_attn(win: Window, cache: Cache, layer: int, t: int, k_r
     B, Hq, D = cache.B, cache.Hq, cache.D
     dev = q.device
     if out is None:
-        out = torch.empty((B, Hq, D), dtype=torch.float32, device=dev)
+        out = _empty((B, Hq, D), (Hq * D, D, 1), torch.float32, dev, stream)
     if lse is None:
-        lse = torch.empty((B, Hq), dtype=torch.float32, device=dev)
+        lse = _empty((B, Hq), (Hq, 1), torch.float32, dev, stream)
     if workspace is None:
-        workspace = torch.empty(max(window_workspace_bytes(win, cache, max_coded), 16), dtype=torch.uint8,
-                                device=dev)
+        workspace = _empty((max(window_workspace_bytes(win, cache, max_coded), 16),), (1,), torch.uint8, dev, stream)
     _check(lib().loopvq_window_append_decode_attn(win.ref(), cache.ref(), layer, t, _ptr(k_rot), _ptr(k_pre), _ptr(v),
                                                   _ptr(q), max_coded, scale, _ptr(out), _ptr(lse), _ptr(workspace),
                                                   workspace.numel() * workspace.element_size(), _stream(stream)))
+    _on_stream(stream, workspace, out, lse)
     return out, lse
 
 
 def dequant_debug(cache: Cache, layer: int, t: int, kv: int, b: int, tok0: int, ntok: int, apply_rope: bool = False,
                   out=None, stream=None):
     if out is None:
-        out = torch.empty((cache.Hkv, ntok, cache.D), dtype=torch.float32, device="cuda")
+        out = _empty((cache.Hkv, ntok, cache.D), (ntok * cache.D, cache.D, 1), torch.float32, "cuda", stream)
     _check(lib().loopvq_dequant_debug(cache.ref(), layer, t, kv, b, tok0, ntok, int(bool(apply_rope)), _ptr(out),
                                       _stream(stream)))
+    _on_stream(stream, None, out)
     return out
 
 

@@ -172,3 +172,39 @@ def test_own_memory_is_made_on_the_stream_that_uses_it(monkeypatch, stream):
     LQ.bf16_decode_attn_scored(cache, q, lens, 32768, score, stream=stream)
     LQ.bf16_evict(cache, score, score.int(), lens, lens, 32768, 100, 4, 8, stream=stream)
     assert made == [stream] * 10                                     # three results and workspaces, and evict's workspace
+
+
+@pytest.mark.parametrize("stream", [None, "side"])
+def test_own_memory_of_every_decode_call(monkeypatch, stream):
+    """decode_attn and its kin, merge2 and dequant_debug: the launch is a stub, what they make comes from the right stream
+    and is recorded there."""
+    made, recorded = [], []
+    monkeypatch.setattr(binding, "_empty", lambda shape, strides, dtype, device, s: (
+        made.append(s), torch.empty_strided(shape, strides, dtype=dtype, device="cpu"))[1])
+    monkeypatch.setattr(binding, "_empty_like", lambda t, s: (made.append(s), torch.empty_like(t))[1])
+    monkeypatch.setattr(binding, "_on_stream", lambda s, ws, *res: recorded.append((s, ws is not None, len(res))))
+    monkeypatch.setattr(binding, "_stream", lambda s: None)
+    real = LQ.lib()
+
+    class Lib:
+        def __getattr__(_, name):
+            return getattr(real, name) if name.endswith("_bytes") or name.endswith("_elems") else lambda *a: 0
+
+    monkeypatch.setattr(binding, "lib", lambda: Lib())
+    cache = LQ.Cache(1, 4, 4, 2, 2, 64, 4, 256, 1, 512, alloc=False)
+    bf = LQ.Bf16Cache(aligned(2 * 512 * 64).view(1, 2, 512, 64), aligned(2 * 512 * 64).view(1, 2, 512, 64), 2)
+    tasq, win = LQ.Tasq(cache, device="cpu"), LQ.Window(cache, device="cpu")
+    q, lens = torch.zeros(1, 2, 64, dtype=torch.bfloat16), torch.zeros(1, dtype=torch.int32)
+    kv, part = torch.zeros(1, 2, 64, dtype=torch.bfloat16), (torch.zeros(1, 2, 64), torch.zeros(1, 2))
+    on = dict(stream=stream)
+    LQ.decode_attn(cache, 0, 0, q, lens, 512, **on)
+    LQ.decode_attn_noalloc(cache, 0, 0, q, lens, 512, **on)
+    LQ.decode_attn_range(cache, 0, 0, q, None, lens, 512, **on)
+    LQ.bf16_decode_attn(bf, q, lens, 512, **on)
+    LQ.tasq_decode_attn(cache, tasq, 0, 0, q, lens, 512, **on)
+    LQ.window_decode_attn(win, cache, 0, 0, q, 512, **on)
+    LQ.window_append_decode_attn(win, cache, 0, 0, kv, kv, kv, q, 512, **on)
+    LQ.merge2(*part, *part, **on)
+    LQ.dequant_debug(cache, 0, 0, 0, 0, 0, 8, **on)
+    assert made == [stream] * (6 * 3 + 2 + 2 + 1)
+    assert recorded == [(stream, True, 2), (stream, False, 2)] + [(stream, True, 2)] * 5 + [(stream, False, 2), (stream, False, 1)]
