@@ -197,23 +197,22 @@ def _empty(shape: tuple, strides: tuple, dtype, device, stream):
         return torch.empty_strided(shape, strides, dtype=dtype, device=device)
 
 
-def _empty_like(t: torch.Tensor, stream):
+def _new(shape: tuple, strides: tuple, device, stream):
+    """A new fp32 result.  Made on another stream, it is not reused before the current one, where the caller reads it
+    (behind a wait of the caller's), is done with it."""
+    t = _empty(shape, strides, torch.float32, device, stream)
+    if stream is not None:
+        t.record_stream(torch.cuda.current_stream())
+    return t
+
+
+def _new_like(t: torch.Tensor, stream):
     if stream is None:
         return torch.empty_like(t)
     with torch.cuda.stream(stream):
-        return torch.empty_like(t)
-
-
-def _on_stream(stream, workspace, *results):
-    """What a call on `stream` uses is not reused before that stream is done with it, and results not before the current
-    stream, where the caller reads them (behind a wait of the caller's), is done either."""
-    if stream is not None:
-        here = torch.cuda.current_stream()
-        if workspace is not None:
-            workspace.record_stream(stream)
-        for t in results:
-            t.record_stream(stream)
-            t.record_stream(here)
+        t = torch.empty_like(t)
+    t.record_stream(torch.cuda.current_stream())
+    return t
 
 
 class Cache:
@@ -281,16 +280,15 @@ def decode_attn(cache: Cache, layer: int, t: int, q: torch.Tensor, lens: torch.T
     B, Hq, D = cache.B, cache.Hq, cache.D
     dev = q.device
     if out is None:
-        out = _empty((B, Hq, D), (Hq * D, D, 1), torch.float32, dev, stream)
+        out = _new((B, Hq, D), (Hq * D, D, 1), dev, stream)
     if lse is None:
-        lse = _empty((B, Hq), (Hq, 1), torch.float32, dev, stream)
+        lse = _new((B, Hq), (Hq, 1), dev, stream)
     need = decode_workspace_bytes(cache, max_len)
     if workspace is None:
         workspace = _empty((max(need, 16),), (1,), torch.uint8, dev, stream)
     _check(lib().loopvq_decode_attn(cache.ref(), layer, t, _ptr(q), _ptr(lens), max_len, scale, _ptr(out),
                                     _ptr(lse), _ptr(workspace), workspace.numel() * workspace.element_size(),
                                     _stream(stream)))
-    _on_stream(stream, workspace, out, lse)
     return out, lse
 
 
@@ -299,12 +297,11 @@ def decode_attn_noalloc(cache: Cache, layer: int, t: int, q: torch.Tensor, lens:
     """decode_attn with the library's built-in scratch array instead of a caller workspace."""
     B, Hq, D = cache.B, cache.Hq, cache.D
     if out is None:
-        out = _empty((B, Hq, D), (Hq * D, D, 1), torch.float32, q.device, stream)
+        out = _new((B, Hq, D), (Hq * D, D, 1), q.device, stream)
     if lse is None:
-        lse = _empty((B, Hq), (Hq, 1), torch.float32, q.device, stream)
+        lse = _new((B, Hq), (Hq, 1), q.device, stream)
     _check(lib().loopvq_decode_attn_noalloc(cache.ref(), layer, t, _ptr(q), _ptr(lens), max_len, scale, _ptr(out),
                                             _ptr(lse), _stream(stream)))
-    _on_stream(stream, None, out, lse)
     return out, lse
 
 
@@ -314,16 +311,15 @@ def decode_attn_range(cache: Cache, layer: int, t: int, q: torch.Tensor, starts,
     B, Hq, D = cache.B, cache.Hq, cache.D
     dev = q.device
     if out is None:
-        out = _empty((B, Hq, D), (Hq * D, D, 1), torch.float32, dev, stream)
+        out = _new((B, Hq, D), (Hq * D, D, 1), dev, stream)
     if lse is None:
-        lse = _empty((B, Hq), (Hq, 1), torch.float32, dev, stream)
+        lse = _new((B, Hq), (Hq, 1), dev, stream)
     need = decode_workspace_bytes(cache, max_len)
     if workspace is None:
         workspace = _empty((max(need, 16),), (1,), torch.uint8, dev, stream)
     _check(lib().loopvq_decode_attn_range(cache.ref(), layer, t, _ptr(q), _ptr(starts), _ptr(lens), max_len, scale,
                                           _ptr(out), _ptr(lse), _ptr(workspace),
                                           workspace.numel() * workspace.element_size(), _stream(stream)))
-    _on_stream(stream, workspace, out, lse)
     return out, lse
 
 
@@ -353,16 +349,15 @@ def bf16_decode_attn(cache: Bf16Cache, q: torch.Tensor, lens: torch.Tensor, max_
     B, Hq, D = cache.B, cache.Hq, cache.D
     dev = q.device
     if out is None:
-        out = _empty((B, Hq, D), (Hq * D, D, 1), torch.float32, dev, stream)
+        out = _new((B, Hq, D), (Hq * D, D, 1), dev, stream)
     if lse is None:
-        lse = _empty((B, Hq), (Hq, 1), torch.float32, dev, stream)
+        lse = _new((B, Hq), (Hq, 1), dev, stream)
     need = bf16_decode_workspace_bytes(cache, max_len)
     if workspace is None:
         workspace = _empty((max(need, 16),), (1,), torch.uint8, dev, stream)
     _check(lib().loopvq_bf16_decode_attn(cache.ref(), _ptr(q), _ptr(starts), _ptr(lens), max_len, scale, _ptr(out),
                                          _ptr(lse), _ptr(workspace), workspace.numel() * workspace.element_size(),
                                          _stream(stream)))
-    _on_stream(stream, workspace, out, lse)
     return out, lse
 
 
@@ -371,12 +366,11 @@ def merge2(out_a, lse_a, out_b, lse_b, out=None, lse=None, stream=None):
     D = out_a.shape[-1]
     rows = out_a.numel() // D
     if out is None:
-        out = _empty_like(out_a, stream)
+        out = _new_like(out_a, stream)
     if lse is None:
-        lse = _empty_like(lse_a, stream)
+        lse = _new_like(lse_a, stream)
     _check(lib().loopvq_merge2(_ptr(out_a), _ptr(lse_a), _ptr(out_b), _ptr(lse_b), rows, D, _ptr(out), _ptr(lse),
                                _stream(stream)))
-    _on_stream(stream, None, out, lse)
     return out, lse
 
 
@@ -392,9 +386,17 @@ def _result(t, name: str, shape: tuple, like: torch.Tensor, stream):
     """An fp32 output: the caller's, or a new one."""
     if t is None:
         strides = (shape[1] * shape[2], shape[2], 1) if len(shape) == 3 else (shape[1], 1)
-        return _empty(shape, strides, torch.float32, like.device, stream)
+        return _new(shape, strides, like.device, stream)
     _need(t, name, shape, _F32, like.device)
     return t
+
+
+def _on_stream(stream, *tensors):
+    """A caller's memory that is used on another stream than its own is not reused before that stream is done with it."""
+    if stream is not None:
+        for t in tensors:
+            if t is not None:
+                t.record_stream(stream)
 
 
 _sizes = {}
@@ -480,7 +482,7 @@ def bf16_shared_attn(cache: Bf16Cache, seq: int, q: torch.Tensor, lens: torch.Te
                                      _ptr(oo), _ptr(ol), out.data_ptr(), lse.data_ptr(), ws, n,
                                      _stream(stream)))
     _keep_size(key, need)
-    _on_stream(stream, workspace, out, lse)
+    _on_stream(stream, out, lse, workspace)
     return out, lse
 
 
@@ -497,7 +499,7 @@ def shared_attn(cache: Cache, layer: int, t: int, seq: int, q: torch.Tensor, len
                                 _ptr(oo), _ptr(ol), out.data_ptr(), lse.data_ptr(), ws, n,
                                 _stream(stream)))
     _keep_size(key, need)
-    _on_stream(stream, workspace, out, lse)
+    _on_stream(stream, out, lse, workspace)
     return out, lse
 
 
@@ -534,7 +536,7 @@ def bf16_decode_attn_scored(cache: Bf16Cache, q: torch.Tensor, lens: torch.Tenso
                                             _ptr(ol), _ptr(score), score_out.data_ptr(), out.data_ptr(),
                                             lse.data_ptr(), ws, n, _stream(stream)))
     _keep_size(key, need)
-    _on_stream(stream, workspace, out, lse)
+    _on_stream(stream, out, lse, workspace)
     return out, lse, score_out
 
 
@@ -608,16 +610,15 @@ def tasq_decode_attn(cache: Cache, tasq: Tasq, layer: int, t: int, q, lens, max_
     B, Hq, D = cache.B, cache.Hq, cache.D
     dev = q.device
     if out is None:
-        out = _empty((B, Hq, D), (Hq * D, D, 1), torch.float32, dev, stream)
+        out = _new((B, Hq, D), (Hq * D, D, 1), dev, stream)
     if lse is None:
-        lse = _empty((B, Hq), (Hq, 1), torch.float32, dev, stream)
+        lse = _new((B, Hq), (Hq, 1), dev, stream)
     need = decode_workspace_bytes(cache, max_len)
     if workspace is None:
         workspace = _empty((max(need, 16),), (1,), torch.uint8, dev, stream)
     _check(lib().loopvq_tasq_decode_attn(cache.ref(), tasq.ref(), layer, t, _ptr(q), _ptr(lens), max_len, scale,
                                          _ptr(out), _ptr(lse), _ptr(workspace),
                                          workspace.numel() * workspace.element_size(), _stream(stream)))
-    _on_stream(stream, workspace, out, lse)
     return out, lse
 
 
@@ -662,15 +663,14 @@ def window_decode_attn(win: Window, cache: Cache, layer: int, t: int, q, max_cod
     B, Hq, D = cache.B, cache.Hq, cache.D
     dev = q.device
     if out is None:
-        out = _empty((B, Hq, D), (Hq * D, D, 1), torch.float32, dev, stream)
+        out = _new((B, Hq, D), (Hq * D, D, 1), dev, stream)
     if lse is None:
-        lse = _empty((B, Hq), (Hq, 1), torch.float32, dev, stream)
+        lse = _new((B, Hq), (Hq, 1), dev, stream)
     if workspace is None:
         workspace = _empty((max(window_workspace_bytes(win, cache, max_coded), 16),), (1,), torch.uint8, dev, stream)
     _check(lib().loopvq_window_decode_attn(win.ref(), cache.ref(), layer, t, _ptr(q), max_coded, scale, _ptr(out),
                                            _ptr(lse), _ptr(workspace), workspace.numel() * workspace.element_size(),
                                            _stream(stream)))
-    _on_stream(stream, workspace, out, lse)
     return out, lse
 
 
@@ -681,25 +681,23 @@ def window_append_decode_attn(win: Window, cache: Cache, layer: int, t: int, k_r
     B, Hq, D = cache.B, cache.Hq, cache.D
     dev = q.device
     if out is None:
-        out = _empty((B, Hq, D), (Hq * D, D, 1), torch.float32, dev, stream)
+        out = _new((B, Hq, D), (Hq * D, D, 1), dev, stream)
     if lse is None:
-        lse = _empty((B, Hq), (Hq, 1), torch.float32, dev, stream)
+        lse = _new((B, Hq), (Hq, 1), dev, stream)
     if workspace is None:
         workspace = _empty((max(window_workspace_bytes(win, cache, max_coded), 16),), (1,), torch.uint8, dev, stream)
     _check(lib().loopvq_window_append_decode_attn(win.ref(), cache.ref(), layer, t, _ptr(k_rot), _ptr(k_pre), _ptr(v),
                                                   _ptr(q), max_coded, scale, _ptr(out), _ptr(lse), _ptr(workspace),
                                                   workspace.numel() * workspace.element_size(), _stream(stream)))
-    _on_stream(stream, workspace, out, lse)
     return out, lse
 
 
 def dequant_debug(cache: Cache, layer: int, t: int, kv: int, b: int, tok0: int, ntok: int, apply_rope: bool = False,
                   out=None, stream=None):
     if out is None:
-        out = _empty((cache.Hkv, ntok, cache.D), (ntok * cache.D, cache.D, 1), torch.float32, "cuda", stream)
+        out = _new((cache.Hkv, ntok, cache.D), (ntok * cache.D, cache.D, 1), "cuda", stream)
     _check(lib().loopvq_dequant_debug(cache.ref(), layer, t, kv, b, tok0, ntok, int(bool(apply_rope)), _ptr(out),
                                       _stream(stream)))
-    _on_stream(stream, None, out)
     return out
 
 

@@ -125,3 +125,20 @@ def test_a_stream_of_another_gpu_is_refused():
     with pytest.raises(LQ.LoopVQError) as e:
         LQ.bf16_shared_attn(cache, 0, bf16(g, 1, 1, 64), i32([64]), 64, stream=Stream())
     assert e.value.status == 1
+
+
+def test_default_memory_of_decode_and_merge_on_two_streams():
+    g = gen(32)
+    n, hkv, hq = 20000, 4, 16
+    cache = LQ.Bf16Cache(bf16(g, 2, hkv, n, 128), bf16(g, 2, hkv, n, 128), hq)
+    coded = coded_cache(g, hkv, hq, 128, 8, 4, 256, n, seqs=2)
+    q, lens = bf16(g, 2, hq, 128), i32([n, n - 7])
+    part = torch.randn(2, hq, 128, generator=g, device="cuda"), torch.randn(2, hq, generator=g, device="cuda")
+    side = torch.cuda.Stream()
+    for call in (lambda s: LQ.bf16_decode_attn(cache, q, lens, n, stream=s), lambda s: LQ.decode_attn(coded, 0, 1, q, lens, n, stream=s),
+                 lambda s: LQ.merge2(*part, *part, stream=s)):
+        want = [x.clone() for x in call(None)]
+        torch.cuda.synchronize()
+        got = [call(side if i % 2 else None) for i in range(16)]
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, y) for r in got for x, y in zip(r, want))
