@@ -309,8 +309,8 @@ template <int D, int QPK>
 __global__ void __launch_bounds__(kScoreThreads) bf16_scored_merge_kernel(const Bf16Args a, float *out, float *lse) {
     const int h = blockIdx.y, b = blockIdx.z, tid = threadIdx.x;
     grid_wait();
-    const int len = min(max(__ldg(a.lens + b), 0), a.max_len);
-    const int st = a.starts ? min(max(__ldg(a.starts + b), 0), len) : 0;
+    const int len = min(max(word(a.lens + b), 0), a.max_len);
+    const int st = a.starts ? min(max(word(a.starts + b), 0), len) : 0;
     const bool last = blockIdx.x == gridDim.x - 1;         // writes out and lse
     const int n0 = (int)blockIdx.x * kScoreChunk;
     if (!last && (n0 >= len || n0 + kScoreChunk <= st)) return;

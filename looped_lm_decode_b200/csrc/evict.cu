@@ -65,8 +65,8 @@ struct RegKeys {
     __device__ __forceinline__ int load(const EvictArgs &a, size_t row, int b, int part, int) {
         constexpr int B = 5;                                         // pairs of loads in flight
         base = part * (NT * ITEMS) + (threadIdx.x >> 5) * (ITEMS * 32) + (threadIdx.x & 31);
-        int len = __ldg(a.lens_in + b);
-        const long long from = (long long)__ldg(a.next_pos + b) - a.n_recent;
+        int len = word(a.lens_in + b);
+        const long long from = (long long)word(a.next_pos + b) - a.n_recent;
         len = min(max(len, 0), a.max_len);
         const int stay = min(len, a.budget);
 #pragma unroll
@@ -143,11 +143,11 @@ struct MemKeys {
     int n_sink, base, count;
     long long from;
     __device__ __forceinline__ int load(const EvictArgs &a, size_t row, int b, int part, int parts) {
-        const int len = min(max(__ldg(a.lens_in + b), 0), a.max_len), stay = min(len, a.budget);
+        const int len = min(max(word(a.lens_in + b), 0), a.max_len), stay = min(len, a.budget);
         score = a.score_in + row;
         pos = a.pos_in + row;
         n_sink = a.n_sink;
-        from = (long long)__ldg(a.next_pos + b) - a.n_recent;
+        from = (long long)word(a.next_pos + b) - a.n_recent;
         count = (len + NT * parts - 1) / (NT * parts);
         base = (part * (NT / 32) + (threadIdx.x >> 5)) * (count * 32) + (threadIdx.x & 31);
         const int end = min(stay, (part + 1) * count * NT);

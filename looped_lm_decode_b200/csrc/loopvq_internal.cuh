@@ -65,6 +65,11 @@ cudaError_t allow_large_clusters(const void *kern);
 __device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void grid_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
+// A word that the kernel before may have written (lengths, which an eviction writes and lets the next kernel begin).  Not
+// __ldg: a load through the read-only path may be moved before the wait, and is not promised to see what was written while
+// this kernel was already there.
+__device__ __forceinline__ int word(const int32_t *p) { return *p; }
+
 template <typename... P, typename... A>
 inline cudaError_t launch_pdl(void (*kern)(P...), dim3 grid, unsigned threads, size_t smem, cudaStream_t s, const A &...args) {
     cudaLaunchConfig_t cfg{};

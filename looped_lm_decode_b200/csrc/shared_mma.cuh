@@ -218,8 +218,8 @@ __global__ void __launch_bounds__(Plan<D, MB, C, PG, FINE>::kThreads, 1)
 
     grid_trigger();
     grid_wait();
-    const int len = min(max(__ldg(a.len), 0), a.max_len);
-    const int st = a.start ? min(max(__ldg(a.start), 0), len) : 0;
+    const int len = min(max(word(a.len), 0), a.max_len);
+    const int st = a.start ? min(max(word(a.start), 0), len) : 0;
     const int tok0 = coded ? (st & ~3) : st;                         // index words come in tiles of 4 tokens
     const int tiles_all = len > st ? (len - tok0 + NT - 1) / NT : 0;
     const int t_first = (int)((long long)split * tiles_all / a.nsplit);

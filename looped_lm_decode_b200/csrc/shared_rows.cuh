@@ -70,8 +70,8 @@ struct RowTiles {
     long long per_head, before;      // tiles of a KV head; those of the sequences before b
 };
 __device__ __forceinline__ int row_tiles(const int32_t *starts, const int32_t *lens, int max_len, int b) {
-    const int len = min(max(__ldg(lens + b), 0), max_len);
-    const int st = starts ? min(max(__ldg(starts + b), 0), len) : 0;
+    const int len = min(max(word(lens + b), 0), max_len);
+    const int st = starts ? min(max(word(starts + b), 0), len) : 0;
     return (len - st + 127) >> 7;
 }
 __device__ __forceinline__ RowTiles row_space(const int32_t *starts, const int32_t *lens, int max_len, int seqs, int lane,
@@ -247,8 +247,8 @@ __global__ void __launch_bounds__(RowsPlan<D, NR, C, PG>::kThreads, 1)
         Item x;
         x.b = b;
         x.h = h;
-        x.len = min(max(__ldg(a.lens + b), 0), a.max_len);
-        x.st = a.starts ? min(max(__ldg(a.starts + b), 0), x.len) : 0;
+        x.len = min(max(word(a.lens + b), 0), a.max_len);
+        x.st = a.starts ? min(max(word(a.starts + b), 0), x.len) : 0;
         const int tok0 = coded ? (x.st & ~3) : x.st;                 // index words come in tiles of 4 tokens
         const int tiles = x.len > x.st ? (x.len - tok0 + NT - 1) / NT : 0;
         x.tok_first = tok0 + (int)skip * NT;

@@ -142,3 +142,53 @@ def test_default_memory_of_decode_and_merge_on_two_streams():
         got = [call(side if i % 2 else None) for i in range(16)]
         torch.cuda.synchronize()
         assert all(torch.equal(x, y) for r in got for x, y in zip(r, want))
+
+
+# ------------------------------------------------------------------ calls in a row
+
+@pytest.mark.parametrize("hkv,hq", [(2, 2), (2, 8), (8, 8)])
+@pytest.mark.parametrize("n", [900, 2400])
+def test_lengths_that_an_eviction_writes_are_read_by_the_next_call(n, hkv, hq):
+    """Evictions in place with scored decodes, prefix attentions and further evictions right behind them, in a graph without
+    a kernel of anything else between: what the same calls give one by one."""
+    b, d, steps = 4, 64, 12
+    g = gen(n + hkv)
+    k, v, q = bf16(g, b, hkv, n, d), bf16(g, b, hkv, n, d), bf16(g, b, hq, d)
+    score0 = torch.rand(b, hkv, n, generator=g, device="cuda")
+    pos0 = torch.arange(n, device="cuda", dtype=torch.int32).expand(b, hkv, n).contiguous()
+    lens0, nxt = i32([n, n - 5, n - 60, n - 200]), i32([n] * b)
+    budgets = [n - 10 - 20 * i for i in range(steps)]
+
+    def run(cache, score, pos, lens, out, lse, ws, wait):
+        for i, budget in enumerate(budgets):
+            LQ.bf16_evict(cache, score, pos, lens, nxt, n, budget, n_sink=4, n_recent=16, workspace=ws[0])
+            wait()
+            if i % 3 == 0:
+                LQ.bf16_decode_attn_scored(cache, q, lens, n, score, out=out[i], lse=lse[i], workspace=ws[1])
+            elif i % 3 == 1:
+                LQ.bf16_shared_attn(cache, 1, q, lens, n, out=out[i], lse=lse[i], workspace=ws[2])
+            wait()
+
+    def fresh():
+        cache = LQ.Bf16Cache(k.clone(), v.clone(), hq)
+        need = [max(LQ.bf16_evict_workspace_bytes(cache, n, x) for x in budgets), LQ.bf16_scored_workspace_bytes(cache, n),
+                LQ.bf16_shared_workspace_bytes(cache, b, n)]
+        return (cache, score0.clone(), pos0.clone(), lens0.clone(), torch.zeros(steps, b, hq, d, device="cuda"),
+                torch.zeros(steps, b, hq, device="cuda"), [torch.zeros(x, dtype=torch.uint8, device="cuda") for x in need])
+
+    alone = fresh()
+    run(*alone, torch.cuda.synchronize)
+    assert alone[3].tolist() == [budgets[-1]] * b
+    for _ in range(3):
+        state = fresh()
+        graph = torch.cuda.CUDAGraph()
+        torch.cuda.synchronize()
+        with torch.cuda.graph(graph):
+            run(*state, lambda: None)
+        graph.replay()
+        torch.cuda.synchronize()
+        LQ.fault_check()
+        m = budgets[-1]
+        assert torch.equal(state[3], alone[3]) and torch.equal(state[4], alone[4]) and torch.equal(state[5], alone[5])
+        assert torch.equal(state[1][..., :m], alone[1][..., :m]) and torch.equal(state[2][..., :m], alone[2][..., :m])
+        assert torch.equal(state[0].k[:, :, :m], alone[0].k[:, :, :m]) and torch.equal(state[0].v[:, :, :m], alone[0].v[:, :, :m])
