@@ -125,9 +125,9 @@ __device__ __forceinline__ void to_cta(void *p, int rank, uint32_t v) {
 __device__ __forceinline__ void add_at_cta(void *p, int rank, uint32_t v) {
     asm volatile("red.relaxed.cluster.shared::cluster.add.u32 [%0], %1;" ::"r"(at_cta(p, rank)), "r"(v) : "memory");
 }
-__device__ __forceinline__ void cluster_sync() {
-    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+__device__ __forceinline__ void cluster_sync() {                     // (not .aligned: some calls come behind divergent loops)
+    asm volatile("barrier.cluster.arrive.release;" ::: "memory");
+    asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
 }
 template <int CL>
 __device__ __forceinline__ void sync_row() {                         // the CTAs of a row
