@@ -102,32 +102,36 @@ loopvq_status check_apart(const Span (&outs)[O], const Span (&ins)[I]) {
 namespace loopvq {
 void set_last_error(const char *msg) { snprintf(g_err, sizeof(g_err), "%s", msg); }
 
+// Attributes that are set, per kernel and device.  No exception leaves it: the entry points are C.
+template <typename Set>
+static cudaError_t raise_once(std::map<std::pair<const void *, int>, size_t> &done, const void *kern, size_t value, Set set) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    static std::mutex mu;
+    try {
+        std::lock_guard<std::mutex> lock(mu);
+        size_t &cur = done[{kern, dev}];
+        if (cur >= value) return cudaSuccess;
+        e = set();
+        if (e == cudaSuccess) cur = value;
+        return e;
+    } catch (...) {                                        // no memory for the entry, or no lock
+        return cudaErrorMemoryAllocation;
+    }
+}
+
 cudaError_t ensure_dynamic_smem(const void *kern, size_t bytes) {
     if (bytes <= 48u * 1024u) return cudaSuccess;          // within the default limit
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return e;
-    static std::mutex mu;
     static std::map<std::pair<const void *, int>, size_t> done;
-    std::lock_guard<std::mutex> lock(mu);
-    size_t &cur = done[{kern, dev}];
-    if (cur >= bytes) return cudaSuccess;
-    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
-    if (e == cudaSuccess) cur = bytes;
-    return e;
+    return raise_once(done, kern, bytes, [&] {
+        return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    });
 }
+
 cudaError_t allow_large_clusters(const void *kern) {
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return e;
-    static std::mutex mu;
-    static std::map<std::pair<const void *, int>, bool> done;
-    std::lock_guard<std::mutex> lock(mu);
-    bool &set = done[{kern, dev}];
-    if (set) return cudaSuccess;
-    e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-    set = e == cudaSuccess;
-    return e;
+    static std::map<std::pair<const void *, int>, size_t> done;
+    return raise_once(done, kern, 1, [&] { return cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1); });
 }
 }  // namespace loopvq
 
