@@ -12,8 +12,9 @@
 //    product and have accumulators of their own, added when the result is read: V is read once for all of them, and the
 //    small parts are not cut to the large one's last place.
 //  - A row's maximum would be a reduction over lanes.  Any reference is exact, and fp32 and bf16 have 8 exponent bits, so
-//    the reference only has to keep exp2 in range: it is the score of a stream's first token and moves only when some
-//    score passes it by 2^40, which the warps of a stream agree on with one barrier vote per tile.
+//    the reference only has to keep exp2 in range: it is the score of a stream's first token (a first score of -inf or far
+//    from 0: the lowest number) and moves, to the tile's maximum, only when some score passes it by 2^40, which the warps of
+//    a stream agree on with one barrier vote per tile.
 //  - Sums are kept per (thread, row) and added over the lanes at the end (a product of ones and P would give them too, at
 //    8 more products a tile; every product takes 46 clocks or more, however few its columns).
 //
@@ -26,6 +27,8 @@
 // 87% of a copy; 16 ragged sequences of up to 16384 tokens with scores: 305 MB in 56 us and 8 us of merge), short ones the
 // chain of a tile through copy, product, softmax and product (1000 tokens, 3 queries, 16 heads, one launch: 10.1 us).
 #pragma once
+
+#include <cfloat>
 
 #include <cuda.h>
 
@@ -111,7 +114,8 @@ struct RowsPlan {
     static constexpr int offTurn = offTable + 2 * kTable;
     static constexpr int offRef = offTurn + (coded ? D * 4 : 0);     // per stream: references, their moves, maxima
     static constexpr int kRef = 6 * NR * 4 + 16;
-    static constexpr int offInfo = offRef + 2 * kRef;                // this CTA's first piece
+    static constexpr int offZero = offRef + 2 * kRef;                // NR zeros
+    static constexpr int offInfo = offZero + NR * 4;                 // this CTA's first piece
     static constexpr int offBar = offInfo + 32;
     static constexpr int kBars = 4 * ST + 2 * NQ + 7;
     static constexpr int offTmem = offBar + kBars * 8;
@@ -175,6 +179,7 @@ __global__ void __launch_bounds__(RowsPlan<D, NR, C, PG>::kThreads, 1)
     constexpr bool coded = C != 0;
     constexpr int NT = P::NT, KP = P::KP, ST = P::ST, NQ = P::NQ, PARTS = P::PARTS, NPAN = D / 64;
     constexpr float kFar = 40.f;                                     // log2 units a score may pass the reference by
+    constexpr float kExact = 16777216.f;                             // scores up to here are held to 2 log2 units
 
     extern __shared__ unsigned char smem_raw[];
     const uint32_t base = (tc::smem_u32(smem_raw) + 1023u) & ~1023u;
@@ -199,6 +204,7 @@ __global__ void __launch_bounds__(RowsPlan<D, NR, C, PG>::kThreads, 1)
         tc::prefetch_map(&kmap);
         tc::prefetch_map(&vmap);
     }
+    if (tid < NR) reinterpret_cast<float *>(smem + P::offZero)[tid] = 0.f;
     if (warp == P::kMma) {
         if (lane == 0) {
             for (int s = 0; s < ST; ++s) {
@@ -365,6 +371,7 @@ __global__ void __launch_bounds__(RowsPlan<D, NR, C, PG>::kThreads, 1)
             float osum[DIRECT ? 1 : NR] = {};                        // this channel's O of the tiles before the last move
             float kept[SCORES && DIRECT ? kDirectTiles / 2 : 1][8] = {};   // this token's scores in the stream's tiles
             int j = 0;                                               // tiles of this stream in the item
+            bool far = false;                                        // some reference is past kExact (the stream's threads alike)
             for (int t = 0; ok && t < x.ntiles; ++t, ++g) {
                 if ((g & 1) != w) continue;
                 // S of this step; and P of the stream's step before is read, O written
@@ -388,21 +395,24 @@ __global__ void __launch_bounds__(RowsPlan<D, NR, C, PG>::kThreads, 1)
                     }
                 }
                 // 16 columns in the exponent's units relative to the reference
+                float qs = a.qscale;
+                const float *nref = ref;
                 auto load = [&](int c, float (&v)[16]) {
                     uint32_t s[16];
                     tc::tmem_ld16(ts + c, s);
                     tc::tmem_wait_ld16(s);
 #pragma unroll
                     for (int k = 0; k < 16; k += 4) {
-                        const float4 nr = *reinterpret_cast<const float4 *>(ref + c + k);
-                        v[k] = fmaf(__uint_as_float(s[k]), a.qscale, nr.x);
-                        v[k + 1] = fmaf(__uint_as_float(s[k + 1]), a.qscale, nr.y);
-                        v[k + 2] = fmaf(__uint_as_float(s[k + 2]), a.qscale, nr.z);
-                        v[k + 3] = fmaf(__uint_as_float(s[k + 3]), a.qscale, nr.w);
+                        const float4 nr = *reinterpret_cast<const float4 *>(nref + c + k);
+                        v[k] = fmaf(__uint_as_float(s[k]), qs, nr.x);
+                        v[k + 1] = fmaf(__uint_as_float(s[k + 1]), qs, nr.y);
+                        v[k + 2] = fmaf(__uint_as_float(s[k + 2]), qs, nr.z);
+                        v[k + 3] = fmaf(__uint_as_float(s[k + 3]), qs, nr.w);
                     }
                 };
                 if (j == 0) {
-                    // an item's first tile: its first attended token gives the reference (0 if its score is no number)
+                    // an item's first tile: its first attended token gives the reference.  Where that is -inf, or far, the
+                    // lowest number does, which any other score passes (and exp2 of -inf is 0 against it)
                     if (ok && wq == 0) {
 #pragma unroll 1
                         for (int c = 0; c < cols; c += 16) {
@@ -413,7 +423,7 @@ __global__ void __launch_bounds__(RowsPlan<D, NR, C, PG>::kThreads, 1)
 #pragma unroll
                                 for (int k = 0; k < 16; ++k) {
                                     const float v = __uint_as_float(s[k]) * a.qscale;
-                                    ref[c + k] = fabsf(v) < CUDART_INF_F ? -v : 0.f;
+                                    ref[c + k] = fabsf(v) <= kExact ? -v : FLT_MAX;
                                 }
                             }
                         }
@@ -432,17 +442,19 @@ __global__ void __launch_bounds__(RowsPlan<D, NR, C, PG>::kThreads, 1)
                         }
                     }
                 }
-                if (stream_any(bar, !ok || (in && top > kFar))) {
-                    // rare: move the references to the maxima of this tile, and what was summed with them
+                if (stream_any(bar, !ok || far || (in && top > kFar))) {
+                    // rare: move the references to the maxima of this tile, and what was summed with them.  Maxima of the scores
+                    // themselves: relative to a reference far below they have lost their last places
                     if (lane == 0) wok[wq] = ok;
                     if (ok) {
 #pragma unroll 1
                         for (int c = 0; c < cols; c += 16) {
-                            float v[16];
-                            load(c, v);
+                            uint32_t s[16];
+                            tc::tmem_ld16(ts + c, s);
+                            tc::tmem_wait_ld16(s);
 #pragma unroll
                             for (int k = 0; k < 16; ++k) {
-                                const int m = __reduce_max_sync(0xffffffffu, in ? ordered(v[k]) : ordered(0.f));
+                                const int m = __reduce_max_sync(0xffffffffu, ordered(in ? __uint_as_float(s[k]) * a.qscale : -FLT_MAX));
                                 if (lane == 0) wmax[wq * NR + c + k] = unordered(m);
                             }
                         }
@@ -452,9 +464,10 @@ __global__ void __launch_bounds__(RowsPlan<D, NR, C, PG>::kThreads, 1)
                     if (!ok) break;                                  // every warp of the stream alike
                     const int r = tid % 128;
                     if (r < cols) {                                  // how far the row's reference rises
-                        const float up = fmaxf(fmaxf(fmaxf(wmax[r], wmax[NR + r]), fmaxf(wmax[2 * NR + r], wmax[3 * NR + r])), 0.f);
-                        corr[r] = ex2(-up);
-                        ref[r] -= up;
+                        const float was = -ref[r];
+                        const float now = fmaxf(was, fmaxf(fmaxf(wmax[r], wmax[NR + r]), fmaxf(wmax[2 * NR + r], wmax[3 * NR + r])));
+                        corr[r] = ex2(was - now);
+                        ref[r] = -now;
                     }
                     stream_sync(bar);
 #pragma unroll
@@ -476,23 +489,46 @@ __global__ void __launch_bounds__(RowsPlan<D, NR, C, PG>::kThreads, 1)
                         }
                         tc::tmem_wait_st();
                     }
+                    // a reference that cannot hold fractions of its scores: the difference of two rounded numbers, which is 0
+                    // at the maximum, takes the place of the scores, instead of an exact product less a rounded one
+                    far = false;
+                    for (int r2 = 0; r2 < cols; ++r2) far = far || (fabsf(ref[r2]) > kExact && ref[r2] != FLT_MAX);
+                    if (far) {
+#pragma unroll 1
+                        for (int c = 0; c < cols; c += 16) {
+                            uint32_t s[16];
+                            tc::tmem_ld16(ts + c, s);
+                            tc::tmem_wait_ld16(s);
+#pragma unroll
+                            for (int k = 0; k < 16; ++k)
+                                s[k] = __float_as_uint(__fadd_rn(__fmul_rn(__uint_as_float(s[k]), qs), ref[c + k]));
+                            tc::tmem_st16(ts + c, s);
+                        }
+                        tc::tmem_wait_st();
+                        qs = 1.f;
+                        nref = reinterpret_cast<const float *>(smem + P::offZero);
+                    }
                 }
                 if constexpr (SCORES) {
                     uint32_t s[16];
                     tc::tmem_ld16(ts, s);
                     tc::tmem_wait_ld16(s);
+                    if (far) {                                       // they were replaced above
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) s[k] = __float_as_uint(__uint_as_float(s[k]) - ref[k]);
+                    }
                     if constexpr (DIRECT) {
 #pragma unroll
                         for (int q = 0; q < kDirectTiles / 2; ++q)
                             if (j == q) {
 #pragma unroll
-                                for (int k = 0; k < 8; ++k) kept[q][k] = __uint_as_float(s[k]) * a.qscale;
+                                for (int k = 0; k < 8; ++k) kept[q][k] = __uint_as_float(s[k]) * qs;
                             }
                     } else {
                         float *sc = a.ws_s + ((size_t)x.b * a.Hq + x.h * a.R) * a.sstride + n;
 #pragma unroll
                         for (int k = 0; k < 8; ++k)
-                            if (in && k < a.R) sc[(size_t)k * a.sstride] = __uint_as_float(s[k]) * a.qscale;
+                            if (in && k < a.R) sc[(size_t)k * a.sstride] = __uint_as_float(s[k]) * qs;
                     }
                 }
 #pragma unroll

@@ -192,3 +192,93 @@ def test_lengths_that_an_eviction_writes_are_read_by_the_next_call(n, hkv, hq):
         assert torch.equal(state[3], alone[3]) and torch.equal(state[4], alone[4]) and torch.equal(state[5], alone[5])
         assert torch.equal(state[1][..., :m], alone[1][..., :m]) and torch.equal(state[2][..., :m], alone[2][..., :m])
         assert torch.equal(state[0].k[:, :, :m], alone[0].k[:, :, :m]) and torch.equal(state[0].v[:, :, :m], alone[0].v[:, :, :m])
+
+
+# ------------------------------------------------------------------ scores of -inf and of the lowest values
+#
+# Tolerances.  A score is a sum over D products; here one of them moves it by FAR natural units, so the sum's roundings (8 of
+# 2^-22 of sum |q k| scale, as in test_gpu_shared.py, where that sum is below 8) grow by (8 + FAR) / 8, and weights and
+# outputs with them: GROW times that file's bounds.
+
+FAR = 100.0
+GROW = 1 + FAR / 8
+LOWEST = torch.finfo(torch.bfloat16).min
+
+
+def masked_case(g, b, hkv, hq, n, d, masked, kind):
+    """Caches and queries whose tokens `masked` score -inf (or about -1e37), and all others FAR below 0: beyond fp32's exponent
+    range from a reference of 0."""
+    k, v, q = bf16(g, b, hkv, n, d), bf16(g, b, hkv, n, d), bf16(g, b, hq, d)
+    q[..., 1], k[..., 1] = 8, -FAR * math.sqrt(d) / 8
+    q[..., 0], k[..., 0] = (1, 0) if kind == "inf" else (0.5, 0)
+    k[:, :, masked, 0] = -math.inf if kind == "inf" else LOWEST
+    return k, v, q
+
+
+def fp64_attention(q, k, v, other=None):
+    """q [Hq][D], k and v [Hkv][n][D] of one sequence: out, lse, sum p |v| and every token's weight per KV head.  Scores past
+    fp32's range are -inf."""
+    hkv, d = k.shape[0], q.shape[-1]
+    s = torch.einsum("hgd,hnd->hgn", q.double().view(hkv, -1, d), k.double()) / math.sqrt(d)
+    s = torch.where(s < torch.finfo(torch.float32).min, -math.inf, s)
+    lse = torch.logsumexp(s, 2)
+    joint = lse if other is None else torch.logaddexp(lse, other[1].double().view(hkv, -1))
+    p = torch.exp(s - torch.where(joint == -math.inf, 0.0, joint)[..., None])
+    out, mag = p @ v.double(), p @ v.double().abs()
+    if other is not None:
+        po = torch.exp(other[1].double().view(hkv, -1) - torch.where(joint == -math.inf, 0.0, joint))[..., None]
+        out, mag = out + po * other[0].double().view(hkv, -1, d), mag + po * other[0].double().abs().view(hkv, -1, d)
+    return out.reshape(-1, d), joint.reshape(-1), mag.reshape(-1, d), p.sum(1)
+
+
+def close(out, lse, want):
+    ro, rl, mag = want[:3]
+    empty = rl == -math.inf
+    assert (lse[empty] == -math.inf).all() and (out[empty] == 0).all()
+    assert ((out.double() - ro).abs() <= GROW * 2.5e-4 * mag).all(), ((out.double() - ro).abs() / (mag + 1e-30)).max().item()
+    assert ((lse.double() - rl)[~empty].abs() <= GROW * 1e-4).all()
+
+
+def spots(which, n):
+    return dict(first=slice(0, 1), tiles=slice(0, min(n - 1, 300)), every_other=slice(0, n, 2), all=slice(0, n))[which]
+
+
+@pytest.mark.parametrize("kind", ["inf", "lowest"])
+@pytest.mark.parametrize("which", ["first", "tiles", "every_other", "all"])
+@pytest.mark.parametrize("n", [200, 900, 5000])
+@pytest.mark.parametrize("rows,hkv,hq", [(1, 1, 1), (5, 2, 8), (60, 2, 4), (300, 1, 1)])
+def test_prefix_scores_of_minus_infinity_weigh_nothing(rows, hkv, hq, n, which, kind):
+    """At the first tokens above all, which give some kernels their reference: the other tokens are not lost."""
+    if kind == "lowest" and which == "all":
+        pytest.skip("below")
+    g, d = gen(rows + n), 128
+    k, v, _ = masked_case(g, 1, hkv, hq, n, d, spots(which, n), kind)
+    q = bf16(g, rows, hq, d)
+    q[..., 1], q[..., 0] = 8, 1 if kind == "inf" else 0.5
+    cache = LQ.Bf16Cache(k, v, hq)
+    other = torch.randn(rows, hq, d, generator=g, device="cuda"), torch.randn(rows, hq, generator=g, device="cuda") - FAR
+    for o in (None, other):
+        out, lse = LQ.bf16_shared_attn(cache, 0, q, i32([n]), n, other=o)
+        LQ.fault_check()
+        for r in range(0, rows, 7):
+            close(out[r], lse[r], fp64_attention(q[r], k[0], v[0], None if o is None else (o[0][r], o[1][r])))
+
+
+@pytest.mark.parametrize("kind", ["inf", "lowest"])
+@pytest.mark.parametrize("which", ["first", "tiles", "every_other"])
+@pytest.mark.parametrize("hq,n", [(2, 300), (8, 300), (4, 1500), (8, 5000)])
+def test_scored_decode_with_scores_of_minus_infinity(hq, n, which, kind):
+    """On the tensor cores, in one launch and in two: outputs, log-sum-exps and weights."""
+    g, b, hkv, d = gen(n + hq), 3, 2, 64
+    k, v, q = masked_case(g, b, hkv, hq, n, d, spots(which, n), kind)
+    score = torch.rand(b, hkv, n, generator=g, device="cuda")
+    other = torch.randn(b, hq, d, generator=g, device="cuda"), torch.randn(b, hq, generator=g, device="cuda") - FAR
+    for o in (None, other):
+        out, lse, s = LQ.bf16_decode_attn_scored(LQ.Bf16Cache(k, v, hq), q, i32([n] * b), n, score, other=o,
+                                                 score_out=torch.zeros_like(score))
+        LQ.fault_check()
+        for i in range(b):
+            want = fp64_attention(q[i], k[i], v[i], None if o is None else (o[0][i], o[1][i]))
+            close(out[i], lse[i], want)
+            total = score[i].double() + want[3]
+            assert ((s[i].double() - total).abs() <= GROW * 2e-4 * want[3] + 2.0 ** -23 * total).all()
