@@ -101,6 +101,8 @@ constexpr int kTmemCols = 512;                                       // O of str
 template <int D, int NT, int PARTS>
 struct RowSoftmax {
     float m, l;                                                      // maximum reference (log2 units), sum
+    bool far = false;                                                // some row of the warp's is past kExact
+    static constexpr float kExact = 16777216.f;                      // scores up to here are held to 2 log2 units
 
     // S columns at ts (a third part of P goes to tp); tokens [lo, hi) of the tile count; O columns at to.  first: O holds
     // nothing yet.
@@ -139,6 +141,7 @@ struct RowSoftmax {
             const float corr = up ? ex2(m - mt) : 1.f;
             if (up) m = mt;
             l *= corr;
+            far = __any_sync(0xffffffffu, fabsf(m) > kExact && m != -CUDART_INF_F);
             if (!first) {
                 const bool ok = tc::mbar_wait_or_dead(odone, odone_parity, limit, dead);
                 if (!__all_sync(0xffffffffu, ok)) return false;
@@ -154,7 +157,23 @@ struct RowSoftmax {
                 }
             }
         }
-        const float nm = m == -CUDART_INF_F ? 0.f : -m;
+        float nm = m == -CUDART_INF_F ? 0.f : -m;
+        if (far) {
+            // a reference that cannot hold fractions of its scores: the difference of two rounded numbers, which is 0 at the
+            // maximum, takes the place of the scores, instead of an exact product less a rounded one
+#pragma unroll 1
+            for (int c = 0; c < NT; c += 32) {
+                uint32_t x[32];
+                tc::tmem_ld32(ts + c, x);
+                tc::tmem_wait_ld(x);
+#pragma unroll
+                for (int k = 0; k < 32; ++k) x[k] = __float_as_uint(__fadd_rn(__fmul_rn(__uint_as_float(x[k]), qs), nm));
+                tc::tmem_st32(ts + c, x);
+            }
+            tc::tmem_wait_st();
+            qs = 1.f;
+            nm = 0.f;
+        }
         float s0 = 0.f, s1 = 0.f;
 #pragma unroll 1
         for (int c = 0; c < NT; c += 32) {
@@ -358,7 +377,7 @@ __global__ void __launch_bounds__(Plan<D, MB, C, PG, FINE>::kThreads, 1)
         const uint32_t ts = tmem + lane_base + w * P::colS, to = tmem + lane_base + 256 + w * 128;
         const int rq = r0 + (MB == 2 ? w * 128 : 0) + row;           // query row of this thread
         const bool any = __any_sync(0xffffffffu, rq < a.R);          // warps of padding only keep step
-        RowSoftmax<D, NT, P::PARTS> sm{-CUDART_INF_F, 0.f};
+        RowSoftmax<D, NT, P::PARTS> sm{-CUDART_INF_F, 0.f, false};
         bool ok = true;
         int j = 0;
         for (int i = w; i < nsteps; i += 2, ++j) {

@@ -282,3 +282,37 @@ def test_scored_decode_with_scores_of_minus_infinity(hq, n, which, kind):
             close(out[i], lse[i], want)
             total = score[i].double() + want[3]
             assert ((s[i].double() - total).abs() <= GROW * 2e-4 * want[3] + 2.0 ** -23 * total).all()
+
+
+@pytest.mark.parametrize("rows,n", [(4, 200), (4, 900), (4, 5000), (60, 300), (60, 5000), (300, 300), (300, 5000)])
+def test_prefix_scores_far_from_zero(rows, n):
+    """Every score about -1e37, or one of 1e37: whatever rounding leaves of their order, a row is an average of values, or the
+    one value, and its log-sum-exp the scores' size."""
+    g, d = gen(rows + n), 128
+    k, v, q = bf16(g, 1, 1, n, d), bf16(g, 1, 1, n, d), bf16(g, rows, 1, d)
+    q[..., 0], size = 0.5, -0.5 * LOWEST / math.sqrt(d)
+    for keys, sign in ((slice(0, n), -1), (slice(n // 2, n // 2 + 1), 1), (slice(n - 1, n), 1), (slice(0, 1), 1)):
+        kk = k.clone()
+        kk[0, 0, keys, 0] = -LOWEST * sign
+        out, lse = LQ.bf16_shared_attn(LQ.Bf16Cache(kk, v, 1), 0, q, i32([n]), n)
+        LQ.fault_check()
+        assert ((lse / (sign * size) - 1).abs() <= 2.0 ** -20).all()
+        if sign < 0:
+            assert (out <= v.float().amax(2) + 1e-4).all() and (out >= v.float().amin(2) - 1e-4).all()
+        else:
+            assert torch.equal(out[:, 0], v[0, 0, keys].float().expand(rows, d))
+
+
+@pytest.mark.parametrize("hq,n", [(1, 300), (8, 300), (1, 1500), (4, 1500), (8, 5000)])
+def test_scored_decode_with_scores_far_from_zero(hq, n):
+    g, b, d = gen(hq + n), 2, 64
+    k, v, q = bf16(g, b, 1, n, d), bf16(g, b, 1, n, d), bf16(g, b, hq, d)
+    q[..., 0] = 0.5
+    for at in (0, n // 2, n - 1):
+        kk = k.clone()
+        kk[:, 0, at, 0] = -LOWEST
+        out, lse, score = LQ.bf16_decode_attn_scored(LQ.Bf16Cache(kk, v, hq), q, i32([n] * b), n, None,
+                                                     score_out=torch.zeros(b, 1, n, device="cuda"))
+        LQ.fault_check()
+        assert torch.equal(out, v[:, :, at].float().expand(b, hq, d)) and (score[:, 0, at] == hq).all()
+        assert (score.sum(2) == hq).all() and ((lse / (-0.5 * LOWEST / math.sqrt(d)) - 1).abs() <= 2.0 ** -20).all()
