@@ -402,10 +402,13 @@ __global__ void __launch_bounds__(kScoreThreads) bf16_scored_merge_kernel(const 
     const size_t row = ((size_t)b * a.Hkv + h) * a.Nmax;
     const float *s0 = a.ws_s + ((size_t)b * a.Hq + h * QPK) * a.sstride;
     const int n1 = min(n0 + kScoreChunk, len);
+    float l2[QPK];                                         // a head without weight gives none: exp2(-inf - inf)
+#pragma unroll
+    for (int g = 0; g < QPK; ++g) l2[g] = s_l2[g] == -CUDART_INF_F ? CUDART_INF_F : s_l2[g];
     for (int n = max(n0, st) + tid; n < n1; n += kScoreThreads) {
         float w = 0.f;
 #pragma unroll
-        for (int g = 0; g < QPK; ++g) w += ex2(s0[(size_t)g * a.sstride + n] - s_l2[g]);
+        for (int g = 0; g < QPK; ++g) w += ex2(s0[(size_t)g * a.sstride + n] - l2[g]);
         a.score_out[row + n] = (a.score_in ? a.score_in[row + n] : 0.f) + w;
     }
 }

@@ -658,6 +658,12 @@ __global__ void __launch_bounds__(RowsPlan<D, NR, C, PG>::kThreads, 1)
                 }
                 if constexpr (SCORES) {
                     const size_t row = ((size_t)x.b * a.Hkv + x.h) * a.head_rows;
+                    float l2[8];                                     // a head without weight gives none: exp2(-inf - inf)
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        l2[k] = coef[3 * NR + k];
+                        if (l2[k] == -CUDART_INF_F) l2[k] = CUDART_INF_F;
+                    }
 #pragma unroll
                     for (int q = 0; q < kDirectTiles / 2; ++q) {
                         const int n = x.tok_first + (2 * q + w) * NT + token;
@@ -665,7 +671,7 @@ __global__ void __launch_bounds__(RowsPlan<D, NR, C, PG>::kThreads, 1)
                             float sum = 0.f;
 #pragma unroll
                             for (int k = 0; k < 8; ++k)
-                                if (k < a.R) sum += ex2(kept[q][k] - coef[3 * NR + k]);
+                                if (k < a.R) sum += ex2(kept[q][k] - l2[k]);
                             a.score_out[row + n] = (a.score_in ? a.score_in[row + n] : 0.f) + sum;
                         }
                     }

@@ -316,3 +316,27 @@ def test_scored_decode_with_scores_far_from_zero(hq, n):
         LQ.fault_check()
         assert torch.equal(out, v[:, :, at].float().expand(b, hq, d)) and (score[:, 0, at] == hq).all()
         assert (score.sum(2) == hq).all() and ((lse / (-0.5 * LOWEST / math.sqrt(d)) - 1).abs() <= 2.0 ** -20).all()
+
+
+@pytest.mark.parametrize("hq,n", [(2, 300), (8, 300), (4, 1500), (8, 5000)])
+def test_heads_whose_every_score_is_minus_infinity_weigh_nothing(hq, n):
+    """Beside heads of the same KV head that have weight: no output, a log-sum-exp of -inf (or the other part's), and no trace
+    in the scores.  A KV head of nothing but such heads leaves its scores as they were."""
+    g, b, hkv, d = gen(n + hq), 2, 2, 64
+    k, v, q = bf16(g, b, hkv, n, d), bf16(g, b, hkv, n, d), bf16(g, b, hq, d)
+    k[..., 0], q[..., 0] = LOWEST, 2.0 ** -126                       # adds about -4 to an ordinary head's sums
+    q[0, 0, 0], q[1, hq // 2:, 0] = 64, 64                           # overflows to -inf: one head; a KV head's all
+    score = torch.rand(b, hkv, n, generator=g, device="cuda")
+    other = torch.randn(b, hq, d, generator=g, device="cuda"), torch.randn(b, hq, generator=g, device="cuda")
+    for o in (None, other):
+        out, lse, s = LQ.bf16_decode_attn_scored(LQ.Bf16Cache(k, v, hq), q, i32([n] * b), n, score, other=o,
+                                                 score_out=torch.zeros_like(score))
+        LQ.fault_check()
+        for i in range(b):
+            want = fp64_attention(q[i], k[i], v[i], None if o is None else (o[0][i], o[1][i]))
+            close(out[i], lse[i], want)
+            total = score[i].double() + want[3]
+            assert ((s[i].double() - total).abs() <= GROW * 2e-4 * want[3] + 2.0 ** -23 * total).all()
+        assert torch.equal(s[1, 1], score[1, 1])
+        if o is not None:
+            assert torch.equal(out[0, 0], o[0][0, 0]) and torch.allclose(lse[0, 0], o[1][0, 0], rtol=1e-6, atol=0)
