@@ -17,6 +17,8 @@
 // slots of a CTA are combined in shared memory as in the coded kernel.
 // Keys in the cache are already rotated (RoPE at write time), so no rotation
 // happens here.
+#include <cfloat>
+
 #include "shared_rows.cuh"
 
 namespace loopvq {
@@ -120,8 +122,8 @@ __global__ void __launch_bounds__(WARPS * 32, MINB) bf16_split_kernel(const Bf16
     float2 o[QPK][4];
 #pragma unroll
     for (int j = 0; j < QPK; ++j) {
-        m_[j] = -CUDART_INF_F;
-        l_[j] = 0.f;
+        m_[j] = -FLT_MAX;                                  // no maximum yet: exp2 of a score of -inf is 0 against it, any
+        l_[j] = 0.f;                                       // other score passes it (only the lowest itself, which weighs 1)
 #pragma unroll
         for (int i = 0; i < 4; ++i) o[j][i] = f2(0.f, 0.f);
     }
@@ -225,18 +227,19 @@ __global__ void __launch_bounds__(WARPS * 32, MINB) bf16_split_kernel(const Bf16
     for (int it = tid; it < QPK * D; it += NT) {
         const int d = it % D;
         const int hq = it / D;
-        float mx = -CUDART_INF_F;
+        float mx = -FLT_MAX;
         for (int s2 = 0; s2 < NSLOT; ++s2) mx = fmaxf(mx, red[((size_t)s2 * QPK + hq) * RS + D]);
         float acc = 0.f, lsum = 0.f;
-        if (mx != -CUDART_INF_F) {
-            for (int s2 = 0; s2 < NSLOT; ++s2) {
-                const float *rec = red + ((size_t)s2 * QPK + hq) * RS;
-                const float wgt = ex2(rec[D] - mx);
-                acc += rec[d] * wgt;
-                lsum += rec[D + 1] * wgt;
-            }
-        } else if constexpr (SCORED) {                     // scores of nothing but NaN: the maximum passes them over
-            for (int s2 = 0; s2 < NSLOT; ++s2) lsum += red[((size_t)s2 * QPK + hq) * RS + D + 1];
+        for (int s2 = 0; s2 < NSLOT; ++s2) {
+            const float *rec = red + ((size_t)s2 * QPK + hq) * RS;
+            const float wgt = ex2(rec[D] - mx);
+            acc += rec[d] * wgt;
+            lsum += rec[D + 1] * wgt;
+        }
+        if (mx == -FLT_MAX && !(lsum > 0.f)) {             // no score but -inf (or NaN, which the maximum passes over)
+            mx = -CUDART_INF_F;
+            acc = 0.f;
+            if (!SCORED || lsum == 0.f) lsum = 0.f;        // the scored merge makes the row NaN
         }
         const size_t bh = (size_t)b * a.Hq + h * QPK + hq;
         a.ws_o[(bh * a.nsplit + split) * D + d] = acc;

@@ -340,3 +340,39 @@ def test_heads_whose_every_score_is_minus_infinity_weigh_nothing(hq, n):
         assert torch.equal(s[1, 1], score[1, 1])
         if o is not None:
             assert torch.equal(out[0, 0], o[0][0, 0]) and torch.allclose(lse[0, 0], o[1][0, 0], rtol=1e-6, atol=0)
+
+
+@pytest.mark.parametrize("kind", ["inf", "lowest"])
+@pytest.mark.parametrize("which", ["first", "tiles", "every_other", "all"])
+@pytest.mark.parametrize("hq,n", [(2, 300), (2, 1500), (2, 9000), (4, 1500), (16, 300)])
+def test_decode_with_scores_of_minus_infinity(hq, n, which, kind):
+    """The kernel that splits a sequence's tokens: with scores (one head per KV head) and without (any)."""
+    if kind == "lowest" and which == "all":
+        pytest.skip("rounding decides among scores of -1e37")
+    g, b, hkv, d = gen(n + hq), 2, 2, 64
+    k, v, q = masked_case(g, b, hkv, hq, n, d, spots(which, n), kind)
+    cache, lens, score = LQ.Bf16Cache(k, v, hq), i32([n, n - 1]), torch.rand(b, hkv, n, generator=g, device="cuda")
+    out, lse = LQ.bf16_decode_attn(cache, q, lens, n)
+    scored = LQ.bf16_decode_attn_scored(cache, q, lens, n, score, score_out=score.clone())
+    for i, m in enumerate(lens.tolist()):
+        want = fp64_attention(q[i], k[i, :, :m], v[i, :, :m])
+        if kind == "lowest" and which == "tiles" and m == n - 1 == 299:
+            # nothing but scores of about -2e37 is left, which fp32 holds to 2^101: it cannot tell them apart, fp64 does
+            assert out[i].isfinite().all() and scored[0][i].isfinite().all()
+            continue
+        close(out[i], lse[i], want)
+        close(scored[0][i], scored[1][i], want)
+        total = score[i, :, :m].double() + want[3]
+        assert ((scored[2][i, :, :m].double() - total).abs() <= GROW * 2e-4 * want[3] + 2.0 ** -23 * total).all()
+
+
+def test_decode_of_nan_queries_as_before():
+    """Of nothing but NaN the decode without scores makes zeros and -inf (as it did), the scored one NaN."""
+    g, n = gen(40), 3000
+    cache = LQ.Bf16Cache(bf16(g, 1, 1, n, 64), bf16(g, 1, 1, n, 64), 1)
+    q = bf16(g, 1, 1, 64)
+    q[0, 0, 3] = math.nan
+    out, lse = LQ.bf16_decode_attn(cache, q, i32([n]), n)
+    assert (out == 0).all() and (lse == -math.inf).all()
+    out, lse, score = LQ.bf16_decode_attn_scored(cache, q, i32([n]), n, None, score_out=torch.zeros(1, 1, n, device="cuda"))
+    assert out.isnan().all() and lse.isnan().all() and score.isnan().all()
