@@ -126,6 +126,11 @@ constexpr int kDirectTilesM = 3, kDirectTilesCoded = 4, kManyRows = 2048;
 // tokens are off by 2.9e-6 with two parts, 5.8e-7 with three (3 bf16 tiles 12.3 us against 10.8, 4 coded ones 14.9 / 13.1).
 constexpr int kFineTokens = 512;
 
+// Tokens that a stream of the kernel with rows as M adds into one O before that moves to a sum in the workspace.  Values of
+// one sign (1 + N(0, 0.1)) are off by, and 2000 queries, 16 heads, 32768 tokens take: 512 tokens 2.1e-6, 841 us; 1024 3.8e-6,
+// 754; 2048 7.9e-6, 709; 4096 1.9e-5, 690; never 2.2e-4, 668.  P's two parts may be off by 7.6e-6 themselves.
+constexpr int kRunTokens = 2048;
+
 // Splits: a CTA owns an SM (its tiles fill shared memory), so the splits that fill whole waves of 148 CTAs are
 // compared by waves x (tiles per split + set-up), the set-up and drain of a CTA counted as two tiles.
 SharedPlan plan_shared(int Hkv, int R, int max_len, bool coded) {
@@ -161,13 +166,19 @@ SharedPlan plan_shared(int Hkv, int R, int max_len, bool coded) {
     if (!p.few && p.nsplit == 1) p.direct = true;                    // enough rows to fill the SMs: nothing to merge
     p.fine = !p.few && p.direct && p.mb == 1 && tiles * nt <= kFineTokens;
     p.nrec = p.direct ? 0 : p.few ? 2 * p.nsplit : p.nsplit;         // a CTA's two streams write a record each
+    const long most = (tiles + p.nsplit - 1) / p.nsplit;             // tiles of a CTA; with one block of rows its streams share them
+    p.run = !p.few && (p.mb == 2 ? most : (most + 1) / 2) > kRunTokens / nt ? kRunTokens / nt : 0;
     return p;
 }
 
 size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 
-size_t ws_bytes(const SharedPlan &p, size_t RT, int D) {
-    return p.nrec == 0 ? 0 : align256(p.nrec * RT * D * sizeof(float)) + p.nrec * RT * sizeof(float2);
+// Records (O, then maxima and sums), then the sums of runs.
+size_t record_bytes(const SharedPlan &p, size_t RT, int D) {
+    return p.nrec == 0 ? 0 : align256(p.nrec * RT * D * sizeof(float)) + align256(p.nrec * RT * sizeof(float2));
+}
+size_t ws_bytes(const SharedPlan &p, int Hkv, size_t RT, int D) {
+    return record_bytes(p, RT, D) + (p.run == 0 ? 0 : (size_t)p.nsplit * Hkv * p.nz * 2 * 128 * D * sizeof(float));
 }
 
 // cuTensorMapEncodeTiled through the runtime: the library does not link the driver.
@@ -230,6 +241,8 @@ SharedArgs common_args(int rows, int Hkv, int Hq, int D, const SharedPlan &p, co
     a.ws_o = reinterpret_cast<float *>(workspace);
     a.ws_ml = reinterpret_cast<float2 *>(reinterpret_cast<char *>(workspace) +
                                          align256(p.nrec * (size_t)rows * Hq * D * sizeof(float)));
+    a.run = p.run > 0 ? p.run : INT32_MAX;
+    a.ws_run = reinterpret_cast<float4 *>(reinterpret_cast<char *>(workspace) + record_bytes(p, (size_t)rows * Hq, D));
     a.wait_ns = wait_limit_ns();
     return a;
 }
@@ -282,7 +295,7 @@ cudaError_t launch_rows_scored(const loopvq_bf16_cache &c, const uint16_t *q, co
 }
 
 size_t shared_ws_bytes(int Hkv, int Hq, int D, int rows, int max_len, bool coded) {
-    return ws_bytes(plan_shared(Hkv, rows * (Hq / Hkv), max_len, coded), (size_t)rows * Hq, D);
+    return ws_bytes(plan_shared(Hkv, rows * (Hq / Hkv), max_len, coded), Hkv, (size_t)rows * Hq, D);
 }
 
 cudaError_t launch_bf16_shared(const loopvq_bf16_cache &c, int seq, const uint16_t *q, int rows, const int32_t *starts,

@@ -11,13 +11,14 @@ struct SharedPlan {
     bool direct;             // one CTA per KV head (and block of rows), which writes the result itself
     bool fine;               // shared_attn_kernel with P and rebuilt keys in three bf16 parts, tiles of 64 tokens
     int mb, nsplit, nz, nrec;
+    int run;                 // tiles of a stream after which its O leaves tensor memory; 0: never
 };
 
-template <int D, int MB, int C, bool PG, bool FINE>
+template <int D, int MB, int C, bool PG, bool FINE, bool RUNS>
 inline cudaError_t launch_t(const SharedArgs &a, const SharedPlan &p, const CUtensorMap &km, const CUtensorMap &vm,
                      cudaStream_t s) {
     using PL = Plan<D, MB, C, PG, FINE>;
-    auto kern = shared_attn_kernel<D, MB, C, PG, FINE>;
+    auto kern = shared_attn_kernel<D, MB, C, PG, FINE, RUNS>;
     cudaError_t e = ensure_dynamic_smem((const void *)kern, PL::kAlloc);
     if (e != cudaSuccess) return e;
     return launch_pdl(kern, dim3(p.nsplit, a.Hkv, p.nz), PL::kThreads, PL::kAlloc, s, a, km, vm);
@@ -87,8 +88,10 @@ inline cudaError_t launch_p(const SharedArgs &a, const SharedPlan &p, const CUte
         x.out = out;
         x.lse = lse;
     }
-    if (p.fine) return launch_t<D, 1, C, PG, true>(x, p, km, vm, s);
-    return p.mb == 2 ? launch_t<D, 2, C, PG, false>(x, p, km, vm, s) : launch_t<D, 1, C, PG, false>(x, p, km, vm, s);
+    if (p.fine) return launch_t<D, 1, C, PG, true, false>(x, p, km, vm, s);
+    if (p.run > 0)
+        return p.mb == 2 ? launch_t<D, 2, C, PG, false, true>(x, p, km, vm, s) : launch_t<D, 1, C, PG, false, true>(x, p, km, vm, s);
+    return p.mb == 2 ? launch_t<D, 2, C, PG, false, false>(x, p, km, vm, s) : launch_t<D, 1, C, PG, false, false>(x, p, km, vm, s);
 }
 
 template <int C, bool PG>

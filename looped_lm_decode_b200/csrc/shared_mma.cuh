@@ -19,6 +19,10 @@
 // accumulator, or three where tokens are few (FINE); a rebuilt, rotated key is split the same way.  bf16 queries, keys
 // and values are exact.
 //
+// The tensor cores cut their fp32 sums toward zero at every product, so values of one sign come out low by as much as there
+// are products: 256 tiles in a row (2000 query rows, 32768 tokens) 2.2e-4.  Every 2048 tokens (256 products: 6e-6) a
+// stream therefore adds its O to a sum in the workspace and starts afresh: 8e-6 there, for 709 us instead of 668.
+//
 // P overwrites S in place, 16 score columns becoming 8 + 8 columns of packed pairs (one product's tokens; a third part
 // has columns of its own).  The running maximum moves only when a tile passes it by 2^8 (any reference is exact; it
 // bounds P), so O is rarely rescaled.
@@ -52,6 +56,9 @@ struct SharedArgs {
     const uint16_t *slk, *slv;
     const float *rope;
     int K;
+    // tiles of a stream after which O leaves tensor memory (run), and where it is summed: [CTA][stream][D / 4][128][4]
+    int run;
+    float4 *ws_run;
     // one split: the kernel writes the result itself, merged with the other part (null where there is none)
     const float *other_out, *other_lse;
     float *out, *lse;        // out null: records for the merge; lse may be null
@@ -101,7 +108,8 @@ constexpr int kTmemCols = 512;                                       // O of str
 template <int D, int NT, int PARTS>
 struct RowSoftmax {
     float m, l;                                                      // maximum reference (log2 units), sum
-    bool far = false;                                                // some row of the warp's is past kExact
+    bool far;                                                        // some row of the warp's is past kExact
+    float carry;                                                     // factor that brings the sum of earlier runs to m
     static constexpr float kExact = 16777216.f;                      // scores up to here are held to 2 log2 units
 
     // S columns at ts (a third part of P goes to tp); tokens [lo, hi) of the tile count; O columns at to.  first: O holds
@@ -141,6 +149,7 @@ struct RowSoftmax {
             const float corr = up ? ex2(m - mt) : 1.f;
             if (up) m = mt;
             l *= corr;
+            carry *= corr;
             far = __any_sync(0xffffffffu, fabsf(m) > kExact && m != -CUDART_INF_F);
             if (!first) {
                 const bool ok = tc::mbar_wait_or_dead(odone, odone_parity, limit, dead);
@@ -203,12 +212,40 @@ struct RowSoftmax {
         tc::tmem_wait_st();
         return true;
     }
+
+    // O at `to` is added to the sum of the runs before (more) at `sum`, in fp32 rounded to nearest; the next product starts
+    // O afresh.
+    __device__ __forceinline__ void end_run(uint32_t to, float4 *sum, bool more) {
+#pragma unroll 1
+        for (int k0 = 0; k0 < D; k0 += 32) {
+            uint32_t o[32];
+            tc::tmem_ld32(to + k0, o);
+            tc::tmem_wait_ld(o);
+            if (more) add_runs(o, sum, k0);
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                sum[(k0 / 4 + k) * 128] = make_float4(__uint_as_float(o[4 * k]), __uint_as_float(o[4 * k + 1]),
+                                                      __uint_as_float(o[4 * k + 2]), __uint_as_float(o[4 * k + 3]));
+        }
+        carry = 1.f;
+    }
+    __device__ __forceinline__ void add_runs(uint32_t (&o)[32], const float4 *sum, int k0) const {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const float4 y = sum[(k0 / 4 + k) * 128];
+            o[4 * k] = __float_as_uint(fmaf(y.x, carry, __uint_as_float(o[4 * k])));
+            o[4 * k + 1] = __float_as_uint(fmaf(y.y, carry, __uint_as_float(o[4 * k + 1])));
+            o[4 * k + 2] = __float_as_uint(fmaf(y.z, carry, __uint_as_float(o[4 * k + 2])));
+            o[4 * k + 3] = __float_as_uint(fmaf(y.w, carry, __uint_as_float(o[4 * k + 3])));
+        }
+    }
 };
 
 // D channels (64 or 128), MB blocks of 128 query rows per CTA, C = 0 for a bf16 cache or the channels per code of
 // a coded one; PG: one codebook per channel group, whose slices (128 bytes per entry and more) do not fit beside
-// the tiles and are gathered from L2.
-template <int D, int MB, int C, bool PG, bool FINE>
+// the tiles and are gathered from L2.  RUNS: O leaves tensor memory every a.run tiles of a stream (as a test of a.run in one
+// kernel for both: 16347 tokens, 64 grouped queries 26.4 us against 26.0).
+template <int D, int MB, int C, bool PG, bool FINE, bool RUNS>
 __global__ void __launch_bounds__(Plan<D, MB, C, PG, FINE>::kThreads, 1)
     shared_attn_kernel(const SharedArgs a, const __grid_constant__ CUtensorMap kmap,
                        const __grid_constant__ CUtensorMap vmap) {
@@ -377,17 +414,24 @@ __global__ void __launch_bounds__(Plan<D, MB, C, PG, FINE>::kThreads, 1)
         const uint32_t ts = tmem + lane_base + w * P::colS, to = tmem + lane_base + 256 + w * 128;
         const int rq = r0 + (MB == 2 ? w * 128 : 0) + row;           // query row of this thread
         const bool any = __any_sync(0xffffffffu, rq < a.R);          // warps of padding only keep step
-        RowSoftmax<D, NT, P::PARTS> sm{-CUDART_INF_F, 0.f, false};
+        RowSoftmax<D, NT, P::PARTS> sm{-CUDART_INF_F, 0.f, false, 1.f};
         bool ok = true;
-        int j = 0;
-        for (int i = w; i < nsteps; i += 2, ++j) {
+        int j = 0, in_run = 0;                                       // tiles of the stream, and of its O
+        [[maybe_unused]] float4 *runs = a.ws_run + ((((size_t)blockIdx.z * a.Hkv + h) * a.nsplit + split) * 2 + w) * (D / 4) * 128 + row;
+        for (int i = w; i < nsteps; i += 2, ++j, ++in_run) {
             const int t = MB == 2 ? j : i;
             ok = __all_sync(0xffffffffu, tc::mbar_wait_or_dead(sfull(w), j & 1, a.wait_ns, dead));
             if (!ok) break;
             tc::tc_fence_after();
+            if constexpr (RUNS) {
+                if (in_run == a.run) {                               // (S of this step is behind the last product of O)
+                    if (any) sm.end_run(to, runs, j > in_run);
+                    in_run = 0;
+                }
+            }
             if (any) {
                 const int n0 = tok_first + t * NT;
-                ok = sm.tile(ts, tmem + lane_base + P::colP3 + w * 32, to, st - n0, len - n0, a.qscale, j == 0, odone(w),
+                ok = sm.tile(ts, tmem + lane_base + P::colP3 + w * 32, to, st - n0, len - n0, a.qscale, in_run == 0, odone(w),
                              (j - 1) & 1, a.wait_ns, dead);
                 if (!ok) break;
             }
@@ -427,6 +471,7 @@ __global__ void __launch_bounds__(Plan<D, MB, C, PG, FINE>::kThreads, 1)
                     if (j > 0) {
                         tc::tmem_ld32(to + c, o);
                         tc::tmem_wait_ld(o);
+                        if (RUNS && j > in_run) sm.add_runs(o, runs, c);
                     } else {
 #pragma unroll
                         for (int k = 0; k < 32; ++k) o[k] = 0u;
@@ -465,6 +510,7 @@ __global__ void __launch_bounds__(Plan<D, MB, C, PG, FINE>::kThreads, 1)
                 uint32_t o[32];
                 tc::tmem_ld32(to + c, o);
                 tc::tmem_wait_ld(o);
+                if (RUNS && j > in_run) sm.add_runs(o, runs, c);
                 if (rq < a.R) {
                     float4 *rec_o = reinterpret_cast<float4 *>(a.ws_o) + (rec / a.R * (D / 4) + c / 4) * a.R + rq;
 #pragma unroll
@@ -529,6 +575,7 @@ __global__ void __launch_bounds__(Plan<D, MB, C, PG, FINE>::kThreads, 1)
             }
             __syncwarp();
         };
+        int in_run = 0;                                              // tiles in the O of this step's stream
         qk(0);
         if (ok && nsteps > 1) qk(1);
         for (int i = 0; ok && i < nsteps; ++i) {
@@ -551,7 +598,7 @@ __global__ void __launch_bounds__(Plan<D, MB, C, PG, FINE>::kThreads, 1)
             tc::tc_fence_after();
             const uint32_t od = tc::uniform(tmem + 256 + w * 128), pa = tc::uniform(tmem + w * P::colS);
             [[maybe_unused]] const uint32_t pz = tc::uniform(tmem + P::colP3 + w * 32);
-            const uint32_t v_lo = tc::uniform(tc::desc_lo(vb, P::kPanel)), more = tc::uniform(i > 1);
+            const uint32_t v_lo = tc::uniform(tc::desc_lo(vb, P::kPanel)), more = tc::uniform(in_run != 0);
             if (tc::elect_one()) {
 #pragma unroll
                 for (int part = 0; part < P::PARTS; ++part)
@@ -563,6 +610,7 @@ __global__ void __launch_bounds__(Plan<D, MB, C, PG, FINE>::kThreads, 1)
                 tc::mma_commit(odone(w));
             }
             __syncwarp();
+            if (w == 1 && ++in_run == a.run && RUNS) in_run = 0;
             if (i + 2 < nsteps) qk(i + 2);
         }
     } else if constexpr (!coded) {

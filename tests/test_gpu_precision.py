@@ -1,0 +1,78 @@
+"""How exact the shared-prefix and scored attention are where a rule of their kernels says so.
+
+The tensor cores add in fp32 and cut each sum to 24 bits toward zero: a product's sum loses less than 2^-23 of itself, so N
+products in a row that add values of one sign lose less than N / 2 * 2^-23 of the result (the sums grow evenly).  With queries
+of zeros every score is 0 and every weight exactly 1, and what is left is that, and some fp32 roundings of 2^-24 each."""
+import math
+
+import pytest
+import torch
+
+import looped_lm_decode_b200 as LQ
+from tests.test_gpu_edges import bf16, gen, i32
+
+pytestmark = pytest.mark.gpu
+
+CUT = 2.0 ** -23
+
+
+def positive(g, *shape):
+    """Of many magnitudes: sums of many of them need more than 24 bits."""
+    return torch.randn(*shape, generator=g, device="cuda").exp().bfloat16()
+
+
+def off(out, v):
+    """The largest relative error of out [rows][Hq][D] against the means of v [Hkv][n][D]."""
+    want = v.double().mean(1).repeat_interleave(out.shape[1] // v.shape[0], 0)
+    return ((out.double() - want) / want).abs().max().item()
+
+
+@pytest.mark.parametrize("n,rows,hkv,hq,d", [(32768, 2048, 16, 16, 128), (32768, 200, 16, 16, 128), (30001, 600, 40, 40, 64),
+                                             (70001, 40, 40, 40, 64), (131072, 64, 4, 16, 128)])
+def test_rows_as_m_do_not_drift_over_long_prefixes(n, rows, hkv, hq, d):
+    """At most 2048 tokens, 128 products of weights with a remainder of 0, in a run; then sums of at most 64 runs and some
+    twenty roundings of the merge and the division."""
+    g = gen(n + rows)
+    k, v = bf16(g, 1, hkv, n, d), positive(g, 1, hkv, n, d)
+    out, lse = LQ.bf16_shared_attn(LQ.Bf16Cache(k, v, hq), 0, torch.zeros(rows, hq, d, dtype=torch.bfloat16, device="cuda"), i32([n]), n)
+    LQ.fault_check()
+    assert off(out, v[0]) <= 128 / 2 * CUT + (64 + 20) * 2.0 ** -24
+    assert (lse - math.log(n)).abs().max().item() <= 2.0 ** -23 * math.log(n) + 1e-5
+
+
+def test_runs_with_a_rising_maximum_and_an_other_part():
+    """Sums of runs follow the maximum: scores that rise by 2^8 and more from run to run, and fall again."""
+    g, n, rows, d = gen(2), 32768, 2000, 64
+    k, v, q = bf16(g, 1, 16, n, d), bf16(g, 1, 16, n, d), bf16(g, rows, 16, d)
+    q[..., 0] = 8
+    t = torch.linspace(-1, 1, n, device="cuda")
+    k[0, :, :, 0] = (40 * torch.where(t < 0.4, t, 0.8 - t)).bfloat16()
+    other = torch.randn(rows, 16, d, generator=g, device="cuda"), 10 + torch.randn(rows, 16, generator=g, device="cuda")
+    for o in (None, other):
+        out, lse = LQ.bf16_shared_attn(LQ.Bf16Cache(k, v, 16), 0, q, i32([n]), n, other=o)
+        LQ.fault_check()
+        for r, h in ((0, 0), (777, 7), (1999, 15)):
+            s = k[0, h].double() @ q[r, h].double() / math.sqrt(d)
+            l = torch.logsumexp(s, 0)
+            joint = l if o is None else torch.logaddexp(l, o[1][r, h].double())
+            p = torch.exp(s - joint)
+            want, mag = p @ v[0, h].double(), p @ v[0, h].double().abs()
+            if o is not None:
+                po = torch.exp(o[1][r, h].double() - joint)
+                want, mag = want + po * o[0][r, h].double(), mag + po * o[0][r, h].double().abs()
+            # |q k| scale reaches 48: test_gpu_shared.py's bounds for sums below 8, times 7
+            assert ((out[r, h].double() - want).abs() <= 7 * 2.5e-4 * mag).all()
+            assert abs(lse[r, h].item() - joint.item()) <= 7e-4
+
+
+def test_an_other_part_in_place_with_runs():
+    g, n, rows, d = gen(3), 32768, 2000, 64
+    k, v, q = bf16(g, 1, 16, n, d), bf16(g, 1, 16, n, d), bf16(g, rows, 16, d)
+    cache, lens = LQ.Bf16Cache(k, v, 16), i32([n])
+    other = torch.randn(rows, 16, d, generator=g, device="cuda"), 10 + torch.randn(rows, 16, generator=g, device="cuda")
+    want = LQ.bf16_shared_attn(cache, 0, q, lens, n, other=other)
+    again = LQ.bf16_shared_attn(cache, 0, q, lens, n, other=other)
+    assert torch.equal(want[0], again[0]) and torch.equal(want[1], again[1])
+    out = other[0].clone()
+    LQ.bf16_shared_attn(cache, 0, q, lens, n, other=(out, other[1]), out=out)
+    assert torch.equal(out, want[0])
