@@ -100,7 +100,7 @@ class OnHost:
 
 def aligned(n, off=0):
     """n bf16 elements at an address that is a multiple of 16, or two bytes behind one."""
-    x = torch.zeros(n + 16, dtype=torch.bfloat16)
+    x = torch.empty(n + 16, dtype=torch.bfloat16)                    # (never read; filling it would start threads)
     at = (-x.data_ptr() // 2) % 8 + off
     return x[at:at + n]
 
@@ -115,10 +115,11 @@ def test_a_refused_cache_leaves_no_size_behind(monkeypatch, op):
     """The library answers a size of 0 for a cache that it refuses; a right call of the same shape gets its own."""
     host = OnHost(monkeypatch)
     odd, right = odd_and_right(2, 32768, 64, 2)
-    q, lens, score = torch.zeros(1, 2, 64, dtype=torch.bfloat16), torch.zeros(1, dtype=torch.int32), torch.zeros(1, 2, 32768)
+    q, lens, score = torch.zeros(1, 2, 64, dtype=torch.bfloat16), torch.zeros(1, dtype=torch.int32), torch.empty(1, 2, 32768)
+    pos = torch.empty(1, 2, 32768, dtype=torch.int32)
     call = dict(shared=lambda c: LQ.bf16_shared_attn(c, 0, q, lens, 32768),
                 scored=lambda c: LQ.bf16_decode_attn_scored(c, q, lens, 32768, score),
-                evict=lambda c: LQ.bf16_evict(c, score, score.int(), lens, lens, 32768, 100, 4, 8))[op]
+                evict=lambda c: LQ.bf16_evict(c, score, pos, lens, lens, 32768, 100, 4, 8))[op]
     with pytest.raises(LQ.LoopVQError):
         call(odd)
     call(right)
@@ -166,13 +167,14 @@ def test_own_memory_is_made_on_the_stream_that_uses_it(monkeypatch, stream):
     monkeypatch.setattr(torch.cuda, "current_stream", lambda: None)
     monkeypatch.setattr(torch.Tensor, "record_stream", lambda *_: None)
     _, cache = odd_and_right(2, 32768, 64, 2)
-    q, lens, score = torch.zeros(1, 2, 64, dtype=torch.bfloat16), torch.zeros(1, dtype=torch.int32), torch.zeros(1, 2, 32768)
+    q, lens, score = torch.zeros(1, 2, 64, dtype=torch.bfloat16), torch.zeros(1, dtype=torch.int32), torch.empty(1, 2, 32768)
+    pos = torch.empty(1, 2, 32768, dtype=torch.int32)
     coded = LQ.Cache(1, 4, 4, 2, 2, 64, 4, 256, 1, 32768, alloc=False)
     coded.idx = coded.codebook = coded.slices = coded.rope = torch.zeros(16)
     LQ.bf16_shared_attn(cache, 0, q, lens, 32768, stream=stream)
     LQ.shared_attn(coded, 0, 0, 0, q, lens, 32768, stream=stream)
     LQ.bf16_decode_attn_scored(cache, q, lens, 32768, score, stream=stream)
-    LQ.bf16_evict(cache, score, score.int(), lens, lens, 32768, 100, 4, 8, stream=stream)
+    LQ.bf16_evict(cache, score, pos, lens, lens, 32768, 100, 4, 8, stream=stream)
     assert made == [stream] * 10                                     # three results and workspaces, and evict's workspace
 
 
@@ -196,7 +198,7 @@ def test_own_memory_of_every_decode_call(monkeypatch, stream):
     monkeypatch.setattr(binding, "lib", lambda: Lib())
     cache = LQ.Cache(1, 4, 4, 2, 2, 64, 4, 256, 1, 512, alloc=False)
     bf = LQ.Bf16Cache(aligned(2 * 512 * 64).view(1, 2, 512, 64), aligned(2 * 512 * 64).view(1, 2, 512, 64), 2)
-    tasq, win = LQ.Tasq(cache, device="cpu"), LQ.Window(cache, device="cpu")
+    tasq, win = LQ.Tasq(cache, device="cpu"), LQ.Window(cache, 8, 8, device="cpu")
     q, lens = torch.zeros(1, 2, 64, dtype=torch.bfloat16), torch.zeros(1, dtype=torch.int32)
     kv, part = torch.zeros(1, 2, 64, dtype=torch.bfloat16), (torch.zeros(1, 2, 64), torch.zeros(1, 2))
     on = dict(stream=stream)
