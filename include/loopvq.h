@@ -239,7 +239,8 @@ size_t loopvq_shared_workspace_bytes(const loopvq_cache *cache, int rows, int ma
  *
  * seq        0 <= seq < B: the sequence that holds the prefix.
  * q          bf16 [rows][Hq][D], rotated at the queries' positions, 16-byte aligned.
- * rows       >= 0 query tokens (of any number of sequences); 0 launches nothing.
+ * rows       >= 0 query tokens (of any number of sequences; rows * Hq / Hkv up to
+ *            65535 * 128); 0 launches nothing.
  * starts, lens  int32 [B] device (starts may be NULL); the entries of seq are
  *            read and clamped as in loopvq_decode_attn_range.
  * max_len    host upper bound of len, 0 <= max_len <= Nmax.
@@ -303,7 +304,7 @@ size_t loopvq_bf16_scored_workspace_bytes(const loopvq_bf16_cache *cache, int ma
  * any workspace.  Sums run in a fixed order: equal inputs give equal bits.
  * Grouped heads and short calls run on the tensor cores: waits, faults and the
  * first call on a device as in loopvq_bf16_shared_attn (scores of a KV head whose
- * wait ran out are undefined).
+ * wait ran out are undefined).  B and Hkv up to 65535, B * Hkv * Nmax < 2^31.
  */
 loopvq_status loopvq_bf16_decode_attn_scored(const loopvq_bf16_cache *cache, const uint16_t *q,
                                              const int32_t *starts, const int32_t *lens, int max_len, float scale,
@@ -337,6 +338,7 @@ size_t loopvq_bf16_evict_workspace_bytes(const loopvq_bf16_cache *cache, int max
  *           the call (anything else is refused, lens_out = next_pos too).  Written
  *           for slots n < min(len_b, budget) = lens_out_b only.
  * workspace of at least loopvq_bf16_evict_workspace_bytes bytes, 16-byte aligned.
+ * B * Hkv up to 65535.
  */
 loopvq_status loopvq_bf16_evict(const loopvq_bf16_cache *cache, const float *score_in, const int32_t *pos_in,
                                 const int32_t *lens_in, const int32_t *next_pos, int max_len, int budget,

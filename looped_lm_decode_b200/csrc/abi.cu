@@ -430,6 +430,8 @@ loopvq_status loopvq_bf16_decode_attn_scored(const loopvq_bf16_cache *c, const u
     if (!std::isfinite(scale)) return fail(LOOPVQ_ERR_INVALID_ARG, "scale is not finite");
     if (scale <= 0.f) scale = 1.0f / std::sqrt((float)c->D);
     if (c->B > 65535 || c->Hkv > 65535) return fail(LOOPVQ_ERR_UNSUPPORTED, "B or Hkv exceeds 65535");
+    if ((int64_t)c->B * c->Hkv * c->Nmax + 128 > INT32_MAX)          // rows of the tensor maps
+        return fail(LOOPVQ_ERR_UNSUPPORTED, "B * Hkv * Nmax = %lld exceeds 2^31", (long long)c->B * c->Hkv * c->Nmax);
     const loopvq::DecodePlan plan = loopvq::plan_bf16(*c, max_len);
     if (plan.nsplit > 65535) return fail(LOOPVQ_ERR_UNSUPPORTED, "too many splits");
     const size_t need = loopvq::plan_scored(*c, max_len).ws_bytes;

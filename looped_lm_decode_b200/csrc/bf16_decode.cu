@@ -458,18 +458,27 @@ static cudaError_t launch_bf16_t(const Bf16Args &a, float *out, float *lse, cuda
     return cudaGetLastError();
 }
 
+// Query heads per KV head from which the scored form runs on the tensor cores: the split kernel's fp32 products grow
+// with them (D 128, 16 ragged sequences of up to 16384 tokens, 4 KV heads, split kernel / tensor cores, us: 2 heads 67.0 /
+// 62.5, 4 heads 110 / 64.7, 8 heads 351 / 72.4; 1 head takes the split kernel 59.8, and equal lengths reach 94% of the
+// copy rate: 32 sequences of 4096 tokens, 16 heads, 176).
+constexpr int kScoredRows = 2;
+
+// One query head per KV head: the split kernel with scores, then the merge; more: the merge behind the tensor-core kernel.
 template <int D, int QPK>
 static cudaError_t launch_bf16_scored_t(const Bf16Args &a, float *out, float *lse, cudaStream_t s) {
-    constexpr int NSLOT = kBfWarps * (32 / (D / 8));
-    const size_t smem = bf16_smem_bytes();
-    if ((size_t)NSLOT * QPK * (D + 4) * sizeof(float) > smem) return cudaErrorInvalidConfiguration;
-    auto kern = bf16_split_kernel<D, QPK, kBfWarps, kBfMinBlocks, kBfDepth, true>;
-    cudaError_t e = ensure_dynamic_smem((const void *)kern, smem);
-    if (e != cudaSuccess) return e;
-    if (a.nsplit > 0) {
-        kern<<<dim3(a.nsplit, a.Hkv, a.B), kBfWarps * 32, smem, s>>>(a);
-        e = cudaGetLastError();
+    if constexpr (QPK < kScoredRows) {
+        constexpr int NSLOT = kBfWarps * (32 / (D / 8));
+        const size_t smem = bf16_smem_bytes();
+        if ((size_t)NSLOT * QPK * (D + 4) * sizeof(float) > smem) return cudaErrorInvalidConfiguration;
+        auto kern = bf16_split_kernel<D, QPK, kBfWarps, kBfMinBlocks, kBfDepth, true>;
+        cudaError_t e = ensure_dynamic_smem((const void *)kern, smem);
         if (e != cudaSuccess) return e;
+        if (a.nsplit > 0) {
+            kern<<<dim3(a.nsplit, a.Hkv, a.B), kBfWarps * 32, smem, s>>>(a);
+            e = cudaGetLastError();
+            if (e != cudaSuccess) return e;
+        }
     }
     const unsigned chunks = (unsigned)((a.max_len + kScoreChunk - 1) / kScoreChunk) + 1;
     return launch_pdl(bf16_scored_merge_kernel<D, QPK>, dim3(chunks, a.Hkv, a.B), kScoreThreads, 0, s, a, out, lse);
@@ -487,20 +496,13 @@ static cudaError_t dispatch_bf16(int qpk, const Bf16Args &a, float *out, float *
     }
 }
 
-// Query heads per KV head from which the scored form runs on the tensor cores: the split kernel's fp32 products grow
-// with them (D 128, 16 ragged sequences of up to 16384 tokens, 4 KV heads, split kernel / tensor cores, us: 2 heads 67.0 /
-// 62.5, 4 heads 110 / 64.7, 8 heads 351 / 72.4; 1 head takes the split kernel 59.8, and equal lengths reach 94% of the
-// copy rate: 32 sequences of 4096 tokens, 16 heads, 176).
-constexpr int kScoredRows = 2;
-
 ScoredPlan plan_scored(const loopvq_bf16_cache &c, int max_len) {
     ScoredPlan p{};
     const size_t heads = (size_t)c.B * c.Hq;
-    const bool fits = (int64_t)c.B * c.Hkv * c.Nmax + 128 <= INT32_MAX;   // rows of the tensor maps
     // few tokens on no more (sequence, KV head) pairs than SMs: one launch, whatever the heads
-    p.direct = fits && max_len <= kDirectTiles * 128 && c.B * c.Hkv <= kRowCtas;
+    p.direct = max_len <= kDirectTiles * 128 && (int64_t)c.B * c.Hkv <= kRowCtas;
     if (p.direct) return p;
-    p.rows = fits && c.Hq / c.Hkv >= kScoredRows;
+    p.rows = c.Hq / c.Hkv >= kScoredRows;
     // records of D values: every segment has at most a piece more than the CTAs that it spans
     const size_t records = p.rows ? ((size_t)c.B * c.Hkv + kRowCtas) * 2 * (c.Hq / c.Hkv)
                                   : heads * plan_bf16(c, max_len).nsplit;

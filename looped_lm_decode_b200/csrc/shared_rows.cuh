@@ -177,6 +177,7 @@ __global__ void __launch_bounds__(RowsPlan<D, NR, C, PG>::kThreads, 1)
                        const __grid_constant__ CUtensorMap vmap) {
     using P = RowsPlan<D, NR, C, PG>;
     constexpr bool coded = C != 0;
+    static_assert(!coded || DIRECT, "over a coded cache only calls of one launch");
     constexpr int NT = P::NT, KP = P::KP, ST = P::ST, NQ = P::NQ, PARTS = P::PARTS, NPAN = D / 64;
     constexpr float kFar = 40.f;                                     // log2 units a score may pass the reference by
     constexpr float kExact = 16777216.f;                             // scores up to here are held to 2 log2 units
@@ -237,7 +238,7 @@ __global__ void __launch_bounds__(RowsPlan<D, NR, C, PG>::kThreads, 1)
     }
     if constexpr (coded) {                                           // an item's KV head is this CTA's: one item per CTA
         if constexpr (!PG) {
-            const int h = DIRECT ? blockIdx.x % a.Hkv : blockIdx.x / a.nsplit;
+            const int h = blockIdx.x % a.Hkv;
             fill_tables<C>(smem + P::offTable, a.slk + (size_t)h * a.K * C, a.slv + (size_t)h * a.K * C, a.K, P::kThreads);
         }
         for (int i = tid; i < D; i += P::kThreads)                   // row 64 is there when a second tile is

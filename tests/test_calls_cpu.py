@@ -9,7 +9,7 @@ import torch
 
 import looped_lm_decode_b200 as LQ
 import looped_lm_decode_b200.loopvq as binding
-from tests.test_operators_cpu import A, B_, Cc, D_, INVALID, P, WORKSPACE, coded, evict, message, scored, shared
+from tests.test_operators_cpu import A, B_, Cc, D_, INVALID, P, UNSUPPORTED, WORKSPACE, coded, desc, evict, message, scored, shared
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
@@ -26,6 +26,12 @@ def test_workspace_of_no_rows():
 def test_no_rows_are_checked_like_any():
     for call in (shared, coded):
         assert call(rows=0, seq=2) == INVALID and "seq" in message()
+
+
+def test_scored_refuses_more_rows_than_its_maps_hold():
+    """2^31 rows of keys are 275 GB at 64 channels."""
+    d = desc(B=64, Hkv=1 << 10, Hq=1 << 12, D=64, Nmax=1 << 15)
+    assert scored(d, max_len=64) == UNSUPPORTED and "2^31" in message()
 
 
 # what a call writes and what it reads: A, B_, Cc, D_ lie far apart, and arrays of the small shapes end well before the next
