@@ -376,3 +376,81 @@ def test_decode_of_nan_queries_as_before():
     assert (out == 0).all() and (lse == -math.inf).all()
     out, lse, score = LQ.bf16_decode_attn_scored(cache, q, i32([n]), n, None, score_out=torch.zeros(1, 1, n, device="cuda"))
     assert out.isnan().all() and lse.isnan().all() and score.isnan().all()
+
+
+# ------------------------------------------------------------------ sizes and places no other test reaches
+
+def check_rows(out, lse, q, k, v, rows):
+    """Rows of out against fp64: q [rows][Hq][D], k and v [Hkv][n][D]."""
+    for r in rows:
+        want = fp64_attention(q[r], k, v)
+        assert ((out[r].double() - want[0]).abs() <= 2.5e-4 * want[2]).all() and ((lse[r].double() - want[1]).abs() <= 1e-4).all()
+
+
+@pytest.mark.parametrize("rows", [3, 40, 200])
+@pytest.mark.parametrize("layer,t", [(0, 0), (1, 6), (2, 3)])
+def test_coded_prefix_of_any_layer_and_block(layer, t, rows):
+    from tests.test_gpu_shared import rebuild
+    g, n, hkv, hq, d = gen(layer), 333, 2, 4, 128
+    cache = coded_cache(g, hkv, hq, d, 4, 4, 256, 336, layers=3, loops=8, seqs=3)
+    one = LQ.Cache(1, 8, 4, hkv, hq, d, 4, 256, 3, 336)              # that layer alone, for the plain form
+    one.idx.copy_(cache.idx.view(3, -1)[layer])
+    one.codebook.copy_(cache.codebook.view(3, -1)[layer])
+    LQ.prepare(one)
+    q, lens = bf16(g, rows, hq, d), i32([5, n, 9])
+    out, lse = LQ.shared_attn(cache, layer, t, 1, q, lens, 336, starts=i32([0, 6, 0]))
+    LQ.fault_check()
+    k, v = rebuild(one, t, 1, 6, n)
+    check_rows(out, lse, q, k, v, range(0, rows, 13))
+
+
+@pytest.mark.parametrize("rows,n", [(2000, 3000), (1025, 130)])
+def test_coded_prefix_of_a_prompt(rows, n):
+    from tests.test_gpu_shared import rebuild
+    g, hkv, hq, d = gen(rows), 2, 2, 128
+    cache = coded_cache(g, hkv, hq, d, 8, 4, 256, (n + 3) // 4 * 4)
+    q = bf16(g, rows, hq, d)
+    out, lse = LQ.shared_attn(cache, 0, 1, 0, q, i32([n]), n)
+    LQ.fault_check()
+    check_rows(out, lse, q, *rebuild(cache, 1, 0, 0, n), range(0, rows, 97))
+
+
+def test_as_many_rows_as_a_grid_holds():
+    """65000 blocks of 128 rows."""
+    g, rows, hq, d, n = gen(60), 1040000, 8, 64, 5
+    cache, q = LQ.Bf16Cache(bf16(g, 1, 1, 8, d), bf16(g, 1, 1, 8, d), hq), bf16(g, rows, hq, d)
+    out, lse = LQ.bf16_shared_attn(cache, 0, q, i32([n]), n)
+    LQ.fault_check()
+    check_rows(out, lse, q, cache.k[0, :, :n], cache.v[0, :, :n], [0, 1, 77777, 524287, 524288, rows - 1])
+    for a in range(0, rows, 80000):                                  # all of them, in fp32
+        s = (q[a:a + 80000].float() @ cache.k[0, 0, :n].float().T) / math.sqrt(d)
+        plain = torch.softmax(s, 2) @ cache.v[0, 0, :n].float()
+        assert (out[a:a + 80000] - plain).abs().max().item() <= 1e-3
+
+
+@pytest.mark.parametrize("hq", [18, 36])
+def test_offsets_past_two_to_the_31(hq):
+    """18 heads of a million tokens: 2.3e9 elements, the last head past 2^31."""
+    g, n, hkv, d = gen(61), 1000000, 18, 128
+    k, v = (torch.empty(1, hkv, n, d, device="cuda", dtype=torch.bfloat16).normal_(generator=g) for _ in range(2))
+    cache, start, lens = LQ.Bf16Cache(k, v, hq), n - 700, i32([n - 3])
+    for rows in (1, 50):
+        q = bf16(g, rows, hq, d)
+        out, lse = LQ.bf16_shared_attn(cache, 0, q, lens, n, starts=i32([start]))
+        LQ.fault_check()
+        check_rows(out, lse, q, k[0, :, start:n - 3], v[0, :, start:n - 3], [0, rows - 1])
+    score = torch.zeros(1, hkv, n, device="cuda")
+    q = bf16(g, 1, hq, d)
+    out, lse, score = LQ.bf16_decode_attn_scored(cache, q, lens, n, score, starts=i32([start]))
+    LQ.fault_check()
+    check_rows(out, lse, q, k[0, :, start:n - 3], v[0, :, start:n - 3], [0])
+    w = fp64_attention(q[0], k[0, :, start:n - 3], v[0, :, start:n - 3])[3]
+    assert ((score[0, :, start:n - 3].double() - w).abs() <= 2e-4 * w).all()
+    assert (score[..., :start] == 0).all() and (score[..., n - 3:] == 0).all()
+    # eviction to 4 slots behind which everything lies: the rows of the last head move, too
+    pos = torch.arange(n, device="cuda", dtype=torch.int32).expand(1, hkv, n).contiguous()
+    best = score[0].topk(4, 1).indices.sort(1).values
+    want = [k[0, h, best[h]].clone() for h in range(hkv)]
+    so, po, lo = LQ.bf16_evict(cache, score, pos, lens, i32([n]), n, 4, n_sink=0, n_recent=0)
+    assert lo.tolist() == [4] and torch.equal(po[0, :, :4].long(), best)
+    assert all(torch.equal(k[0, h, :4], want[h]) for h in range(hkv))

@@ -143,3 +143,31 @@ def test_rebuilt_keys_of_short_calls_are_held_in_fp32(rows, n):
     ref = torch.einsum("rhn,hnd->rhd", want, v)
     size = torch.einsum("rhn,hnd->rhd", want, v.abs())
     assert ((out.double() - ref).abs() <= (2 * few + 2e-6) * size).all()
+
+
+@pytest.mark.parametrize("coded", [False, True])
+def test_a_wait_that_runs_out_with_runs(coded):
+    """Rows of NaN, a fault, and the next call as before, where O had left tensor memory, too."""
+    from tests.test_gpu_edges import coded_cache
+    g, n, rows, d = gen(6), 20000, 2000 if not coded else 600, 64
+    q, lens = bf16(g, rows, 16, d), i32([n])
+    if coded:
+        cache = coded_cache(g, 16, 16, d, 4, 4, 256, n)
+        call = lambda: LQ.shared_attn(cache, 0, 1, 0, q, lens, n)  # noqa: E731
+    else:
+        cache = LQ.Bf16Cache(bf16(g, 1, 16, n, d), bf16(g, 1, 16, n, d), 16)
+        call = lambda: LQ.bf16_shared_attn(cache, 0, q, lens, n)  # noqa: E731
+    good = call()
+    LQ.fault_check()
+    before = LQ.wait_limit_ns()
+    LQ.set_wait_limit_ns(0)
+    try:
+        bad = call()
+        with pytest.raises(LQ.LoopVQError) as e:
+            LQ.fault_check()
+        assert e.value.status == 5 and bad[0].isnan().all() and bad[1].isnan().all()
+    finally:
+        LQ.set_wait_limit_ns(before)
+    again = call()
+    LQ.fault_check()
+    assert torch.equal(good[0], again[0]) and torch.equal(good[1], again[1])
