@@ -127,9 +127,10 @@ constexpr int kDirectTilesM = 3, kDirectTilesCoded = 4, kManyRows = 2048;
 constexpr int kFineTokens = 512;
 
 // Tokens that a stream of the kernel with rows as M adds into one O before that moves to a sum in the workspace.  Values of
-// one sign (1 + N(0, 0.1)) are off by, and 2000 queries, 16 heads, 32768 tokens take: 512 tokens 2.1e-6, 841 us; 1024 3.8e-6,
-// 754; 2048 7.9e-6, 709; 4096 1.9e-5, 690; never 2.2e-4, 668.  P's two parts may be off by 7.6e-6 themselves.
-constexpr int kRunTokens = 2048;
+// one sign (1 + N(0, 0.1)) are off by, and 2000 queries, 16 heads, 32768 tokens take: 1024 tokens
+// 3.8e-6, 689 us; 2048 7.9e-6, 656; 4096 1.9e-5, 639; never 2.2e-4, 620.  200 queries, whose CTAs have 3700 tokens: 1024
+// 3.0e-6, 99.1 us; 2048 6.5e-6, 96.1; 4096 and never 1.55e-5, 90.2.
+constexpr int kRunTokens = 4096;
 
 // Splits: a CTA owns an SM (its tiles fill shared memory), so the splits that fill whole waves of 148 CTAs are
 // compared by waves x (tiles per split + set-up), the set-up and drain of a CTA counted as two tiles.

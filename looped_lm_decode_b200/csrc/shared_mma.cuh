@@ -20,8 +20,8 @@
 // and values are exact.
 //
 // The tensor cores cut their fp32 sums toward zero at every product, so values of one sign come out low by as much as there
-// are products: 256 tiles in a row (2000 query rows, 32768 tokens) 2.2e-4.  Every 2048 tokens (256 products: 6e-6) a
-// stream therefore adds its O to a sum in the workspace and starts afresh: 8e-6 there, for 709 us instead of 668.
+// are products: 256 tiles in a row (2000 query rows, 32768 tokens) 2.2e-4.  Every 4096 tokens a stream therefore adds its O
+// to a sum in the workspace and starts afresh (RUNS): 1.9e-5 there, in 639 us instead of 620.
 //
 // P overwrites S in place, 16 score columns becoming 8 + 8 columns of packed pairs (one product's tokens; a third part
 // has columns of its own).  The running maximum moves only when a tile passes it by 2^8 (any reference is exact; it
@@ -214,13 +214,23 @@ struct RowSoftmax {
     }
 
     // O at `to` is added to the sum of the runs before (more) at `sum`, in fp32 rounded to nearest; the next product starts
-    // O afresh.
+    // O afresh.  Where the maximum has not moved since (carry 1 in the whole warp) the memory does the addition and nothing
+    // waits for it: an element has one thread, so the order is fixed.
     __device__ __forceinline__ void end_run(uint32_t to, float4 *sum, bool more) {
+        const bool moved = __any_sync(0xffffffffu, carry != 1.f);
 #pragma unroll 1
         for (int k0 = 0; k0 < D; k0 += 32) {
             uint32_t o[32];
             tc::tmem_ld32(to + k0, o);
             tc::tmem_wait_ld(o);
+            if (more && !moved) {
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    asm volatile("red.relaxed.gpu.global.add.v4.f32 [%0], {%1, %2, %3, %4};" ::"l"(sum + (k0 / 4 + k) * 128),
+                                 "f"(__uint_as_float(o[4 * k])), "f"(__uint_as_float(o[4 * k + 1])),
+                                 "f"(__uint_as_float(o[4 * k + 2])), "f"(__uint_as_float(o[4 * k + 3])) : "memory");
+                continue;
+            }
             if (more) add_runs(o, sum, k0);
 #pragma unroll
             for (int k = 0; k < 8; ++k)
@@ -232,7 +242,7 @@ struct RowSoftmax {
     __device__ __forceinline__ void add_runs(uint32_t (&o)[32], const float4 *sum, int k0) const {
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
-            const float4 y = sum[(k0 / 4 + k) * 128];
+            const float4 y = __ldcg(sum + (k0 / 4 + k) * 128);           // (the additions are made in L2)
             o[4 * k] = __float_as_uint(fmaf(y.x, carry, __uint_as_float(o[4 * k])));
             o[4 * k + 1] = __float_as_uint(fmaf(y.y, carry, __uint_as_float(o[4 * k + 1])));
             o[4 * k + 2] = __float_as_uint(fmaf(y.z, carry, __uint_as_float(o[4 * k + 2])));

@@ -30,13 +30,13 @@ def off(out, v):
 @pytest.mark.parametrize("n,rows,hkv,hq,d", [(32768, 2048, 16, 16, 128), (32768, 200, 16, 16, 128), (30001, 600, 40, 40, 64),
                                              (70001, 40, 40, 40, 64), (131072, 64, 4, 16, 128)])
 def test_rows_as_m_do_not_drift_over_long_prefixes(n, rows, hkv, hq, d):
-    """At most 2048 tokens, 128 products of weights with a remainder of 0, in a run; then sums of at most 64 runs and some
-    twenty roundings of the merge and the division."""
+    """At most 4096 tokens, 256 products of weights with a remainder of 0, in a run; then sums of at most 32 runs and some
+    twenty roundings of the merge and the division.  (Without runs 2048 products in the largest cases.)"""
     g = gen(n + rows)
     k, v = bf16(g, 1, hkv, n, d), positive(g, 1, hkv, n, d)
     out, lse = LQ.bf16_shared_attn(LQ.Bf16Cache(k, v, hq), 0, torch.zeros(rows, hq, d, dtype=torch.bfloat16, device="cuda"), i32([n]), n)
     LQ.fault_check()
-    assert off(out, v[0]) <= 128 / 2 * CUT + (64 + 20) * 2.0 ** -24
+    assert off(out, v[0]) <= 256 / 2 * CUT + (32 + 20) * 2.0 ** -24
     assert (lse - math.log(n)).abs().max().item() <= 2.0 ** -23 * math.log(n) + 1e-5
 
 
