@@ -195,7 +195,8 @@ size_t loopvq_bf16_decode_workspace_bytes(const loopvq_bf16_cache *cache, int ma
  *           clamped as in loopvq_decode_attn_range.  max_len <= Nmax is a host
  *           upper bound of the lengths.
  * scale     <= 0 selects 1/sqrt(D).
- * out, lse, workspace as for loopvq_decode_attn.
+ * out, lse, workspace as for loopvq_decode_attn.  A score of -inf weighs nothing; a
+ *           row of no others gives zeros and -inf.
  */
 loopvq_status loopvq_bf16_decode_attn(const loopvq_bf16_cache *cache, const uint16_t *q,
                                       const int32_t *starts, const int32_t *lens, int max_len,
@@ -251,7 +252,8 @@ size_t loopvq_shared_workspace_bytes(const loopvq_cache *cache, int rows, int ma
  *            other_out itself; otherwise out, lse and the workspace overlap neither
  *            an input nor one another (refused).
  * out        fp32 [rows][Hq][D]; lse fp32 [rows][Hq], may be NULL.  No tokens at
- *            all: zeros and -inf.
+ *            all: zeros and -inf.  A score of -inf (of an infinite key, or of products
+ *            past fp32's range) weighs nothing; a row of no others has no tokens.
  * workspace  of at least loopvq_bf16_shared_workspace_bytes(cache, rows, max_len)
  *            bytes, 16-byte aligned, ordered like any workspace.
  * B * Hkv * Nmax counts rows of the cache; Hkv * Nmax < 2^31.  Waits inside the
@@ -296,6 +298,7 @@ size_t loopvq_bf16_scored_workspace_bytes(const loopvq_bf16_cache *cache, int ma
  *            both NULL; a row with other_lse = -inf has no other tokens.  out may
  *            be other_out itself; otherwise outputs and workspace overlap neither an
  *            input nor one another (refused).
+ *            Scores <q, k> of -inf weigh nothing, as in loopvq_bf16_shared_attn.
  * score_in   fp32 [B][Hkv][Nmax], or NULL for zeros.
  * score_out  fp32 [B][Hkv][Nmax]: score_in itself, or memory apart from it;
  *            elements of other tokens stay as they are.

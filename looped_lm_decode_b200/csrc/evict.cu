@@ -18,7 +18,7 @@
 // the atomics' order does not matter.  Keys are read once and stay in registers; a long row is shared out over a cluster
 // of up to 8 CTAs, which send one another their counts and lists.
 //
-// What bounds it: a step's eviction (32 sequences x 16 heads, 2049 slots to 2048: 8.9 us, 17 MB read and written) is a
+// What bounds it: a step's eviction (32 sequences x 16 heads, 2049 slots to 2048: 9.0 us, 17 MB read and written) is a
 // chain of latencies, 12000 clocks: loads 3500, histogram 1000, digit 1000, list 2500, marks 2800 (clocks that
 // several CTAs of an SM share).  A long one (2 x 16 heads, 32768 slots to 4096: 41 us) selects in 20 us, of which the
 // cluster's slowest loads are half (its CTAs wait for one another), and reads and writes 117 MB of rows of 256 bytes in 20.

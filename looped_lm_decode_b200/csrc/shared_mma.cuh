@@ -28,9 +28,9 @@
 // bounds P), so O is rarely rescaled.
 //
 // What bounds it: over a bf16 prefix the products and, with few tiles a CTA, its set-up and exchange (16347 tokens, 64
-// queries, 4 KV / 16 query heads: 26 us with the merge, tensor pipe busy 35% of 23); over a coded one the shared-memory
-// pipe, which gathers, tile stores and the products' operands share (32768 tokens, 32 queries, 16 heads: 76 us, the pipe
-// busy 74% of it).
+// queries, 4 KV / 16 query heads: 26 us with the merge, tensor pipe busy 33% of 24); over a coded one the shared-memory
+// pipe, which gathers, tile stores and the products' operands share (32768 tokens, 32 queries, 16 heads: 77 us, the pipe
+// busy 73% of it).
 #pragma once
 
 #include "shared_rows.cuh"
