@@ -239,7 +239,7 @@ __global__ void __launch_bounds__(WARPS * 32, MINB) bf16_split_kernel(const Bf16
         if (mx == -FLT_MAX && !(lsum > 0.f)) {             // no score but -inf (or NaN, which the maximum passes over)
             mx = -CUDART_INF_F;
             acc = 0.f;
-            if (!SCORED || lsum == 0.f) lsum = 0.f;        // the scored merge makes the row NaN
+            if constexpr (!SCORED) lsum = 0.f;             // of NaN the scored merge makes a row of NaN
         }
         const size_t bh = (size_t)b * a.Hq + h * QPK + hq;
         a.ws_o[(bh * a.nsplit + split) * D + d] = acc;

@@ -322,7 +322,7 @@ __global__ void __launch_bounds__(RowsPlan<D, NR, C, PG>::kThreads, 1)
     // the next item with tiles; false behind the last
     auto advance = [&](Item &x) {
         const long long left = x.left - x.ntiles;
-        if (coded || DIRECT || left <= 0) return false;
+        if (DIRECT || left <= 0) return false;
         int b = x.b, h = x.h;
         do {
             if (++b == a.seqs) {

@@ -3,6 +3,10 @@
 Argument marshalling only: torch provides device memory and streams, and
 every step of the path runs in the library's CUDA kernels.  Loading fails
 loudly if the library has not been built; there is no fallback.
+
+stream: the torch stream that a call runs on (None: the current one).  What a
+call makes itself is made there; the caller sees to it that inputs are ready on
+that stream, and waits for it before reading results on another.
 """
 from __future__ import annotations
 
@@ -160,12 +164,12 @@ def _check(status):
 
 def fault_check(stream=None):
     """loopvq_fault_check: synchronise the stream, then raise LoopVQError if a kernel on this GPU recorded a
-    fault (an encode wait that ran out, a window roll without room) since the last check."""
+    fault (an encode or attention wait that ran out, a window roll without room) since the last check."""
     _check(lib().loopvq_fault_check(_stream(stream)))
 
 
 def set_wait_limit_ns(ns: int):
-    """loopvq_set_wait_limit_ns: bound on each wait of the tensor-core encoder (process-wide)."""
+    """loopvq_set_wait_limit_ns: bound on each wait of the tensor-core kernels (process-wide)."""
     lib().loopvq_set_wait_limit_ns(int(ns))
 
 
