@@ -250,7 +250,7 @@ def spots(which, n):
 def test_prefix_scores_of_minus_infinity_weigh_nothing(rows, hkv, hq, n, which, kind):
     """At the first tokens above all, which give some kernels their reference: the other tokens are not lost."""
     if kind == "lowest" and which == "all":
-        pytest.skip("below")
+        pytest.skip("rounding decides among scores of -1e37: test_prefix_scores_far_from_zero")
     g, d = gen(rows + n), 128
     k, v, _ = masked_case(g, 1, hkv, hq, n, d, spots(which, n), kind)
     q = bf16(g, rows, hq, d)
